@@ -494,3 +494,8 @@ class LSTM:
         if stream is None:
             stream = torch.cuda.current_stream(self._ws.device).cuda_stream
         return lstm_device_status(self._ws.data_ptr(), self._ws.numel(), stream)
+
+
+# operators beside the recurrent layers (include/lstm_ops.h)
+from .ops import (adamw_states, adamw_step, layer_norm, layer_norm_backward, linear_attention,  # noqa: E402,F401
+                  linear_attention_backward, linear_attention_step)

@@ -14,7 +14,7 @@ ARCH = "gfx950"
 
 SOURCES = ["lstm_api.cpp", "kernels.hip", "rec_f32.hip", "rec_bf16.hip", "rec_bf16_wide.hip", "backward.hip",
            "pack.hip", "noalloc.hip", "rec_wave.hip", "rec_xcd.hip",
-           "rec_res.hip"]
+           "rec_res.hip", "ops_api.cpp", "linear_attention.hip", "layer_norm.hip", "adamw.hip"]
 # Packed-fp32 VALU ops stay off: the device code uses plain fp32 arithmetic.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # Per-source flags.  rec_res.hip keeps W_hh (up to 256 registers a wave) beside

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/lstm.h"
+#include "host.h"
 #include "kernels.h"
 #include "pack.h"
 
@@ -554,17 +555,6 @@ void span_end(lstm_plan *p, int idx, hipStream_t st, int launches) {
     if (idx < 0) return;
     p->spans[idx].launches = launches;
     if (hipEventRecord(p->spans[idx].b, st) != hipSuccess) (void)hipGetLastError();
-}
-
-bool is_device_ptr(const void *ptr, int dev) {
-    hipPointerAttribute_t attr;
-    std::memset(&attr, 0, sizeof(attr));
-    if (hipPointerGetAttributes(&attr, ptr) != hipSuccess) {
-        (void)hipGetLastError();
-        return false;
-    }
-    const bool dev_mem = attr.type == hipMemoryTypeDevice || attr.type == hipMemoryTypeManaged;
-    return dev_mem && attr.device == dev;
 }
 
 int validate(const lstm_plan *p, const void *x, const void *h0, const float *c0,

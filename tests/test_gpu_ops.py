@@ -1,0 +1,587 @@
+"""The operators of include/lstm_ops.h on the GPU against the fp64 oracle.
+
+Tolerances are bounds on rounding, element by element: the oracle run on
+magnitudes gives the sum A of the absolute values of the terms of an output;
+fp32 arithmetic loses at most (roundings in a chain) * 2^-24 of A, and a bf16
+operand or result 2^-8 of A each time a value is rounded to bf16.
+"""
+import numpy as np
+import pytest
+
+import layer_lstm_forward_amd as pkg
+from layer_lstm_forward_amd import ops
+from layer_lstm_forward_amd.synth import bf16_bits_to_f32, f32_to_bf16_bits
+from oracle import ops as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+U32, U16 = 2.0 ** -24, 2.0 ** -8  # half a unit in the last place, relative: 24 and 8 significant bits
+
+
+def draw(rng, shape, dtype, std=1.0):
+    """fp32 values that are exact in the dtype."""
+    x = rng.normal(0.0, std, size=shape).astype(np.float32)
+    return bf16_bits_to_f32(f32_to_bf16_bits(x)) if dtype == "bf16" else x
+
+
+def dev(x, dtype="f32"):
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+    return t.to(torch.bfloat16) if dtype == "bf16" else t
+
+
+def host(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def close(got, want, tol, what):
+    got = host(got)
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    bad = np.abs(got - want) > tol
+    worst = np.max(np.abs(got - want) / np.maximum(tol, 1e-300)) if got.size else 0.0
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.size} outside, worst {worst:.3g} x tolerance"
+
+
+# ---------------------------------------------------------- linear attention
+def la_tol(A, dtype, T, Dk, Dv, g, out16):
+    """A: the outputs' sum of magnitudes.  fp32: both products' sums (Dk or Dv and at most T terms), the weights
+    (the exponent T |g| log2 e, rounded, moves its power by as much; only weights above 2^-24 count, so at most 24
+    of it do) and the state's own roundings; bf16: the weighted products or the carried matrix are rounded once, the
+    result once more."""
+    chain = Dk + Dv + T + 2 * min(24.0, T * float(np.max(np.abs(np.where(np.isfinite(g), g, 0.0))))) * 2 + 64
+    tol = chain * U32 * A
+    if dtype == "bf16":
+        tol = tol + (2 * U16 * A if out16 else U16 * U16 * 2 * A)
+    return tol + 1e-30
+
+
+class La:
+    """Inputs of a case; host copies are exact in the dtype, [B, T, heads, dim]."""
+
+    def __init__(self, T, B, H, G, Dk, Dv, dtype, decays=None, state=True, lengths=None, batch_first=False,
+                 packed=False, seed=0, scale=None):
+        rng = np.random.default_rng(seed + 17 * T + Dk)
+        self.__dict__.update(T=T, B=B, H=H, G=G, Dk=Dk, Dv=Dv, dtype=dtype, batch_first=batch_first)
+        self.q, self.k = draw(rng, (B, T, H, Dk), dtype), draw(rng, (B, T, G, Dk), dtype, Dk ** -0.5)
+        self.v, self.do = draw(rng, (B, T, G, Dv), dtype), draw(rng, (B, T, H, Dv), dtype)
+        self.S = draw(rng, (B, H, Dk, Dv), "f32") if state else None
+        self.dS = draw(rng, (B, H, Dk, Dv), "f32") if state else None
+        self.g = (np.asarray(decays, np.float32) if decays is not None
+                  else np.log1p(-np.exp2(-rng.uniform(1, 9, H))).astype(np.float32))
+        self.lengths = lengths
+        self.scale = Dk ** -0.5 if scale is None else scale
+        x = {n: getattr(self, n) for n in ("q", "k", "v", "do")}
+        if lengths is not None:  # what is past a row's end must not be read
+            for n in x:
+                x[n] = x[n].copy()
+                for b, m in enumerate(lengths):
+                    x[n][b, m:] = np.nan
+        if not batch_first:
+            x = {n: np.swapaxes(a, 0, 1) for n, a in x.items()}
+        if packed:
+            wide = dev(np.concatenate([x[n].reshape(*x[n].shape[:2], -1) for n in ("q", "k", "v")], -1), dtype)
+            a, b = H * Dk, H * Dk + G * Dk
+            self.tq, self.tk, self.tv = (wide[..., :a].unflatten(-1, (H, Dk)), wide[..., a:b].unflatten(-1, (G, Dk)),
+                                         wide[..., b:].unflatten(-1, (G, Dv)))
+        else:
+            self.tq, self.tk, self.tv = (dev(x[n], dtype) for n in ("q", "k", "v"))
+        self.tdo = dev(x["do"], dtype)
+        self.tg = dev(self.g)
+        self.tS, self.tdS = (None if a is None else dev(a) for a in (self.S, self.dS))
+
+    def seq(self, a):
+        return a if self.batch_first else np.swapaxes(a, 0, 1)
+
+    def forward(self, **kw):
+        return pkg.linear_attention(self.tq, self.tk, self.tv, self.tg, scale=self.scale, state=self.tS,
+                                    lengths=self.lengths, batch_first=self.batch_first, **kw)
+
+    def backward(self, **kw):
+        return pkg.linear_attention_backward(self.tq, self.tk, self.tv, self.tg, self.tdo, scale=self.scale,
+                                             state=self.tS, dstate=self.tdS, lengths=self.lengths,
+                                             batch_first=self.batch_first, **kw)
+
+    def check_forward(self, got):
+        args = (self.q, self.k, self.v, self.g, self.scale, self.S, self.lengths)
+        mag = [None if a is None else np.abs(a) for a in (self.q, self.k, self.v, self.S)]
+        want = ref.linear_attention(*args)
+        A = ref.linear_attention(mag[0], mag[1], mag[2], self.g, abs(self.scale), mag[3], self.lengths)
+        for x, w, a, n, out16 in ((got[0], self.seq(want[0]), self.seq(A[0]), "o", True),
+                                  (got[1], want[1], A[1], "state", False)):
+            close(x, w, la_tol(a, self.dtype, self.T, self.Dk, self.Dv, self.g, out16), n)
+
+    def check_backward(self, got):
+        f = ref.linear_attention_backward
+        m = [None if a is None else np.abs(a) for a in (self.q, self.k, self.v, self.do, self.S, self.dS)]
+        want = f(self.q, self.k, self.v, self.g, self.scale, self.do, self.S, self.dS, self.lengths)
+        A = f(m[0], m[1], m[2], self.g, abs(self.scale), m[3], m[4], m[5], self.lengths)
+        for x, w, a, n in zip(got[:3], want[:3], A[:3], ("dq", "dk", "dv")):
+            close(x, self.seq(w), la_tol(self.seq(a), self.dtype, self.T, self.Dk, self.Dv, self.g, True), n)
+        if self.S is not None:
+            close(got[3], want[3], la_tol(A[3], self.dtype, self.T, self.Dk, self.Dv, self.g, False), "dstate")
+        else:
+            assert got[3] is None
+
+
+INF = float("inf")
+LA_CASES = {
+    # one token; one token of a one-wide head; the edges of a chunk; odd widths; the widest heads
+    "one": dict(T=1, B=2, H=2, G=1, Dk=16, Dv=16),
+    "one-wide": dict(T=7, B=1, H=1, G=1, Dk=1, Dv=1),
+    "t31": dict(T=31, B=2, H=2, G=2, Dk=64, Dv=64, state=False),
+    "t63": dict(T=63, B=1, H=2, G=2, Dk=64, Dv=64),
+    "t64": dict(T=64, B=1, H=2, G=2, Dk=128, Dv=64),
+    "t65": dict(T=65, B=1, H=2, G=2, Dk=32, Dv=128, state=False),
+    "t129": dict(T=129, B=2, H=4, G=2, Dk=128, Dv=128, batch_first=True, packed=True),
+    "odd": dict(T=77, B=3, H=6, G=3, Dk=72, Dv=104, packed=True),
+    "odder": dict(T=50, B=2, H=3, G=1, Dk=17, Dv=33, packed=True, batch_first=True),
+    "narrow": dict(T=90, B=2, H=2, G=2, Dk=5, Dv=200),
+    "wide": dict(T=70, B=1, H=1, G=1, Dk=256, Dv=256),
+    "wide-odd": dict(T=40, B=1, H=2, G=1, Dk=131, Dv=250, packed=True),
+    # rows of no, one, a chunk's and all tokens
+    "ragged": dict(T=130, B=6, H=2, G=1, Dk=64, Dv=48, lengths=[0, 1, 64, 65, 129, 130]),
+    "ragged-first": dict(T=40, B=3, H=2, G=2, Dk=40, Dv=64, lengths=[40, 0, 3], batch_first=True, packed=True,
+                         state=False),
+    # gamma of 0, 1, and so small that a chunk's powers leave the fp32 range
+    "decays": dict(T=100, B=1, H=4, G=4, Dk=32, Dv=32, decays=[-INF, 0.0, -5.0, -40.0]),
+    # few rows and many tokens: the sequence is cut into segments
+    "long": dict(T=1500, B=1, H=2, G=1, Dk=64, Dv=64, decays=[-0.001, -0.02]),
+    "long-ragged": dict(T=1100, B=3, H=1, G=1, Dk=48, Dv=80, lengths=[1100, 0, 517], packed=True),
+    "negative-scale": dict(T=20, B=1, H=1, G=1, Dk=16, Dv=16, scale=-0.3),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", LA_CASES)
+def test_linear_attention(name, dtype):
+    c = La(dtype=dtype, **LA_CASES[name])
+    print(f"case {name} {dtype} forward", flush=True)
+    first = c.forward()
+    c.check_forward(first)
+    print(f"case {name} {dtype} backward", flush=True)
+    grads = c.backward()
+    c.check_backward(grads)
+    # the same bits again: nothing depends on the order in which workgroups run
+    for a, b in zip(first + grads, c.forward() + c.backward()):
+        assert a is None or bool((a == b).all())
+
+
+def test_linear_attention_state_in_place_and_out():
+    import torch
+    c = La(T=70, B=2, H=2, G=2, Dk=64, Dv=64, dtype="bf16")
+    o, last = c.forward()
+    wide = torch.full((70, 2, 2, 100), 7.0, dtype=torch.bfloat16, device=DEV)
+    state = c.tS.clone()
+    c.tS = state
+    r = c.forward(out=(wide[..., 20:84], state))
+    assert r[1] is state and torch.equal(state, last) and torch.equal(wide[..., 20:84], o)
+    assert bool((wide[..., :20] == 7).all()) and bool((wide[..., 84:] == 7).all())
+    # two calls on parts of the sequence are one call on the whole
+    c = La(T=70, B=2, H=2, G=2, Dk=64, Dv=64, dtype="f32")
+    o, last = c.forward()
+    a, mid = pkg.linear_attention(c.tq[:33], c.tk[:33], c.tv[:33], c.tg, scale=c.scale, state=c.tS)
+    b, end = pkg.linear_attention(c.tq[33:], c.tk[33:], c.tv[33:], c.tg, scale=c.scale, state=mid)
+    c.check_forward((torch.cat([a, b]), end))
+
+
+def test_linear_attention_strides():
+    """Head-major inputs, a broadcast key, and odd element offsets."""
+    import torch
+    c = La(T=45, B=2, H=2, G=2, Dk=32, Dv=40, dtype="bf16")
+    head_major = c.tv.permute(2, 1, 0, 3).contiguous().permute(2, 1, 0, 3)
+    odd = torch.empty(c.tq.numel() + 3, dtype=torch.bfloat16, device=DEV)[3:].view(c.tq.shape)
+    odd.copy_(c.tq)
+    want = c.forward()
+    c.tq, c.tv = odd, head_major
+    for a, b in zip(want, c.forward()):
+        assert torch.equal(a, b)
+    one = c.tk[:, :1, :1].expand(c.tk.shape)
+    full = one.contiguous()
+    for a, b in zip(pkg.linear_attention(c.tq, one, c.tv, c.tg), pkg.linear_attention(c.tq, full, c.tv, c.tg)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,G,Dk,Dv", [(1, 1, 1, 1, 1), (1, 8, 8, 128, 128), (5, 4, 2, 72, 104), (3, 2, 1, 17, 33),
+                                         (40, 2, 2, 64, 64), (2, 1, 1, 256, 256), (300, 1, 1, 16, 8),
+                                         (2, 3, 3, 5, 130)])
+def test_linear_attention_step(dtype, B, H, G, Dk, Dv):
+    import torch
+    rng = np.random.default_rng(B + Dk)
+    q, k = draw(rng, (B, 1, H, Dk), dtype), draw(rng, (B, 1, G, Dk), dtype)
+    v, g = draw(rng, (B, 1, G, Dv), dtype), -rng.uniform(0, 2, H).astype(np.float32)
+    n = B + 2
+    slots = rng.permutation(n)[:B].astype(np.int32)
+    slots[B // 2] = -1 if B > 2 else slots[B // 2]
+    if B > 4:
+        slots[1] = n  # idle too
+    pool = draw(rng, (n, H, Dk, Dv), "f32")
+    busy = (slots >= 0) & (slots < n)
+    at = np.where(busy, slots, 0)
+    wo, ws = ref.linear_attention(q, k, v, g, Dk ** -0.5, pool[at])
+    Ao, As = ref.linear_attention(np.abs(q), np.abs(k), np.abs(v), g, Dk ** -0.5, np.abs(pool[at]))
+    wide = dev(np.concatenate([x[:, 0].reshape(B, -1) for x in (q, k, v)], -1), dtype)
+    cut = [H * Dk, H * Dk + G * Dk]
+    tq, tk = wide[:, :cut[0]].unflatten(-1, (H, Dk)), wide[:, cut[0]:cut[1]].unflatten(-1, (G, Dk))
+    tp = dev(pool)
+    o = pkg.linear_attention_step(tq, tk, wide[:, cut[1]:].unflatten(-1, (G, Dv)), dev(g), tp, slots=dev(slots))
+    # the state is one product and one sum away from its terms, o a sum over Dk more
+    tol_s = 4 * U32 * As + 1e-30
+    tol_o = (Dk + 8) * U32 * Ao + (U16 * np.abs(wo) if dtype == "bf16" else 0) + 1e-30
+    want = pool.astype(np.float64).copy()
+    tol = np.zeros(want.shape) + 0.0
+    want[slots[busy]], tol[slots[busy]] = ws[busy], tol_s[busy]
+    close(tp, want, tol, "pool")
+    wo, tol_o = np.where(busy[:, None, None, None], wo, 0.0)[:, 0], tol_o[:, 0]
+    close(o, wo, tol_o, "o")
+    if B <= 5:  # without slots: row b is state b
+        tp2 = dev(pool[:B])
+        o2 = pkg.linear_attention_step(dev(q[:, 0], dtype), dev(k[:, 0], dtype), dev(v[:, 0], dtype), dev(g), tp2)
+        wo2, ws2 = ref.linear_attention(q, k, v, g, Dk ** -0.5, pool[:B])
+        A2 = ref.linear_attention(np.abs(q), np.abs(k), np.abs(v), g, Dk ** -0.5, np.abs(pool[:B]))
+        close(tp2, ws2, 4 * U32 * A2[1] + 1e-30, "state")
+        close(o2, wo2[:, 0], (Dk + 8) * U32 * A2[0][:, 0] + (U16 * np.abs(wo2[:, 0]) if dtype == "bf16" else 0)
+              + 1e-30, "o without slots")
+    assert torch.isfinite(tp).all()
+
+
+def test_steps_follow_a_prompt():
+    c = La(T=37, B=3, H=2, G=1, Dk=24, Dv=40, dtype="f32")
+    import torch
+    o, state = pkg.linear_attention(c.tq[:20], c.tk[:20], c.tv[:20], c.tg, scale=c.scale, state=c.tS)
+    rest = [pkg.linear_attention_step(c.tq[t], c.tk[t], c.tv[t], c.tg, state, scale=c.scale) for t in range(20, 37)]
+    c.check_forward((torch.cat([o, torch.stack(rest)]), state))
+
+
+# ----------------------------------------------------------------- layer norm
+def ln_tol(z, w, unit, rstd, dtype):
+    """Of the normalised values times w: the mean's and the variance's sums run in chains of at most width / 64 + 16
+    additions, and the difference z - mean keeps |z| + |mean| in units of its own size."""
+    n = z.shape[1]
+    k = (n / 64 + 40) * U32
+    spread = (np.abs(z).max(1) + np.abs(z).mean(1)) * rstd + 1
+    return k * (np.abs(unit) + 1) * spread[:, None] * np.abs(w), k * spread
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,width,residual,affine", [
+    (1, 1, False, True), (3, 2, True, True), (4, 1024, True, True), (5, 7, False, False), (17, 63, True, True),
+    (2, 64, False, True), (33, 65, True, False), (9, 511, False, True), (6, 1001, True, True), (3, 4096, True, True),
+    (2, 5000, False, True), (2, 8192, True, True), (1, 20011, True, True), (300, 256, False, True),
+    (1030, 130, True, True)])
+def test_layer_norm(dtype, rows, width, residual, affine):
+    rng = np.random.default_rng(rows * 31 + width)
+    x = draw(rng, (rows, width), dtype) * np.float32(2.0)
+    x[0] = 3.0  # a constant row: variance 0
+    res = draw(rng, (rows, width), dtype) if residual else None
+    w = draw(rng, (width,), dtype) if affine else None
+    b = draw(rng, (width,), dtype) if affine else None
+    dy, ds = draw(rng, (rows, width), dtype), draw(rng, (rows, width), dtype) if residual else None
+    z = x if res is None else (bf16_bits_to_f32(f32_to_bf16_bits(x + res)) if dtype == "bf16" else x + res)
+    t = lambda a: None if a is None else dev(a, dtype)  # noqa: E731
+    print(f"case norm {rows}x{width} {dtype}", flush=True)
+    y, mean, rstd, total = pkg.layer_norm(t(x), t(w), t(b), residual=t(res))
+    assert np.array_equal(host(total), z)
+    z = z.astype(np.float64)
+    wy, wm, wr = ref.layer_norm(z, w, b)
+    ww, wb = (np.ones(width), np.zeros(width)) if w is None else (w.astype(np.float64), b.astype(np.float64))
+    unit = (z - wm[:, None]) * wr[:, None]
+    tol, rel = ln_tol(z, ww, unit, wr, dtype)
+    half = U16 if dtype == "bf16" else 2 * U32
+    close(y, wy, tol + half * np.abs(wy) + 4 * U32 * np.abs(wb) + half * 1e-30, "y")
+    close(mean, wm, (width / 64 + 16) * U32 * np.abs(z).mean(1) + 1e-30, "mean")
+    close(rstd, wr, rel * wr, "rstd")
+    dz, dw, db = pkg.layer_norm_backward(t(dy), total, mean, rstd, t(w), dsum=t(ds))
+    wz, wdw, wdb = ref.layer_norm_backward(dy, z, w, dsum=ds)
+    g = np.abs(dy * ww)
+    A = wr[:, None] * (g + g.mean(1, keepdims=True) + (np.abs(unit) + 1) * (g * (np.abs(unit) + 1)).mean(1, keepdims=True))
+    extra = 0 if ds is None else 4 * U32 * np.abs(ds)
+    close(dz, wz, 4 * rel[:, None] * A + extra + half * np.abs(wz), "dz")
+    close(dw, wdw, (np.abs(dy) * (np.abs(unit) + 1) * (2 * rel + rows * U32)[:, None]).sum(0) + half * np.abs(wdw),
+          "dweight")
+    close(db, wdb, (rows + 4) * U32 * np.abs(dy).sum(0) + half * np.abs(wdb), "dbias")
+    for p, r in zip((dz, dw, db), pkg.layer_norm_backward(t(dy), total, mean, rstd, t(w), dsum=t(ds))):
+        assert bool((p == r).all())
+
+
+def test_layer_norm_rows_apart_and_none():
+    import torch
+    rng = np.random.default_rng(5)
+    wide = dev(draw(rng, (12, 100), "bf16"), "bf16")
+    part = wide[:, 3:67]  # rows 100 apart, at an odd offset
+    y, mean, rstd, z = pkg.layer_norm(part)
+    y2, *_ = pkg.layer_norm(part.contiguous())
+    assert z is part and torch.equal(y, y2)
+    a = pkg.layer_norm_backward(part, part, mean, rstd)
+    b = pkg.layer_norm_backward(part.contiguous(), part.contiguous(), mean, rstd)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    y, mean, rstd, z = pkg.layer_norm(torch.empty(0, 64, device=DEV))
+    assert y.shape == (0, 64)
+    dz, dw, db = pkg.layer_norm_backward(y, z, mean, rstd)
+    assert dz.shape == (0, 64) and not dw.any() and not db.any()
+    # a row that is not finite stays alone
+    x = dev(draw(rng, (5, 200), "f32"))
+    want = pkg.layer_norm(x)[0]
+    x[2, 7] = float("nan")
+    x[3, 9] = float("inf")
+    got = pkg.layer_norm(x)[0]
+    keep = [0, 1, 4]
+    assert torch.equal(got[keep], want[keep]) and bool(got[2].isnan().all()) and bool(got[3].isnan().any())
+    # a mean far from zero: the variance comes from the differences
+    z = (1000.0 + rng.normal(size=(4, 333))).astype(np.float32)
+    wy, _, wr = ref.layer_norm(z)
+    unit = wy
+    tol, _ = ln_tol(z.astype(np.float64), np.ones(333), unit, wr, "f32")
+    close(pkg.layer_norm(dev(z))[0], wy, tol + 2 * U32 * np.abs(wy), "y")
+
+
+# ---------------------------------------------------------------------- AdamW
+SIZES = [(1,), (255,), (256,), (257,), (40, 33), (3, 1000), (100003,)]
+
+
+def _adamw_inputs(rng, dtype):
+    p = [draw(rng, s, dtype) for s in SIZES]
+    g = [draw(rng, s, dtype, 1e-2) for s in SIZES]
+    g[2][:] = 0.0
+    return p, g
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("dtype,master", [("f32", False), ("bf16", False), ("bf16", True)])
+def test_adamw_32(dtype, master, offset):
+    """Three steps; offset: tensors that begin at an odd element."""
+    import torch
+    rng = np.random.default_rng(7)
+    p, g = _adamw_inputs(rng, dtype)
+
+    def put(a, dt):
+        t = torch.empty(a.size + offset, dtype=torch.bfloat16 if dt == "bf16" else torch.float32, device=DEV)[offset:]
+        t = t.view(a.shape)
+        t.copy_(dev(a, dt))
+        return t
+
+    tp, tg = [put(a, dtype) for a in p], [put(a, dtype) for a in g]
+    m, v, scales = pkg.adamw_states(tp)
+    masters = [put(a, "f32") for a in p] if master else None
+    lr, wd = [1e-2 * (i + 1) for i in range(len(p))], [0.1 * (i % 2) for i in range(len(p))]
+    gs = torch.full((1,), 0.5, device=DEV)
+    w = [a.astype(np.float64) for a in p]
+    wm, wv = ([np.zeros(a.shape) for a in p] for _ in range(2))
+    tol = [np.zeros(a.shape) for a in p]
+    for t in (1, 2, 3):
+        pkg.adamw_step(tp, tg, m, v, step=t, lr=lr, weight_decay=wd, masters=masters, grad_scale=gs)
+        for i in range(len(p)):
+            w[i], wm[i], wv[i] = ref.adamw(w[i], g[i] * 0.5, wm[i], wv[i], t, lr[i], 0.9, 0.999, 1e-8, wd[i])
+            # about 16 roundings a step; the betas as fp32 are 2^-24 off, which 1 - beta2 = 0.001 makes 1000 times
+            # as much only where it is formed in fp32 (it is not); sqrt halves what v is off by
+            step = np.abs(lr[i] * (wm[i] / (1 - 0.9 ** t)) / (np.sqrt(wv[i] / (1 - 0.999 ** t)) + 1e-8))
+            tol[i] = tol[i] + 16 * U32 * (np.abs(w[i]) + 4 * step)
+            if dtype == "bf16" and not master:
+                tol[i] = tol[i] + U16 * (np.abs(w[i]) + step)
+    for i in range(len(p)):
+        close(m[i], wm[i], 16 * U32 * np.abs(wm[i]), "m")
+        close(v[i], wv[i], 24 * U32 * np.abs(wv[i]), "v")
+        if master:
+            close(masters[i], w[i], tol[i], "master")
+            assert torch.equal(masters[i].to(torch.bfloat16), tp[i])
+        else:
+            close(tp[i], w[i], tol[i], "param")
+
+
+def test_adamw_many_tensors_and_none():
+    import torch
+    pkg.adamw_step([], [], [], [], step=1)
+    rng = np.random.default_rng(8)
+    p = [dev(draw(rng, (int(n),), "f32")) for n in rng.integers(0, 300, 150)]
+    g = [torch.ones_like(x) for x in p]
+    m, v, _ = pkg.adamw_states(p)
+    old = [x.clone() for x in p]
+    pkg.adamw_step(p, g, m, v, step=1, lr=0.5, weight_decay=0.0)
+    for a, b in zip(p, old):  # the first step of a constant gradient is lr
+        assert bool(((b - a) - 0.5).abs().max() < 1e-5) if a.numel() else True
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_adamw_8(dtype):
+    """Every stored state is one of the two codes beside the exact value, the parameters follow from the exact new
+    states, and the codes' mean over seeds is the value."""
+    import torch
+    rng = np.random.default_rng(9)
+    p, g = _adamw_inputs(rng, dtype)
+    p.append(draw(rng, (1000,), dtype))
+    g.append(draw(rng, (1000,), dtype) * np.float32(2.0) ** rng.integers(-16, 1, 1000).astype(np.float32))
+    values = ref.code_values()
+    tp, tg = [dev(a, dtype) for a in p], [dev(a, dtype) for a in g]
+    m, v, scales = pkg.adamw_states(tp, bits=8)
+    pkg.adamw_step(tp, tg, m, v, step=1, scales=scales, seed=1)
+    start = [[t.clone() for t in x] for x in (tp, m, v, scales[0], scales[1])]
+    spread = lambda s, n: np.repeat(host(s), 256)[:n]  # noqa: E731
+    sums = None
+    for seed in range(2, 34):
+        for x, y in zip((tp, m, v, scales[0], scales[1]), start):
+            for a, b in zip(x, y):
+                a.copy_(b)
+        pkg.adamw_step(tp, tg, m, v, step=2, lr=1e-2, scales=scales, seed=seed)
+        got = [(host(a).reshape(-1) * spread(s, a.numel()), host(b).reshape(-1) * spread(r, b.numel()))
+               for a, b, s, r in zip(m, v, *scales)]
+        sums = [(a + c, b + d) for (a, b), (c, d) in zip(got, sums)] if sums else got
+    for i, a in enumerate(p):
+        n = a.size
+        codes = [start[1][i], start[2][i]]
+        om = values[codes[0].view(torch.uint8).cpu().numpy().reshape(-1)] * spread(start[3][i], n)
+        orr = values[codes[1].view(torch.uint8).cpu().numpy().reshape(-1)] * spread(start[4][i], n)
+        wp, wm, wv = ref.adamw(host(start[0][i]).reshape(-1), g[i].reshape(-1), om, orr ** 2, 2, 1e-2, 0.9, 0.999,
+                               1e-8, 0.01)
+        step = np.abs(1e-2 * (wm / (1 - 0.9 ** 2)) / (np.sqrt(wv / (1 - 0.999 ** 2)) + 1e-8))
+        tol = 16 * U32 * (np.abs(wp) + 4 * step) + (U16 * (np.abs(wp)) if dtype == "bf16" else 0)
+        close(tp[i].view(-1), wp, tol, "param")
+        for j, (want, sc) in enumerate(((wm, scales[0][i]), (np.sqrt(wv), scales[1][i]))):
+            s = spread(sc, n)
+            blocks = np.array([np.abs(want[k:k + 256]).max() for k in range(0, n, 256)])
+            top = np.where(blocks > 0, np.floor(np.log2(np.maximum(blocks, 1e-300))), -1000)
+            assert np.array_equal(host(sc), np.exp2(np.maximum(top - 7, -126.0))), "scale"
+            # distance between the codes around the value
+            e = np.floor(np.log2(np.maximum(np.abs(want) / s, 2.0 ** -6)))
+            unit = np.exp2(e - 3) * s
+            off = np.abs(got[i][j] - want)
+            assert np.all(off <= unit * (1 + 1e-4)), f"state {j} of {i}: {np.max(off / unit)}"
+            # 32 draws: the mean's deviation is at most half a unit over sqrt(32), six of those at most; below the
+            # smallest code sqrt(v) is kept at it
+            small = (want > 0) & (want < 2.0 ** -9 * s) if j else np.zeros(n, bool)
+            mean = sums[i][j] / 32
+            assert np.all(np.abs(mean - want)[~small] <= (unit * (6 * 0.5 / 32 ** 0.5 + 1e-3))[~small])
+            if j:
+                assert np.all(got[i][j][want > 0] > 0), "a positive second moment is never stored as 0"
+
+
+def test_adamw_8_follows_32_bits():
+    """A least-squares problem: after 300 steps both have come equally far."""
+    import torch
+    rng = np.random.default_rng(10)
+    A, x0 = dev(draw(rng, (512, 256), "f32")), dev(draw(rng, (256,), "f32"))
+    b = A @ dev(draw(rng, (256,), "f32"))
+    loss = {}
+    for bits in (32, 8):
+        x = x0.clone()
+        m, v, s = pkg.adamw_states([x], bits=bits)
+        for t in range(1, 301):
+            grad = A.T @ (A @ x - b) / 512
+            pkg.adamw_step([x], [grad], m, v, step=t, lr=2e-2, weight_decay=0.0, scales=s, seed=t)
+        loss[bits] = float(((A @ x - b) ** 2).mean())
+    start = float(((A @ x0 - b) ** 2).mean())
+    assert loss[32] < 0.01 * start and loss[8] < 0.02 * start, (start, loss)
+    assert torch.isfinite(x).all()
+
+
+def test_adamw_not_finite_gradients_stay_alone():
+    import torch
+    rng = np.random.default_rng(11)
+    p, g = dev(draw(rng, (700,), "f32")), dev(draw(rng, (700,), "f32"))
+    out = []
+    for bad in (False, True):
+        x, y = p.clone(), g.clone()
+        if bad:
+            y[300], y[301] = float("nan"), float("inf")
+        m, v, s = pkg.adamw_states([x], bits=8)
+        pkg.adamw_step([x], [y], m, v, step=1, scales=s, seed=3)
+        out.append((x, m[0].float(), v[0].float()))
+    keep = torch.ones(700, dtype=torch.bool, device=DEV)
+    keep[300:302] = False
+    for a, b in zip(*out):
+        assert torch.equal(a[keep], b[keep])
+    assert out[1][1][300].isnan() and out[1][1][301].isnan()
+
+
+# ------------------------------------------------------- streams and graphs
+def _everything(c, x, p, g, m, v, pool, **kw):
+    o, last = c.forward(**kw)
+    grads = c.backward(**kw)
+    y, mean, rstd, z = pkg.layer_norm(x, residual=x, **kw)
+    dz, dw, db = pkg.layer_norm_backward(x, z, mean, rstd, **kw)
+    s = pkg.linear_attention_step(c.tq[0], c.tk[0], c.tv[0], c.tg, pool, **kw)
+    pkg.adamw_step([p], [g], [m], [v], step=1, **kw)
+    return [o, last, *grads, y, mean, rstd, dz, dw, db, s, pool, p, m, v]
+
+
+def _fresh():
+    import torch
+    c = La(T=600, B=1, H=2, G=1, Dk=64, Dv=64, dtype="bf16")
+    rng = np.random.default_rng(12)
+    x = dev(draw(rng, (300, 500), "bf16"), "bf16")
+    p, g = dev(draw(rng, (5000,), "f32")), dev(draw(rng, (5000,), "f32"))
+    return c, x, p, g, torch.zeros_like(p), torch.zeros_like(p), dev(draw(rng, (1, 2, 64, 64), "f32"))
+
+
+def test_another_stream():
+    import torch
+    want = _everything(*_fresh())
+    args = _fresh()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = _everything(*args, stream=side.cuda_stream)
+    side.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_graph_replays():
+    import torch
+    want = None
+    args = _fresh()
+    c, x, p, g, m, v, pool = args
+    keep = [t.clone() for t in (p, m, v, pool)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in _everything(*args)]
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _everything(*args)
+    for _ in range(4):
+        for t, k in zip((p, m, v, pool), keep):
+            t.copy_(k)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+        (torch.randn(1000, device=DEV) @ torch.randn(1000, device=DEV)).item()
+
+
+def test_wrapper_refusals():
+    import torch
+    c = La(T=4, B=2, H=2, G=1, Dk=8, Dv=8, dtype="f32")
+    bad = [dict(lengths=[5, 1]), dict(lengths=[1]), dict(lengths=[-1, 2]),
+           dict(lengths=torch.zeros(2, dtype=torch.int64, device=DEV)), dict(state=c.tS.to(torch.bfloat16)),
+           dict(state=c.tS[:1]), dict(scale=0.0)]
+    for kw in bad:
+        with pytest.raises((ValueError, pkg.LSTMError)):
+            pkg.linear_attention(c.tq, c.tk, c.tv, c.tg, **kw)
+    with pytest.raises(ValueError):
+        pkg.linear_attention(c.tq, c.tk.to(torch.bfloat16), c.tv, c.tg)
+    with pytest.raises(ValueError):
+        pkg.linear_attention(c.tq.transpose(-1, -2), c.tk, c.tv, c.tg)
+    with pytest.raises(ValueError):
+        pkg.linear_attention(c.tq, c.tk, c.tv, c.tg.double())
+    with pytest.raises(pkg.LSTMError):
+        pkg.linear_attention(c.tq[:, :, :1].expand(-1, -1, 3, -1), c.tk.expand(-1, -1, 2, -1),
+                             c.tv.expand(-1, -1, 2, -1), torch.zeros(3, device=DEV))
+    with pytest.raises(ValueError):
+        pkg.linear_attention_step(c.tq[0], c.tk[0], c.tv[0], c.tg, c.tS, slots=torch.zeros(2, device=DEV))
+    with pytest.raises(pkg.LSTMError):
+        pkg.linear_attention_step(c.tq[0], c.tk[0], c.tv[0], c.tg, c.tS[:1])
+    x = torch.zeros(3, 8, device=DEV)
+    with pytest.raises(ValueError):
+        pkg.layer_norm(x, torch.zeros(7, device=DEV))
+    with pytest.raises(ValueError):
+        pkg.layer_norm(x, residual=x[:2])
+    with pytest.raises(pkg.LSTMError):
+        pkg.layer_norm(x, eps=-1.0)
+    with pytest.raises(ValueError):
+        pkg.adamw_step([x], [x[:2]], [x], [x], step=1)
+    with pytest.raises(pkg.LSTMError):
+        pkg.adamw_step([x], [x], [x], [x], step=0)
+    assert ops.lstm_layer_norm_forward(0, x.cpu().data_ptr(), 8, 0, 8, 0, 0, 3, 8, 1e-5, x.data_ptr(), 0, 0, 0,
+                                       0) == -4
