@@ -1,17 +1,42 @@
-// linear_attention.hip -- linear attention with a decay for each head.
+// linear_attention.hip -- linear attention with a decay for each head:
+//     S_t = gamma S_{t-1} + b_t c_t^T,   o_t = a_t S_t
+// for whole sequences, chunk by chunk on the matrix cores, and for single
+// tokens.
+//
+// A chunk of C tokens, with the matrix S before it, local indices i and j:
+//     O  = diag(gamma^(i+e)) A S + ((A B^T) . W) Cv,   W_ij = gamma^(i-j) for i >= j, else 0
+//     S' = gamma^C S + B^T diag(gamma^(C-j-e)) Cv
+// with e = 1; in a reversed pass e = 0 and tokens count from the row's end.
+// Every power has an exponent of at least 0, so nothing overflows however
+// small gamma is.
 #include "device.h"
 #include "ops.h"
 #include "ops_dev.h"
 
 namespace lstm_amd {
 
-void la_segments(int T, long long rows, int da, int dc, int dtype, int *nseg, int *seg_tokens) {
-    (void)rows, (void)da, (void)dc, (void)dtype;
-    *nseg = 1;
-    *seg_tokens = T;
-}
-
 namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// log2 gamma, finite: gamma = 0 (log decay -infinity) becomes 2^-1e30, whose
+// power 0 is 1 and whose other powers are 0.  NaN stays.
+__device__ inline float la_log2(float log_decay) {
+    const float g = log_decay * kLog2e;
+    return g < -1e30f ? -1e30f : g;
+}
+__device__ inline float la_pow(float g2, int n) { return __builtin_amdgcn_exp2f((float)n * g2); }
+
+__device__ inline int la_len(const int *lengths, int b, int T) {
+    if (!lengths) return T;
+    const int n = lengths[b];
+    return n < 0 ? 0 : n > T ? T : n;
+}
 
 template <class DT>
 __device__ inline float la_get(const LaTensor &x, int t, int b, int h, int d) {
@@ -28,42 +53,479 @@ __device__ inline void la_put(const LaOut &o, int t, int b, int h, int d, float 
         reinterpret_cast<typename DT::S *>(o.p)[at] = round_to<DT>(v);
 }
 
-// gamma^n for n >= 0; n = 0 is 1 also for gamma = 0 (log decay -infinity).
-__device__ inline float la_pow(float g2, int n) { return n == 0 ? 1.0f : __builtin_amdgcn_exp2f((float)n * g2); }
-
-// One wave per 64 columns of one (batch row, head): the recurrence itself,
-// token by token, the carried matrix in LDS.
-template <class DT>
-__global__ __launch_bounds__(64) void k_la_tokens(LaPass p, const float *log_decay, const int *lengths, int T, int H) {
-    extern __shared__ float S[];  // [da][64]
-    const int lane = threadIdx.x, col = blockIdx.x * 64 + lane;
-    const int h = blockIdx.y % H, b = blockIdx.y / H;
-    const bool on = col < p.dc;
-    int len = lengths ? lengths[b] : T;
-    len = len < 0 ? 0 : len > T ? T : len;
-    const float gamma = la_pow(log_decay[h] * 1.4426950408889634f, 1);
-    const size_t sbase = ((size_t)b * H + h) * p.da * p.dc;
-    for (int d = 0; d < p.da; ++d)
-        S[d * 64 + lane] = p.s0 && on ? p.s0[sbase + (size_t)d * p.srow + (size_t)col * p.scol] * p.in_scale : 0.0f;
-    for (int i = 0; i < len; ++i) {
-        const int t = p.reverse ? len - 1 - i : i;
-        const float cv = on ? la_get<DT>(p.c, t, b, h, col) : 0.0f;
-        float sum = 0.0f;
-        for (int d = 0; d < p.da; ++d) {
-            float s = S[d * 64 + lane];
-            if (!p.reverse) s *= gamma;
-            s += la_get<DT>(p.b, t, b, h, d) * cv;
-            sum += la_get<DT>(p.a, t, b, h, d) * s;
-            if (p.reverse) s *= gamma;
-            S[d * 64 + lane] = s;
-        }
-        if (on) la_put<DT>(p.o, t, b, h, col, sum * p.out_scale);
+// N neighbouring columns of a token from element offset `at`, `left` of them in range.
+template <class DT, int N, class V>
+__device__ inline void la_write(const LaOut &o, long long at, V v, int left) {
+    if (left <= 0) return;
+    if (o.f32 || sizeof(typename DT::S) == 4) {
+        float *q = reinterpret_cast<float *>(o.p) + at;
+        if (left >= N)
+            __builtin_memcpy(q, &v, sizeof(v));
+        else
+            for (int x = 0; x < N; ++x)
+                if (x < left) q[x] = v[x];
+    } else {
+        typename DT::S *q = reinterpret_cast<typename DT::S *>(o.p) + at, tmp[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) tmp[x] = round_to<DT>(v[x]);
+        if (left >= N)
+            __builtin_memcpy(q, tmp, sizeof(tmp));
+        else
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+                if (x < left) q[x] = tmp[x];
     }
-    if (on)
-        for (int t = len; t < T; ++t) la_put<DT>(p.o, t, b, h, col, 0.0f);
-    if (p.s1 && on)
-        for (int d = 0; d < p.da; ++d)
-            p.s1[sbase + (size_t)d * p.srow + (size_t)col * p.scol] = S[d * 64 + lane] * p.s1_scale;
+}
+
+// Shape of a workgroup's tile.  A wave owns NT column tiles of 16 of S (all of
+// its DA rows, in accumulators) for the whole sequence, so S never leaves the
+// registers: the accumulator layout of S (rows 4g+r of a tile, g = lane / 16)
+// is, read as an operand over the row axis, a fragment.  bf16 fragments hold 8
+// consecutive values of a 32-long axis, that is rows 8g..8g+7: the row tiles
+// 2u and 2u+1 take the rows 32u + 8g + r and 32u + 8g + 4 + r (row_of), so a
+// pair of accumulators is the fragment of 32u + 8g.. without a move between
+// lanes.  The same holds for the chunk's products A B^T, whose tiles become
+// the operand of the product with Cv.
+template <class DT, int DA_, int NW_>
+struct LaTile {
+    static constexpr int DA = DA_, NW = NW_, NT = DA_ > 128 ? 1 : 2;
+    static constexpr int PER = DT::PER16, KC = DT::KC, TPK = KC / 16;
+    static constexpr int C = sizeof(typename DT::S) == 2 ? 64 : 32;  // tokens of a chunk
+    static constexpr int NU = DA / KC, JU = C / KC, AT = DA / 16;
+    static constexpr int COLS = NW * 16 * NT;                  // columns of a workgroup
+    static constexpr int THREADS = 64 * NW;
+    static constexpr int RA = DA / PER, RC = COLS / PER;       // 16-byte pieces of a row in LDS
+    static constexpr int PA = C * RA / THREADS, PC = C * RC / THREADS;  // pieces a thread moves
+    static_assert(C * RA % THREADS == 0 && C * RC % THREADS == 0 && THREADS % RA == 0 && THREADS % RC == 0, "tile");
+
+    // row (of the 16-row tile `tile`) that accumulator row 4g + r stands for
+    __device__ static int row_of(int tile, int g, int r) {
+        return TPK == 2 ? 32 * (tile / 2) + 8 * g + 4 * (tile % 2) + r : 16 * tile + 4 * g + r;
+    }
+    // column (of a wave's NT tiles) that position m of tile n stands for
+    __device__ static int col_of(int n, int m) {
+        return TPK == 2 && NT == 2 ? 8 * (m / 4) + 4 * n + m % 4 : 16 * n + m;
+    }
+    // Piece p of LDS row j lies at p ^ key(j): the 16 rows that a fragment
+    // read touches, and the 4 rows x 4 pieces of a transposed read, then all
+    // fall on different banks (64 banks of 4 bytes).
+    template <int R>
+    __device__ static int key(int j) {
+        if (TPK == 1) return j & 15;
+        return R >= 16 ? ((j & 3) << 2) | ((j >> 3) & 3) : (((j >> 1) & 1) << 2) | ((j >> 3) & 3);
+    }
+    template <int R>
+    __device__ static int at(int j, int p) {
+        return (j * R + (p ^ key<R>(j))) * PER;
+    }
+};
+
+// 16 bytes of row p at element d, zero past dim.  No alignment is assumed: the
+// hardware splits what is not aligned.
+template <class DT>
+__device__ inline u32x4 la_load(const typename DT::S *p, int d, int dim) {
+    using S = typename DT::S;
+    u32x4 v = {0, 0, 0, 0};
+    if (d + DT::PER16 <= dim) {
+        __builtin_memcpy(&v, p + d, 16);
+    } else if (d < dim) {
+        S tmp[DT::PER16];
+#pragma unroll
+        for (int e = 0; e < DT::PER16; ++e) tmp[e] = d + e < dim ? p[d + e] : (S)0;
+        v = __builtin_bit_cast(u32x4, tmp);
+    }
+    return v;
+}
+
+// Tokens of one tensor on their way from memory to LDS: piece p of a thread is
+// row tid / R + p * (THREADS / R), 16-byte piece tid % R.
+template <class DT, class TL, int R, int P>
+struct LaStage {
+    const typename DT::S *base;  // the thread's first row
+    long long step;              // elements between tokens, signed by direction
+    int row, piece, dim;
+    u32x4 v[P];
+
+    __device__ void init(const LaTensor &x, int b, int h, int t0, int dir, int d0, int dim_) {
+        row = threadIdx.x / R;
+        piece = threadIdx.x % R;
+        dim = dim_ - d0;
+        step = x.t * dir;
+        base = reinterpret_cast<const typename DT::S *>(x.p) + (long long)t0 * x.t + (long long)b * x.b +
+               (long long)(h / x.hdiv) * x.h + d0 + row * step;
+    }
+    // tokens i0.. of which n are valid
+    __device__ void load(int i0, int n) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            constexpr int RS = TL::THREADS / R;
+            v[p] = u32x4{0, 0, 0, 0};
+            if (row + p * RS < n) v[p] = la_load<DT>(base + (i0 + p * RS) * step, piece * TL::PER, dim);
+        }
+    }
+    __device__ void store(typename DT::S *lds) const {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            *reinterpret_cast<u32x4 *>(lds + TL::template at<R>(row + p * (TL::THREADS / R), piece)) = v[p];
+    }
+};
+
+// Fragment of rows: lane (m, g) gets row tile_row(m), values KC*u + PER*g ...
+template <class DT, class TL, int R>
+__device__ inline u32x4 la_frag(const typename DT::S *lds, int tile, int u, int lane) {
+    const int m = lane % 16, g = lane / 16;
+    return *reinterpret_cast<const u32x4 *>(lds + TL::template at<R>(TL::row_of(tile, m / 4, m % 4), 4 * u + g));
+}
+
+// Fragment of columns over the tokens KC*ju..: lane (m, g) gets column
+// col(m), tokens KC*ju + PER*g + 0..PER-1.  col4(c) is the first of the four
+// columns that positions 4c..4c+3 stand for.  bf16: two transposed reads of 4
+// tokens x 16 columns for each 16 lanes (lane 4r+c of them names row r, columns
+// col4(c).., and receives column 4r+c of all four rows).
+template <class DT, class TL, int R, class F>
+__device__ inline u32x4 la_cols(const typename DT::S *lds, int ju, F col4, int lane) {
+    const int m = lane % 16, g = lane / 16;
+    if constexpr (TL::TPK == 2) {
+        u32x2 h[2];
+        const int c = col4(m % 4);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int j = 32 * ju + 8 * g + 4 * k + m / 4;
+            auto p = (__attribute__((address_space(3))) s16x4 *)(lds + TL::template at<R>(j, c / 8) + c % 8);
+            h[k] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+        }
+        return u32x4{h[0].x, h[0].y, h[1].x, h[1].y};
+    } else {
+        const int c = col4(m / 4) + m % 4;
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = *reinterpret_cast<const uint32_t *>(lds + TL::template at<R>(16 * ju + 4 * g + e, c / 4) + c % 4);
+        return v;
+    }
+}
+
+// Accumulators of TPK row tiles as one fragment (bf16: rounded here, once).
+template <class DT, class TL>
+__device__ inline u32x4 la_pack(const f32x4 *acc, int stride) {
+    if constexpr (TL::TPK == 2) {
+        const f32x4 x = acc[0], y = acc[stride];
+        const bf16x8 v = __builtin_convertvector(f32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}, bf16x8);
+        return __builtin_bit_cast(u32x4, v);
+    } else {
+        return __builtin_bit_cast(u32x4, acc[0]);
+    }
+}
+
+// The state update's operand: column fragments times gamma^(n-1-j+1-e) for the
+// chunk's n valid tokens.  bf16: the weighted value is kept as a sum of two
+// bf16, so that S is exact to about 2^-17 a term (one bf16 would leave 2^-9
+// in a state that is an fp32 result and is carried from call to call).
+template <class DT, class TL>
+struct LaWeighted {
+    u32x4 hi[TL::NT][TL::JU], lo[TL::NT][TL::JU];
+    __device__ void make(const u32x4 (*cf)[TL::JU], float g2, int n, int e, int lane) {
+        const int g = lane / 16;
+#pragma unroll
+        for (int ju = 0; ju < TL::JU; ++ju) {
+            float w[TL::PER];
+#pragma unroll
+            for (int x = 0; x < TL::PER; ++x) {
+                const int j = TL::KC * ju + TL::PER * g + x;
+                w[x] = j < n ? la_pow(g2, n - j - e) : 0.0f;
+            }
+#pragma unroll
+            for (int t = 0; t < TL::NT; ++t) {
+                if constexpr (TL::TPK == 2) {
+                    const bf16x8 v = __builtin_bit_cast(bf16x8, cf[t][ju]);
+                    f32x8 f = __builtin_convertvector(v, f32x8);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) f[x] *= w[x];
+                    const bf16x8 h = __builtin_convertvector(f, bf16x8);
+                    f -= __builtin_convertvector(h, f32x8);
+                    hi[t][ju] = __builtin_bit_cast(u32x4, h);
+                    lo[t][ju] = __builtin_bit_cast(u32x4, __builtin_convertvector(f, bf16x8));
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        hi[t][ju][x] = __float_as_uint(__uint_as_float(cf[t][ju][x]) * w[x]);
+                }
+            }
+        }
+    }
+};
+
+// Where a workgroup is: pass, batch row, head, segment, column slab.
+struct LaWhere {
+    int pass, b, h, seg, slab;
+};
+
+// Workgroups that share operands (the slabs of a head, the passes of a
+// gradient, the heads of a group) get neighbouring numbers; the number is
+// spread so that each of the 8 XCDs, which take workgroups in turn, gets a run
+// of neighbours and finds them in its L2.
+__device__ inline LaWhere la_where(const LaCall &c, int slabs) {
+    const unsigned n = gridDim.x, x = blockIdx.x % 8, i = blockIdx.x / 8;
+    unsigned id = x * (n / 8) + (x < n % 8 ? x : n % 8) + i;
+    LaWhere w;
+    w.slab = id % slabs;
+    id /= slabs;
+    w.pass = id % c.npass;
+    id /= c.npass;
+    w.h = id % c.H;
+    id /= c.H;
+    w.seg = id % c.nseg;
+    w.b = id / c.nseg;
+    return w;
+}
+
+// Offset of a wave's part of a segment's matrix in the workspace: fragment
+// order [segment][row][slab][wave][tile][n][lane], 4 rows each.
+template <class TL>
+__device__ inline size_t la_seg_at(const LaCall &c, const LaWhere &w, int slabs, int wave, int lane) {
+    const size_t row = ((size_t)w.seg * c.B + w.b) * c.H + w.h;
+    return (((row * slabs + w.slab) * TL::NW + wave) * (TL::AT * TL::NT) * 64 + lane) * 4;
+}
+
+template <class DT, class TL, bool STATE_ONLY>
+__global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
+    using S_t = typename DT::S;
+    __shared__ S_t la[STATE_ONLY ? 8 : TL::C * TL::DA], lb[TL::C * TL::DA], lc[TL::C * TL::COLS];
+    const LaWhere at = la_where(c, slabs);
+    const LaPass &p = c.pass[at.pass];
+    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, m = lane % 16, g = lane / 16;
+    const int len = la_len(c.lengths, at.b, c.T);
+    const int i0 = at.seg * c.seg_tokens, i1 = min(len, i0 + c.seg_tokens);  // this segment's tokens
+    const int dir = p.reverse ? -1 : 1, first = p.reverse ? len - 1 : 0, e = p.reverse ? 0 : 1;
+    const float g2 = la_log2(c.log_decay[at.h]);
+    const int slab0 = at.slab * TL::COLS, col0 = slab0 + wave * 16 * TL::NT;
+    const bool busy = col0 < p.dc;  // else the wave only moves data
+
+    f32x4 S[TL::AT * TL::NT];
+#pragma unroll
+    for (int x = 0; x < TL::AT * TL::NT; ++x) S[x] = f32x4{0, 0, 0, 0};
+    if (!STATE_ONLY && busy) {
+        if (p.seg) {
+            const float *src = p.seg + la_seg_at<TL>(c, at, slabs, wave, lane);
+#pragma unroll
+            for (int x = 0; x < TL::AT * TL::NT; ++x) S[x] = *reinterpret_cast<const f32x4 *>(src + x * 256);
+        } else if (p.s0) {
+            const float *src = p.s0 + ((size_t)at.b * c.H + at.h) * p.da * p.dc;
+#pragma unroll
+            for (int t = 0; t < TL::AT; ++t)
+#pragma unroll
+                for (int n = 0; n < TL::NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = TL::row_of(t, g, r), col = col0 + TL::col_of(n, m);
+                        if (row < p.da && col < p.dc)
+                            S[t * TL::NT + n][r] = src[row * p.srow + col * p.scol] * p.in_scale;
+                    }
+        }
+    }
+
+    LaStage<DT, TL, TL::RA, TL::PA> sa, sb;
+    LaStage<DT, TL, TL::RC, TL::PC> sc;
+    if (!STATE_ONLY) sa.init(p.a, at.b, at.h, first, dir, 0, p.da);
+    sb.init(p.b, at.b, at.h, first, dir, 0, p.da);
+    sc.init(p.c, at.b, at.h, first, dir, slab0, p.dc);
+    auto fetch = [&](int i) {
+        const int n = i1 - i;
+        if (!STATE_ONLY) sa.load(i, n);
+        sb.load(i, n);
+        sc.load(i, n);
+    };
+    if (i0 < i1) fetch(i0);
+
+    for (int i = i0; i < i1; i += TL::C) {
+        const int n = min(TL::C, i1 - i);
+        __syncthreads();  // the chunk before has been read
+        if (!STATE_ONLY) sa.store(la);
+        sb.store(lb);
+        sc.store(lc);
+        if (i + TL::C < i1) fetch(i + TL::C);
+        __syncthreads();
+        if (!busy) continue;
+
+        u32x4 cf[TL::NT][TL::JU];
+#pragma unroll
+        for (int t = 0; t < TL::NT; ++t)
+#pragma unroll
+            for (int ju = 0; ju < TL::JU; ++ju)
+                cf[t][ju] = la_cols<DT, TL, TL::RC>(
+                    lc, ju, [&](int x) { return wave * 16 * TL::NT + TL::col_of(t, 4 * x); }, lane);
+
+        if constexpr (!STATE_ONLY) {
+            // outputs, 32 tokens at a time; O is held transposed (rows: columns
+            // of Cv), so that a lane ends with neighbouring columns of a token
+#pragma unroll
+            for (int ib = 0; ib < TL::C / 32; ++ib) {
+                u32x4 af[2][TL::NU];
+#pragma unroll
+                for (int it = 0; it < 2; ++it)
+#pragma unroll
+                    for (int u = 0; u < TL::NU; ++u)
+                        af[it][u] = la_frag<DT, TL, TL::RA>(la, 2 * ib + it, u, lane);
+                f32x4 O[2][TL::NT];
+#pragma unroll
+                for (int it = 0; it < 2; ++it)
+#pragma unroll
+                    for (int t = 0; t < TL::NT; ++t) O[it][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int u = 0; u < TL::NU; ++u)
+#pragma unroll
+                    for (int t = 0; t < TL::NT; ++t) {
+                        const u32x4 sf = la_pack<DT, TL>(&S[u * TL::TPK * TL::NT + t], TL::NT);
+#pragma unroll
+                        for (int it = 0; it < 2; ++it) O[it][t] = mma_chunk(DT{}, O[it][t], sf, af[it][u]);
+                    }
+                int row[2];
+#pragma unroll
+                for (int it = 0; it < 2; ++it) {
+                    row[it] = TL::row_of(2 * ib + it, m / 4, m % 4);
+                    const float w = la_pow(g2, row[it] + e);
+#pragma unroll
+                    for (int t = 0; t < TL::NT; ++t) O[it][t] *= w;
+                }
+#pragma unroll
+                for (int ju = 0; ju < TL::JU; ++ju) {
+                    if (ju * TL::KC > ib * 32 + 31) continue;
+                    f32x4 P[2][TL::TPK];
+#pragma unroll
+                    for (int it = 0; it < 2; ++it)
+#pragma unroll
+                        for (int k = 0; k < TL::TPK; ++k) P[it][k] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < TL::TPK; ++k)
+#pragma unroll
+                        for (int u = 0; u < TL::NU; ++u) {
+                            const u32x4 bf = la_frag<DT, TL, TL::RA>(lb, ju * TL::TPK + k, u, lane);
+#pragma unroll
+                            for (int it = 0; it < 2; ++it) P[it][k] = mma_chunk(DT{}, P[it][k], bf, af[it][u]);
+                        }
+#pragma unroll
+                    for (int it = 0; it < 2; ++it) {
+#pragma unroll
+                        for (int k = 0; k < TL::TPK; ++k)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const int d = row[it] - TL::row_of(ju * TL::TPK + k, g, r);
+                                P[it][k][r] = d >= 0 ? P[it][k][r] * la_pow(g2, d) : 0.0f;
+                            }
+                        const u32x4 pf = la_pack<DT, TL>(P[it], 1);
+#pragma unroll
+                        for (int t = 0; t < TL::NT; ++t) O[it][t] = mma_chunk(DT{}, O[it][t], cf[t][ju], pf);
+                    }
+                }
+#pragma unroll
+                for (int it = 0; it < 2; ++it) {
+                    if (row[it] >= n) continue;
+                    const long long tok = first + (long long)dir * (i + row[it]);
+                    const long long o = tok * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h;
+#pragma unroll
+                    for (int t = 0; t < TL::NT; ++t) O[it][t] *= p.out_scale;
+                    if constexpr (TL::TPK == 2 && TL::NT == 2) {  // 8 neighbouring columns
+                        const int col = col0 + 8 * g;
+                        const f32x8 v = __builtin_shufflevector(O[it][0], O[it][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                        la_write<DT, 8>(p.o, o + col, v, p.dc - col);
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < TL::NT; ++t) {
+                            const int col = col0 + 16 * t + 4 * g;
+                            la_write<DT, 4>(p.o, o + col, O[it][t], p.dc - col);
+                        }
+                    }
+                }
+            }
+        }
+
+        // the state after the chunk, unless nothing reads it
+        if (!STATE_ONLY && i + TL::C >= i1 && !(p.s1 && !p.seg)) continue;
+        LaWeighted<DT, TL> cw;
+        cw.make(cf, g2, n, e, lane);
+        const float whole = la_pow(g2, n);
+#pragma unroll
+        for (int t = 0; t < TL::AT; ++t) {
+#pragma unroll
+            for (int x = 0; x < TL::NT; ++x) S[t * TL::NT + x] *= whole;
+#pragma unroll
+            for (int ju = 0; ju < TL::JU; ++ju) {
+                const u32x4 bt = la_cols<DT, TL, TL::RA>(
+                    lb, ju, [&](int x) { return TL::row_of(t, x, 0); }, lane);
+#pragma unroll
+                for (int x = 0; x < TL::NT; ++x) {
+                    S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.hi[x][ju]);
+                    if constexpr (TL::TPK == 2)
+                        S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.lo[x][ju]);
+                }
+            }
+        }
+    }
+
+    if (!busy) return;
+    if constexpr (STATE_ONLY) {
+        float *dst = p.seg + la_seg_at<TL>(c, at, slabs, wave, lane);
+#pragma unroll
+        for (int x = 0; x < TL::AT * TL::NT; ++x) *reinterpret_cast<f32x4 *>(dst + x * 256) = S[x];
+    } else {
+        if (p.s1 && !p.seg) {
+            float *dst = p.s1 + ((size_t)at.b * c.H + at.h) * p.da * p.dc;
+#pragma unroll
+            for (int t = 0; t < TL::AT; ++t)
+#pragma unroll
+                for (int x = 0; x < TL::NT; ++x)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = TL::row_of(t, g, r), col = col0 + TL::col_of(x, m);
+                        if (row < p.da && col < p.dc)
+                            dst[row * p.srow + col * p.scol] = S[t * TL::NT + x][r] * p.s1_scale;
+                    }
+        }
+        // tokens past the row's end, by the segment of their own position
+        const int width = min(16 * TL::NT, p.dc - col0), t1 = min(c.T, i0 + c.seg_tokens);
+        for (int t = max(len, i0) + lane / 16; t < t1; t += 4)
+            for (int d = m; d < width; d += 16) la_put<DT>(p.o, t, at.b, at.h, col0 + d, 0.0f);
+    }
+}
+
+// Segments' own matrices -> the matrix before each segment, in place:
+//     run = in_scale S0;  for each s: (seg_s, run) = (run, gamma^(tokens of s) run + seg_s)
+// A thread keeps 4 rows of one column; also writes the state after the last.
+template <class DT, class TL>
+__global__ __launch_bounds__(256) void k_la_join(LaCall c, int slabs) {
+    const LaPass &p = c.pass[blockIdx.y];
+    constexpr int PER_ROW = TL::AT * TL::NT * 64;  // threads for a wave's part
+    const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const size_t row_size = (size_t)slabs * TL::NW * PER_ROW, rows = (size_t)c.B * c.H;
+    if (id >= rows * row_size) return;
+    const int bh = (int)(id / row_size), x = (int)(id % row_size);
+    const int lane = x % 64, tile = x / 64 % (TL::AT * TL::NT), wave = x / PER_ROW % TL::NW, slab = x / PER_ROW / TL::NW;
+    const int b = bh / c.H, h = bh % c.H, n = tile % TL::NT;
+    const int col = slab * TL::COLS + wave * 16 * TL::NT + TL::col_of(n, lane % 16);
+    const int row = TL::row_of(tile / TL::NT, lane / 16, 0);  // rows row .. row + 3
+    if (col >= p.dc || row >= p.da) {
+        // never read back into a result: the operands are zero there
+        for (int s = 0; s < c.nseg; ++s)
+            *reinterpret_cast<f32x4 *>(p.seg + (s * rows * row_size + id) * 4) = f32x4{0, 0, 0, 0};
+        return;
+    }
+    const int len = la_len(c.lengths, b, c.T);
+    const float g2 = la_log2(c.log_decay[h]);
+    const size_t own = (size_t)bh * p.da * p.dc;
+    f32x4 run = {0, 0, 0, 0};
+    if (p.s0)
+        for (int r = 0; r < 4 && row + r < p.da; ++r)
+            run[r] = p.s0[own + (row + r) * p.srow + col * p.scol] * p.in_scale;
+    for (int s = 0; s < c.nseg; ++s) {
+        f32x4 *q = reinterpret_cast<f32x4 *>(p.seg + (s * rows * row_size + id) * 4);
+        const f32x4 add = *q;
+        *q = run;
+        const int tokens = min(max(len - s * c.seg_tokens, 0), c.seg_tokens);
+        run = run * la_pow(g2, tokens) + add;
+    }
+    if (p.s1)
+        for (int r = 0; r < 4 && row + r < p.da; ++r)
+            p.s1[own + (row + r) * p.srow + col * p.scol] = run[r] * p.s1_scale;
 }
 
 template <class DT>
@@ -88,7 +550,7 @@ __global__ __launch_bounds__(64) void k_la_step(LaStep c) {
     const int slot = c.slots ? c.slots[b] : b;
     float sum = 0.0f;
     if (slot >= 0 && slot < c.n_slots) {
-        const float gamma = la_pow(c.log_decay[h] * 1.4426950408889634f, 1);
+        const float gamma = la_pow(la_log2(c.log_decay[h]), 1);
         const float v = la_get<DT>(c.v, 0, b, h, col);
         float *s = c.pool + ((size_t)slot * c.H + h) * c.Dk * c.Dv + col;
         for (int d = 0; d < c.Dk; ++d) {
@@ -102,19 +564,64 @@ __global__ __launch_bounds__(64) void k_la_step(LaStep c) {
 
 }  // namespace
 
-hipError_t launch_la(const LaCall &c, hipStream_t s) {
-    for (int i = 0; i < c.npass; ++i) {
-        const LaPass &p = c.pass[i];
-        const dim3 grid((p.dc + 63) / 64, c.B * c.H);
-        const size_t lds = (size_t)p.da * 64 * sizeof(float);
-        if (c.dtype == LSTM_BF16)
-            hipLaunchKernelGGL(k_la_tokens<BF16>, grid, dim3(64), lds, s, p, c.log_decay, c.lengths, c.T, c.H);
-        else
-            hipLaunchKernelGGL(k_la_tokens<F32>, grid, dim3(64), lds, s, p, c.log_decay, c.lengths, c.T, c.H);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+namespace {
+
+// Tile of a call: the contraction dim padded to 64, 128 or 256, and the waves
+// of a workgroup: 4, or 2 where no pass has more columns than two waves take.
+struct LaPlan {
+    int DA, NW, cols;
+};
+LaPlan la_plan(int da, int dc) {
+    LaPlan t;
+    t.DA = da <= 64 ? 64 : da <= 128 ? 128 : 256;
+    t.NW = t.DA == 64 && dc <= 64 ? 2 : 4;
+    t.cols = t.NW * 16 * (t.DA > 128 ? 1 : 2);
+    return t;
+}
+
+template <class DT, int DA, int NW>
+hipError_t la_go(const LaCall &c, int dc, hipStream_t s) {
+    using TL = LaTile<DT, DA, NW>;
+    const int slabs = (dc + TL::COLS - 1) / TL::COLS;
+    const long long blocks = (long long)slabs * c.npass * c.H * c.B * c.nseg;
+    if (blocks > 0x7FFFFFFF / TL::THREADS) return hipErrorInvalidValue;
+    if (c.nseg > 1) {
+        hipLaunchKernelGGL((k_la<DT, TL, true>), dim3((unsigned)blocks), dim3(TL::THREADS), 0, s, c, slabs);
+        const size_t n = (size_t)c.B * c.H * slabs * NW * TL::AT * TL::NT * 64;
+        hipLaunchKernelGGL((k_la_join<DT, TL>), dim3((unsigned)((n + 255) / 256), c.npass), dim3(256), 0, s, c, slabs);
     }
-    return hipSuccess;
+    hipLaunchKernelGGL((k_la<DT, TL, false>), dim3((unsigned)blocks), dim3(TL::THREADS), 0, s, c, slabs);
+    return hipGetLastError();
+}
+
+template <class DT>
+hipError_t la_any(const LaCall &c, hipStream_t s) {
+    const int da = c.npass > 1 ? max(c.pass[0].da, c.pass[0].dc) : c.pass[0].da;
+    const int dc = c.npass > 1 ? da : c.pass[0].dc;
+    const LaPlan t = la_plan(da, dc);
+    if (t.DA == 64) return t.NW == 2 ? la_go<DT, 64, 2>(c, dc, s) : la_go<DT, 64, 4>(c, dc, s);
+    return t.DA == 128 ? la_go<DT, 128, 4>(c, dc, s) : la_go<DT, 256, 4>(c, dc, s);
+}
+
+}  // namespace
+
+void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, int *nseg, int *seg_tokens,
+                 size_t *seg_floats) {
+    if (npass > 1) da = dc = da > dc ? da : dc;
+    const LaPlan t = la_plan(da, dc);
+    const int C = dtype == LSTM_BF16 ? 64 : 32;
+    const long long slabs = (dc + t.cols - 1) / t.cols, blocks = rows * npass * slabs;
+    const int chunks = (T + C - 1) / C;
+    long long want = blocks >= 256 ? 1 : 512 / blocks;
+    if (want > chunks / 2) want = chunks / 2;
+    const int per = want > 1 ? (int)((chunks + want - 1) / want) : chunks;  // chunks of a segment
+    *nseg = (chunks + per - 1) / per;
+    *seg_tokens = per * C;
+    *seg_floats = (size_t)t.DA * slabs * t.cols;
+}
+
+hipError_t launch_la(const LaCall &c, hipStream_t s) {
+    return c.dtype == LSTM_BF16 ? la_any<BF16>(c, s) : la_any<F32>(c, s);
 }
 
 hipError_t launch_la_share(const float *part, LaOut out, int T, int B, int H, int G, int D, int dtype, hipStream_t s) {

@@ -37,7 +37,7 @@ struct LaPass {
     int srow, scol;
     float in_scale, out_scale, s1_scale;
     int reverse;
-    float *seg;           // [nseg][B][H][da][dc] states at the segments' starts, or null (one segment)
+    float *seg;           // matrices before the segments (workspace), or null (one segment)
 };
 struct LaCall {
     LaPass pass[3];
@@ -48,8 +48,11 @@ struct LaCall {
     int nseg, seg_tokens; // segments of the sequence, tokens in each
 };
 
-// Segments a sequence is cut into, and their tokens (a multiple of the chunk).
-void la_segments(int T, long long rows, int da, int dc, int dtype, int *nseg, int *seg_tokens);
+// Segments a sequence of each of `rows` (batch row, head) pairs is cut into,
+// their tokens (a multiple of the chunk), and the floats of one matrix in the
+// workspace.
+void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, int *nseg, int *seg_tokens,
+                 size_t *seg_floats);
 hipError_t launch_la(const LaCall &c, hipStream_t s);
 // out head g = the sum, in order, of the fp32 partial sums [B][T][H][D] of its H / G query heads
 hipError_t launch_la_share(const float *part, LaOut out, int T, int B, int H, int G, int D, int dtype, hipStream_t s);

@@ -77,13 +77,12 @@ struct LaLayout {
 bool la_layout(const lstm_linear_attention_shape *s, bool backward, LaLayout *o) {
     const size_t rows = (size_t)s->B * s->heads;
     const int npass = backward ? 3 : 1;
-    la_segments(s->T, (long long)rows * npass, s->key_dim, s->value_dim, s->dtype, &o->nseg, &o->seg_tokens);
+    size_t floats = 0;
+    la_segments(s->T, (long long)rows, npass, s->key_dim, s->value_dim, s->dtype, &o->nseg, &o->seg_tokens, &floats);
     size_t off = 0;
     for (int i = 0; i < npass; ++i) {
         o->seg[i] = off;
-        if (o->nseg > 1 &&
-            !add_bytes(&off, (size_t)o->nseg, rows, (size_t)s->key_dim * s->value_dim, sizeof(float)))
-            return false;
+        if (o->nseg > 1 && !add_bytes(&off, (size_t)o->nseg, rows, floats, sizeof(float))) return false;
     }
     o->part_k = o->part_v = off;
     if (backward && s->heads != s->kv_heads) {
