@@ -90,12 +90,17 @@ template <class DT, int DA_, int NW_>
 struct LaTile {
     static constexpr int DA = DA_, NW = NW_, NT = DA_ > 128 ? 1 : 2;
     static constexpr int PER = DT::PER16, KC = DT::KC, TPK = KC / 16;
-    static constexpr int C = sizeof(typename DT::S) == 2 ? 64 : 32;  // tokens of a chunk
+    static constexpr int C = 32;                               // tokens of a chunk
     static constexpr int NU = DA / KC, JU = C / KC, AT = DA / 16;
     static constexpr int COLS = NW * 16 * NT;                  // columns of a workgroup
     static constexpr int THREADS = 64 * NW;
     static constexpr int RA = DA / PER, RC = COLS / PER;       // 16-byte pieces of a row in LDS
     static constexpr int PA = C * RA / THREADS, PC = C * RC / THREADS;  // pieces a thread moves
+    static constexpr int ELEMS = C * (2 * DA + COLS);          // a chunk's three tensors in LDS
+    static constexpr int PT = 4 / NW;                          // tiles of A B^T a wave computes
+    static constexpr int P_ELEMS = C * C;                      // and its (A B^T) . W
+    // a second LDS buffer (one barrier less a chunk) where 8 waves still fit a CU's 160 KB
+    static constexpr int BUFS = 2 * (ELEMS + P_ELEMS) * (int)sizeof(typename DT::S) * (8 / NW) <= 160 * 1024 ? 2 : 1;
     static_assert(C * RA % THREADS == 0 && C * RC % THREADS == 0 && THREADS % RA == 0 && THREADS % RC == 0, "tile");
 
     // row (of the 16-row tile `tile`) that accumulator row 4g + r stands for
@@ -290,7 +295,8 @@ __device__ inline size_t la_seg_at(const LaCall &c, const LaWhere &w, int slabs,
 template <class DT, class TL, bool STATE_ONLY>
 __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     using S_t = typename DT::S;
-    __shared__ S_t la[STATE_ONLY ? 8 : TL::C * TL::DA], lb[TL::C * TL::DA], lc[TL::C * TL::COLS];
+    __shared__ __align__(16) S_t tiles[TL::BUFS][TL::ELEMS];
+    __shared__ __align__(16) S_t Ps[STATE_ONLY ? 1 : TL::BUFS][2 * TL::JU][64][TL::PER];  // fragments [it][ju] of (A B^T) . W
     const LaWhere at = la_where(c, slabs);
     const LaPass &p = c.pass[at.pass];
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, m = lane % 16, g = lane / 16;
@@ -299,7 +305,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     const int dir = p.reverse ? -1 : 1, first = p.reverse ? len - 1 : 0, e = p.reverse ? 0 : 1;
     const float g2 = la_log2(c.log_decay[at.h]);
     const int slab0 = at.slab * TL::COLS, col0 = slab0 + wave * 16 * TL::NT;
-    const bool busy = col0 < p.dc;  // else the wave only moves data
+    const bool busy = col0 < p.dc;  // else the wave only moves data and takes its part in A B^T
 
     f32x4 S[TL::AT * TL::NT];
 #pragma unroll
@@ -335,92 +341,125 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
         sb.load(i, n);
         sc.load(i, n);
     };
-    if (i0 < i1) fetch(i0);
+    auto put = [&](S_t *t) {
+        if (!STATE_ONLY) sa.store(t);
+        sb.store(t + TL::C * TL::DA);
+        sc.store(t + 2 * TL::C * TL::DA);
+    };
+    if (i0 < i1) {
+        fetch(i0);
+        put(tiles[0]);
+    }
 
+    int buf = 0;
     for (int i = i0; i < i1; i += TL::C) {
         const int n = min(TL::C, i1 - i);
-        __syncthreads();  // the chunk before has been read
-        if (!STATE_ONLY) sa.store(la);
-        sb.store(lb);
-        sc.store(lc);
-        if (i + TL::C < i1) fetch(i + TL::C);
-        __syncthreads();
-        if (!busy) continue;
+        const bool more = i + TL::C < i1;
+        if (more) fetch(i + TL::C);
+        __syncthreads();  // this chunk lies in LDS
+        const S_t *la = tiles[buf], *lb = la + TL::C * TL::DA, *lc = lb + TL::C * TL::DA;
 
-        u32x4 cf[TL::NT][TL::JU];
-#pragma unroll
-        for (int t = 0; t < TL::NT; ++t)
-#pragma unroll
-            for (int ju = 0; ju < TL::JU; ++ju)
-                cf[t][ju] = la_cols<DT, TL, TL::RC>(
-                    lc, ju, [&](int x) { return wave * 16 * TL::NT + TL::col_of(t, 4 * x); }, lane);
-
+        // This wave's tiles of B A^T (rows: tokens j), weighted, as parts of
+        // the fragments that the product with Cv reads.
+        S_t(*ps)[64][TL::PER] = Ps[STATE_ONLY ? 0 : buf];
         if constexpr (!STATE_ONLY) {
-            // outputs, 32 tokens at a time; O is held transposed (rows: columns
-            // of Cv), so that a lane ends with neighbouring columns of a token
 #pragma unroll
-            for (int ib = 0; ib < TL::C / 32; ++ib) {
-                u32x4 af[2][TL::NU];
-#pragma unroll
-                for (int it = 0; it < 2; ++it)
+            for (int x = 0; x < TL::PT; ++x) {
+                const int it = TL::NW == 4 ? wave % 2 : wave, jt = TL::NW == 4 ? wave / 2 : x;
+                f32x4 P = {0, 0, 0, 0};
+                if (TL::TPK == 2 || jt <= it) {
 #pragma unroll
                     for (int u = 0; u < TL::NU; ++u)
-                        af[it][u] = la_frag<DT, TL, TL::RA>(la, 2 * ib + it, u, lane);
-                f32x4 O[2][TL::NT];
+                        P = mma_chunk(DT{}, P, la_frag<DT, TL, TL::RA>(lb, jt, u, lane),
+                                      la_frag<DT, TL, TL::RA>(la, it, u, lane));
+                    const int ri = TL::row_of(it, m / 4, m % 4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int d = ri - TL::row_of(jt, g, r);
+                        P[r] = d >= 0 ? P[r] * la_pow(g2, d) : 0.0f;
+                    }
+                }
+                if constexpr (TL::TPK == 2)
+                    *reinterpret_cast<bf16x4 *>(&ps[it][lane][4 * jt]) = __builtin_convertvector(P, bf16x4);
+                else
+                    *reinterpret_cast<f32x4 *>(&ps[it * 2 + jt][lane][0]) = P;
+            }
+        }
+
+        f32x4 O[2][TL::NT];
+        u32x4 cf[TL::NT][TL::JU];
+        if (busy) {
+            if constexpr (!STATE_ONLY) {
+                // O = diag(gamma^(i+e)) A S, held transposed (rows: columns of
+                // Cv), so that a lane ends with neighbouring columns of a token
 #pragma unroll
                 for (int it = 0; it < 2; ++it)
 #pragma unroll
                     for (int t = 0; t < TL::NT; ++t) O[it][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int u = 0; u < TL::NU; ++u)
+                for (int u = 0; u < TL::NU; ++u) {
+                    u32x4 af[2];
+#pragma unroll
+                    for (int it = 0; it < 2; ++it) af[it] = la_frag<DT, TL, TL::RA>(la, it, u, lane);
 #pragma unroll
                     for (int t = 0; t < TL::NT; ++t) {
                         const u32x4 sf = la_pack<DT, TL>(&S[u * TL::TPK * TL::NT + t], TL::NT);
 #pragma unroll
-                        for (int it = 0; it < 2; ++it) O[it][t] = mma_chunk(DT{}, O[it][t], sf, af[it][u]);
+                        for (int it = 0; it < 2; ++it) O[it][t] = mma_chunk(DT{}, O[it][t], sf, af[it]);
                     }
-                int row[2];
+                }
 #pragma unroll
                 for (int it = 0; it < 2; ++it) {
-                    row[it] = TL::row_of(2 * ib + it, m / 4, m % 4);
-                    const float w = la_pow(g2, row[it] + e);
+                    const float w = la_pow(g2, TL::row_of(it, m / 4, m % 4) + e);
 #pragma unroll
                     for (int t = 0; t < TL::NT; ++t) O[it][t] *= w;
                 }
+            }
 #pragma unroll
-                for (int ju = 0; ju < TL::JU; ++ju) {
-                    if (ju * TL::KC > ib * 32 + 31) continue;
-                    f32x4 P[2][TL::TPK];
+            for (int t = 0; t < TL::NT; ++t)
 #pragma unroll
-                    for (int it = 0; it < 2; ++it)
+                for (int ju = 0; ju < TL::JU; ++ju)
+                    cf[t][ju] = la_cols<DT, TL, TL::RC>(
+                        lc, ju, [&](int x) { return wave * 16 * TL::NT + TL::col_of(t, 4 * x); }, lane);
+            // the state after the chunk, unless nothing reads it
+            if (STATE_ONLY || more || (p.s1 && !p.seg)) {
+                LaWeighted<DT, TL> cw;
+                cw.make(cf, g2, n, e, lane);
+                const float whole = la_pow(g2, n);
 #pragma unroll
-                        for (int k = 0; k < TL::TPK; ++k) P[it][k] = f32x4{0, 0, 0, 0};
+                for (int t = 0; t < TL::AT; ++t) {
 #pragma unroll
-                    for (int k = 0; k < TL::TPK; ++k)
+                    for (int x = 0; x < TL::NT; ++x) S[t * TL::NT + x] *= whole;
 #pragma unroll
-                        for (int u = 0; u < TL::NU; ++u) {
-                            const u32x4 bf = la_frag<DT, TL, TL::RA>(lb, ju * TL::TPK + k, u, lane);
+                    for (int ju = 0; ju < TL::JU; ++ju) {
+                        const u32x4 bt = la_cols<DT, TL, TL::RA>(
+                            lb, ju, [&](int x) { return TL::row_of(t, x, 0); }, lane);
 #pragma unroll
-                            for (int it = 0; it < 2; ++it) P[it][k] = mma_chunk(DT{}, P[it][k], bf, af[it][u]);
+                        for (int x = 0; x < TL::NT; ++x) {
+                            S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.hi[x][ju]);
+                            if constexpr (TL::TPK == 2)
+                                S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.lo[x][ju]);
                         }
+                    }
+                }
+            }
+        }
+
+        if constexpr (!STATE_ONLY) {
+            __syncthreads();  // the fragments of (A B^T) . W lie in LDS
+            if (busy) {
 #pragma unroll
-                    for (int it = 0; it < 2; ++it) {
+                for (int it = 0; it < 2; ++it) {
 #pragma unroll
-                        for (int k = 0; k < TL::TPK; ++k)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const int d = row[it] - TL::row_of(ju * TL::TPK + k, g, r);
-                                P[it][k][r] = d >= 0 ? P[it][k][r] * la_pow(g2, d) : 0.0f;
-                            }
-                        const u32x4 pf = la_pack<DT, TL>(P[it], 1);
+                    for (int ju = 0; ju < TL::JU; ++ju) {
+                        if (TL::TPK == 1 && ju > it) continue;
+                        const u32x4 pf = *reinterpret_cast<const u32x4 *>(&ps[it * TL::JU + ju][lane][0]);
 #pragma unroll
                         for (int t = 0; t < TL::NT; ++t) O[it][t] = mma_chunk(DT{}, O[it][t], cf[t][ju], pf);
                     }
-                }
-#pragma unroll
-                for (int it = 0; it < 2; ++it) {
-                    if (row[it] >= n) continue;
-                    const long long tok = first + (long long)dir * (i + row[it]);
+                    const int row = TL::row_of(it, m / 4, m % 4);
+                    if (row >= n) continue;
+                    const long long tok = first + (long long)dir * (i + row);
                     const long long o = tok * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h;
 #pragma unroll
                     for (int t = 0; t < TL::NT; ++t) O[it][t] *= p.out_scale;
@@ -438,28 +477,9 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                 }
             }
         }
-
-        // the state after the chunk, unless nothing reads it
-        if (!STATE_ONLY && i + TL::C >= i1 && !(p.s1 && !p.seg)) continue;
-        LaWeighted<DT, TL> cw;
-        cw.make(cf, g2, n, e, lane);
-        const float whole = la_pow(g2, n);
-#pragma unroll
-        for (int t = 0; t < TL::AT; ++t) {
-#pragma unroll
-            for (int x = 0; x < TL::NT; ++x) S[t * TL::NT + x] *= whole;
-#pragma unroll
-            for (int ju = 0; ju < TL::JU; ++ju) {
-                const u32x4 bt = la_cols<DT, TL, TL::RA>(
-                    lb, ju, [&](int x) { return TL::row_of(t, x, 0); }, lane);
-#pragma unroll
-                for (int x = 0; x < TL::NT; ++x) {
-                    S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.hi[x][ju]);
-                    if constexpr (TL::TPK == 2)
-                        S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.lo[x][ju]);
-                }
-            }
-        }
+        if (TL::BUFS == 1 && more) __syncthreads();  // the chunk has been read
+        if (more) put(tiles[TL::BUFS == 2 ? buf ^ 1 : 0]);
+        if (TL::BUFS == 2) buf ^= 1;
     }
 
     if (!busy) return;
@@ -607,9 +627,10 @@ hipError_t la_any(const LaCall &c, hipStream_t s) {
 
 void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, int *nseg, int *seg_tokens,
                  size_t *seg_floats) {
+    (void)dtype;
     if (npass > 1) da = dc = da > dc ? da : dc;
     const LaPlan t = la_plan(da, dc);
-    const int C = dtype == LSTM_BF16 ? 64 : 32;
+    constexpr int C = 32;
     const long long slabs = (dc + t.cols - 1) / t.cols, blocks = rows * npass * slabs;
     const int chunks = (T + C - 1) / C;
     long long want = blocks >= 256 ? 1 : 512 / blocks;
