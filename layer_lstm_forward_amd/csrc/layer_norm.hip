@@ -1,13 +1,20 @@
 // layer_norm.hip -- layer norm with its residual sum, forward and backward.
+//     z = x + residual,  u = (z - mean) rstd,  y = u w + b
+//     dz = rstd (g - mean(g) - u mean(g u)) + dsum  with g = dy w
+//     dw = sum over rows of dy u,  db = sum over rows of dy
+// Both directions are bound by memory: a row is read once, into registers,
+// and its sums are taken from there (the variance from the differences, in a
+// second look at the registers).
 #include "device.h"
 #include "ops.h"
 #include "ops_dev.h"
 
 namespace lstm_amd {
 
+// Two workgroups a CU keep the partial sums of the weight gradients.
 int ln_parts(long long rows, int width) {
     (void)width;
-    return (int)(rows < 256 ? rows : 256);
+    return (int)(rows < 512 ? rows : 512);
 }
 
 namespace {
@@ -21,9 +28,213 @@ __device__ inline float block_sum(float v, float *lds) {
     return lds[0] + lds[1] + lds[2] + lds[3];
 }
 
-// One workgroup per row.
+// A row lies over TPR threads, NV 16-byte pieces each: piece v of thread t is
+// the row's piece v * TPR + t.  A workgroup holds 256 / TPR rows at a time
+// (TPR = 1024: one row over 1024 threads).
+template <class DT, int TPR_, int NV_>
+struct LnTile {
+    static constexpr int TPR = TPR_, NV = NV_, PER = DT::PER16;
+    static constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
+    static constexpr int WIDTH = TPR * NV * PER;  // widest row
+};
+
+// Sum over the TPR threads of a row, the same value in each, in fixed order.
+template <class TL>
+__device__ inline float row_sum(float v, float *lds) {
+#pragma unroll
+    for (int o = (TL::TPR < 64 ? TL::TPR : 64) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    if constexpr (TL::TPR > 64) {
+        __syncthreads();
+        if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TL::TPR / 64; ++i) v += lds[i];
+    }
+    return v;
+}
+
+// One 16-byte piece widened, zeros past the row's end; any alignment.
 template <class DT>
-__global__ __launch_bounds__(256) void k_ln_forward(LnForward c) {
+__device__ inline void ln_load(const typename DT::S *p, int i, int W, float *f) {
+    using S = typename DT::S;
+    S t[DT::PER16];
+    if (i + DT::PER16 <= W)
+        __builtin_memcpy(t, p + i, 16);
+    else
+#pragma unroll
+        for (int e = 0; e < DT::PER16; ++e) t[e] = i + e < W ? p[i + e] : (S)0;
+#pragma unroll
+    for (int e = 0; e < DT::PER16; ++e) f[e] = DT::to_f(t[e]);
+}
+
+template <class DT>
+__device__ inline void ln_store(typename DT::S *p, int i, int W, const float *f) {
+    using S = typename DT::S;
+    S t[DT::PER16];
+#pragma unroll
+    for (int e = 0; e < DT::PER16; ++e) t[e] = round_to<DT>(f[e]);
+    if (i + DT::PER16 <= W)
+        __builtin_memcpy(p + i, t, 16);
+    else
+#pragma unroll
+        for (int e = 0; e < DT::PER16; ++e)
+            if (i + e < W) p[i + e] = t[e];
+}
+
+template <class DT, class TL>
+__global__ __launch_bounds__(TL::THREADS) void k_ln_forward(LnForward c) {
+    using S = typename DT::S;
+    constexpr int PER = TL::PER;
+    __shared__ float lds[16];
+    const int W = c.width, t = threadIdx.x % TL::TPR;
+    const float inv = 1.0f / (float)W;
+    float w[TL::NV][PER], bias[TL::NV][PER];  // kept for all rows of the workgroup
+#pragma unroll
+    for (int v = 0; v < TL::NV; ++v) {
+        const int i = (v * TL::TPR + t) * PER;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) w[v][e] = 1.0f, bias[v][e] = 0.0f;
+        if (c.w) ln_load<DT>(reinterpret_cast<const S *>(c.w), i, W, w[v]);
+        if (c.bias) ln_load<DT>(reinterpret_cast<const S *>(c.bias), i, W, bias[v]);
+    }
+    for (long long r0 = (long long)blockIdx.x * TL::ROWS; r0 < c.rows; r0 += (long long)gridDim.x * TL::ROWS) {
+        const long long r = r0 + threadIdx.x / TL::TPR;
+        const bool on = r < c.rows;  // every thread takes part in the sums
+        const S *x = reinterpret_cast<const S *>(c.x) + (on ? r : 0) * c.xs;
+        const S *res = c.res ? reinterpret_cast<const S *>(c.res) + (on ? r : 0) * c.rs : nullptr;
+        float z[TL::NV][PER], s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < TL::NV; ++v) ln_load<DT>(x, (v * TL::TPR + t) * PER, W, z[v]);
+        if (res) {
+            float y[TL::NV][PER];
+#pragma unroll
+            for (int v = 0; v < TL::NV; ++v) ln_load<DT>(res, (v * TL::TPR + t) * PER, W, y[v]);
+#pragma unroll
+            for (int v = 0; v < TL::NV; ++v)
+#pragma unroll
+                for (int e = 0; e < PER; ++e) z[v][e] = DT::to_f(round_to<DT>(z[v][e] + y[v][e]));
+        }
+#pragma unroll
+        for (int v = 0; v < TL::NV; ++v)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) s += z[v][e];
+        const float mean = row_sum<TL>(s, lds) * inv;
+        s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < TL::NV; ++v)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const float d = z[v][e] - mean;
+                if ((v * TL::TPR + t) * PER + e < W) s += d * d;
+            }
+        const float rstd = 1.0f / sqrtf(row_sum<TL>(s, lds) * inv + c.eps);
+        if (!on) continue;
+        if (t == 0) {
+            if (c.mean) c.mean[r] = mean;
+            if (c.rstd) c.rstd[r] = rstd;
+        }
+#pragma unroll
+        for (int v = 0; v < TL::NV; ++v) {
+            const int i = (v * TL::TPR + t) * PER;
+            if (c.sum) ln_store<DT>(reinterpret_cast<S *>(c.sum) + r * W, i, W, z[v]);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) z[v][e] = (z[v][e] - mean) * rstd * w[v][e] + bias[v][e];
+            ln_store<DT>(reinterpret_cast<S *>(c.y) + r * W, i, W, z[v]);
+        }
+    }
+}
+
+// dz, and the workgroup's own sums of dy u and dy over its rows, which stay in
+// registers until the last row: the weight gradients cost no second pass over
+// dy and z.
+template <class DT, class TL>
+__global__ __launch_bounds__(TL::THREADS) void k_ln_backward(LnBackward c) {
+    using S = typename DT::S;
+    constexpr int PER = TL::PER;
+    __shared__ float lds[16];
+    __shared__ float joint[TL::ROWS > 1 ? TL::ROWS * TL::WIDTH : 1];
+    const int W = c.width, t = threadIdx.x % TL::TPR, mine = threadIdx.x / TL::TPR;
+    const float inv = 1.0f / (float)W;
+    float w[TL::NV][PER], dw[TL::NV][PER], db[TL::NV][PER];
+#pragma unroll
+    for (int v = 0; v < TL::NV; ++v) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) w[v][e] = 1.0f, dw[v][e] = db[v][e] = 0.0f;
+        if (c.w) ln_load<DT>(reinterpret_cast<const S *>(c.w), (v * TL::TPR + t) * PER, W, w[v]);
+    }
+    for (long long r0 = (long long)blockIdx.x * TL::ROWS; r0 < c.rows; r0 += (long long)gridDim.x * TL::ROWS) {
+        const long long r = r0 + mine;
+        const bool on = r < c.rows;
+        const long long q = on ? r : 0;
+        const S *dy = reinterpret_cast<const S *>(c.dy) + q * c.ys, *z = reinterpret_cast<const S *>(c.z) + q * c.zs;
+        const S *ds = c.dsum ? reinterpret_cast<const S *>(c.dsum) + q * W : nullptr;
+        const float mean = c.mean[q], rstd = c.rstd[q];
+        float g[TL::NV][PER], u[TL::NV][PER], add[TL::NV][PER], s = 0.0f, su = 0.0f;
+#pragma unroll
+        for (int v = 0; v < TL::NV; ++v) {
+            const int i = (v * TL::TPR + t) * PER;
+            ln_load<DT>(dy, i, W, g[v]);
+            ln_load<DT>(z, i, W, u[v]);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) add[v][e] = 0.0f;
+            if (ds) ln_load<DT>(ds, i, W, add[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < TL::NV; ++v)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                u[v][e] = (u[v][e] - mean) * rstd;  // past the row's end: times a dy of 0
+                if (on) {
+                    dw[v][e] += g[v][e] * u[v][e];
+                    db[v][e] += g[v][e];
+                }
+                g[v][e] *= w[v][e];
+                s += g[v][e];
+                su += g[v][e] * u[v][e];
+            }
+        const float m = row_sum<TL>(s, lds) * inv, mu = row_sum<TL>(su, lds) * inv;
+        if (!on) continue;
+#pragma unroll
+        for (int v = 0; v < TL::NV; ++v) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) g[v][e] = rstd * (g[v][e] - m - u[v][e] * mu) + add[v][e];
+            ln_store<DT>(reinterpret_cast<S *>(c.dx) + r * W, (v * TL::TPR + t) * PER, W, g[v]);
+        }
+    }
+    if (!c.part) return;
+    float *part = c.part + (size_t)blockIdx.x * 2 * W;
+#pragma unroll
+    for (int k = 0; k < 2; ++k, part += W) {
+        if constexpr (TL::ROWS == 1) {
+#pragma unroll
+            for (int v = 0; v < TL::NV; ++v)
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const int i = (v * TL::TPR + t) * PER + e;
+                    if (i < W) part[i] = k ? db[v][e] : dw[v][e];
+                }
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < TL::NV; ++v)
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    joint[mine * TL::WIDTH + (v * TL::TPR + t) * PER + e] = k ? db[v][e] : dw[v][e];
+            __syncthreads();
+            for (int i = threadIdx.x; i < W; i += TL::THREADS) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < TL::ROWS; ++j) sum += joint[j * TL::WIDTH + i];
+                part[i] = sum;
+            }
+        }
+    }
+}
+
+// Rows too wide for the registers of a workgroup: read again for each sum.
+template <class DT>
+__global__ __launch_bounds__(256) void k_ln_forward_wide(LnForward c) {
     using S = typename DT::S;
     __shared__ float lds[4];
     const int W = c.width;
@@ -56,7 +267,7 @@ __global__ __launch_bounds__(256) void k_ln_forward(LnForward c) {
 }
 
 template <class DT>
-__global__ __launch_bounds__(256) void k_ln_dx(LnBackward c) {
+__global__ __launch_bounds__(256) void k_ln_dx_wide(LnBackward c) {
     using S = typename DT::S;
     __shared__ float lds[4];
     const int W = c.width;
@@ -83,7 +294,7 @@ __global__ __launch_bounds__(256) void k_ln_dx(LnBackward c) {
 
 // Workgroup p sums the rows p, p + parts, ... of every column.
 template <class DT>
-__global__ __launch_bounds__(256) void k_ln_dw(LnBackward c) {
+__global__ __launch_bounds__(256) void k_ln_dw_wide(LnBackward c) {
     using S = typename DT::S;
     const int W = c.width;
     for (int i = threadIdx.x; i < W; i += 256) {
@@ -99,41 +310,94 @@ __global__ __launch_bounds__(256) void k_ln_dw(LnBackward c) {
     }
 }
 
+// The workgroups' partial sums, in their order: 8 threads take every eighth of
+// a column's, then their sums are added.
 template <class DT>
 __global__ __launch_bounds__(256) void k_ln_join(LnBackward c, int parts) {
     using S = typename DT::S;
-    const int W = c.width, i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= W) return;
-    float w = 0.0f, b = 0.0f;
-    for (int p = 0; p < parts; ++p) {
-        w += c.part[(size_t)p * 2 * W + i];
-        b += c.part[((size_t)p * 2 + 1) * W + i];
-    }
-    if (c.dw) reinterpret_cast<S *>(c.dw)[i] = round_to<DT>(w);
-    if (c.db) reinterpret_cast<S *>(c.db)[i] = round_to<DT>(b);
+    __shared__ float lds[8][32];
+    const int W2 = 2 * c.width, x = threadIdx.x % 32, y = threadIdx.x / 32, i = blockIdx.x * 32 + x;
+    float sum = 0.0f;
+    if (i < W2)
+#pragma unroll 8
+        for (int p = y; p < parts; p += 8) sum += c.part[(size_t)p * W2 + i];
+    lds[y][x] = sum;
+    __syncthreads();
+    if (y > 0 || i >= W2) return;
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += lds[k][x];
+    S *out = reinterpret_cast<S *>(i < c.width ? c.dw : c.db);
+    if (out) out[i < c.width ? i : i - c.width] = round_to<DT>(sum);
+}
+
+// The smallest tile that a row fits: f(LnTile) for it, else wide().
+template <class DT, class F, class G>
+void ln_tile(int W, F f, G wide) {
+    constexpr int P = DT::PER16;
+    if (W <= 16 * P)
+        f(LnTile<DT, 16, 1>{});
+    else if (W <= 32 * P)
+        f(LnTile<DT, 16, 2>{});
+    else if (W <= 64 * P)
+        f(LnTile<DT, 64, 1>{});
+    else if (W <= 128 * P)
+        f(LnTile<DT, 64, 2>{});
+    else if (W <= 256 * P)
+        f(LnTile<DT, 64, 4>{});
+    else if (W <= 512 * P)
+        f(LnTile<DT, 256, 2>{});
+    else if (W <= 1024 * P)
+        f(LnTile<DT, 1024, 1>{});
+    else if (W <= 2048 * P)
+        f(LnTile<DT, 1024, 2>{});
+    else
+        wide();
+}
+
+unsigned blocks_of(long long rows, int per, long long most) {
+    const long long n = (rows + per - 1) / per;
+    return (unsigned)(n < most ? n : most);
+}
+
+template <class DT>
+hipError_t ln_forward(const LnForward &c, hipStream_t s) {
+    ln_tile<DT>(
+        c.width,
+        [&](auto tile) {
+            using TL = decltype(tile);
+            hipLaunchKernelGGL((k_ln_forward<DT, TL>), dim3(blocks_of(c.rows, TL::ROWS, 2048)), dim3(TL::THREADS), 0, s,
+                               c);
+        },
+        [&]() { hipLaunchKernelGGL(k_ln_forward_wide<DT>, dim3(blocks_of(c.rows, 1, 65536)), dim3(256), 0, s, c); });
+    return hipGetLastError();
 }
 
 template <class DT>
 hipError_t ln_backward(const LnBackward &c, hipStream_t s) {
-    const int parts = ln_parts(c.rows, c.width);
+    int parts = 0;
     if (c.rows > 0)
-        hipLaunchKernelGGL(k_ln_dx<DT>, dim3((unsigned)(c.rows < 65536 ? c.rows : 65536)), dim3(256), 0, s, c);
-    if (c.dw || c.db) {
-        if (parts) hipLaunchKernelGGL(k_ln_dw<DT>, dim3(parts), dim3(256), 0, s, c);
-        hipLaunchKernelGGL(k_ln_join<DT>, dim3((c.width + 255) / 256), dim3(256), 0, s, c, parts);
-    }
+        ln_tile<DT>(
+            c.width,
+            [&](auto tile) {
+                using TL = decltype(tile);
+                parts = (int)blocks_of(c.rows, TL::ROWS, ln_parts(c.rows, c.width));
+                hipLaunchKernelGGL((k_ln_backward<DT, TL>), dim3(parts), dim3(TL::THREADS), 0, s, c);
+            },
+            [&]() {
+                parts = ln_parts(c.rows, c.width);
+                hipLaunchKernelGGL(k_ln_dx_wide<DT>, dim3(blocks_of(c.rows, 1, 65536)), dim3(256), 0, s, c);
+                if (c.part) hipLaunchKernelGGL(k_ln_dw_wide<DT>, dim3(parts), dim3(256), 0, s, c);
+            });
+    if (c.dw || c.db)
+        hipLaunchKernelGGL(k_ln_join<DT>, dim3((2 * c.width + 31) / 32), dim3(256), 0, s, c, parts);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_ln_forward(const LnForward &c, hipStream_t s) {
-    const dim3 grid((unsigned)(c.rows < 65536 ? c.rows : 65536));
-    if (c.dtype == LSTM_BF16)
-        hipLaunchKernelGGL(k_ln_forward<BF16>, grid, dim3(256), 0, s, c);
-    else
-        hipLaunchKernelGGL(k_ln_forward<F32>, grid, dim3(256), 0, s, c);
-    return hipGetLastError();
+    return c.dtype == LSTM_BF16 ? ln_forward<BF16>(c, s) : ln_forward<F32>(c, s);
 }
 
 hipError_t launch_ln_backward(const LnBackward &c, hipStream_t s) {
