@@ -562,24 +562,61 @@ __global__ __launch_bounds__(256) void k_la_share(const float *part, LaOut o, in
     }
 }
 
-// One wave per 64 value columns of one (request, head).
-template <class DT>
-__global__ __launch_bounds__(64) void k_la_step(LaStep c) {
-    const int col = blockIdx.x * 64 + threadIdx.x, h = blockIdx.y % c.H, b = blockIdx.y / c.H;
-    if (col >= c.Dv) return;
+// One token.  The state is read and written once, which is all the time goes
+// into: a workgroup takes TX * VEC columns of one (request, head), TX lanes to
+// a row, and has RB rows a thread on their way before it needs the first.  o
+// is summed over a thread's rows, then over the row groups through LDS, in
+// fixed order.
+template <class DT, int VEC, int TX>
+__global__ __launch_bounds__(256) void k_la_step(LaStep c, int slabs) {
+    constexpr int TY = 256 / TX, RB = 16;
+    __shared__ float qs[256], ks[256], part[TY][TX * VEC];
+    const int tid = threadIdx.x, x = tid % TX, y = tid / TX;
+    const int slab = blockIdx.x % slabs, h = blockIdx.x / slabs % c.H, b = blockIdx.x / slabs / c.H;
+    const int col = (slab * TX + x) * VEC;
     const int slot = c.slots ? c.slots[b] : b;
-    float sum = 0.0f;
-    if (slot >= 0 && slot < c.n_slots) {
+    const bool live = slot >= 0 && slot < c.n_slots, on = live && col < c.Dv;  // VEC divides Dv
+    float o[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
+    if (live) {
         const float gamma = la_pow(la_log2(c.log_decay[h]), 1);
-        const float v = la_get<DT>(c.v, 0, b, h, col);
         float *s = c.pool + ((size_t)slot * c.H + h) * c.Dk * c.Dv + col;
-        for (int d = 0; d < c.Dk; ++d) {
-            const float x = s[(size_t)d * c.Dv] * gamma + la_get<DT>(c.k, 0, b, h, d) * v;
-            s[(size_t)d * c.Dv] = x;
-            sum += la_get<DT>(c.q, 0, b, h, d) * x;
+        float v[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = on ? la_get<DT>(c.v, 0, b, h, col + e) : 0.0f;
+        if (tid < c.Dk) {
+            qs[tid] = la_get<DT>(c.q, 0, b, h, tid);
+            ks[tid] = la_get<DT>(c.k, 0, b, h, tid);
+        }
+        for (int d0 = y; d0 < c.Dk || d0 == y; d0 += TY * RB) {
+            float st[RB][VEC];
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                if (on && d0 + r * TY < c.Dk) __builtin_memcpy(st[r], s + (size_t)(d0 + r * TY) * c.Dv, VEC * 4);
+            if (d0 == y) __syncthreads();  // q and k lie in LDS
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const int d = d0 + r * TY;
+                if (!on || d >= c.Dk) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    st[r][e] = st[r][e] * gamma + ks[d] * v[e];
+                    o[e] += qs[d] * st[r][e];
+                }
+                __builtin_memcpy(s + (size_t)d * c.Dv, st[r], VEC * 4);
+            }
         }
     }
-    la_put<DT>(c.o, 0, b, h, col, sum * c.scale);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) part[y][x * VEC + e] = o[e];
+    __syncthreads();
+    const int out = slab * TX * VEC + tid;
+    if (tid >= TX * VEC || out >= c.Dv) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < TY; ++k) sum += part[k][tid];
+    la_put<DT>(c.o, 0, b, h, out, sum * c.scale);
 }
 
 }  // namespace
@@ -655,12 +692,29 @@ hipError_t launch_la_share(const float *part, LaOut out, int T, int B, int H, in
     return hipGetLastError();
 }
 
-hipError_t launch_la_step(const LaStep &c, hipStream_t s) {
-    const dim3 grid((c.Dv + 63) / 64, c.B * c.H);
-    if (c.dtype == LSTM_BF16)
-        hipLaunchKernelGGL(k_la_step<BF16>, grid, dim3(64), 0, s, c);
+namespace {
+
+template <class DT, int VEC, int TX>
+void la_step_go(const LaStep &c, hipStream_t s) {
+    const int slabs = (c.Dv + TX * VEC - 1) / (TX * VEC);
+    hipLaunchKernelGGL((k_la_step<DT, VEC, TX>), dim3((unsigned)slabs * c.B * c.H), dim3(256), 0, s, c, slabs);
+}
+
+template <class DT>
+void la_step_any(const LaStep &c, hipStream_t s) {
+    // 16-byte accesses where rows allow them; narrow column slabs while there
+    // are fewer states than two for each CU
+    const bool vec = c.Dv % 4 == 0 && (uintptr_t)c.pool % 16 == 0, few = (long long)c.B * c.H < 512;
+    if (vec)
+        few || c.Dv <= 32 ? la_step_go<DT, 4, 8>(c, s) : la_step_go<DT, 4, 32>(c, s);
     else
-        hipLaunchKernelGGL(k_la_step<F32>, grid, dim3(64), 0, s, c);
+        la_step_go<DT, 1, 32>(c, s);
+}
+
+}  // namespace
+
+hipError_t launch_la_step(const LaStep &c, hipStream_t s) {
+    c.dtype == LSTM_BF16 ? la_step_any<BF16>(c, s) : la_step_any<F32>(c, s);
     return hipGetLastError();
 }
 
