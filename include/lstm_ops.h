@@ -29,9 +29,10 @@ extern "C" {
  * Query head h reads key/value head h / (heads / kv_heads). */
 
 /* A [T, B, heads, dim] tensor of the call's dtype: element strides of the
- * time, batch and head axes; the last axis is dense.  Any strides are taken
- * for an input (0 repeats it); an output must not overlap itself, which is
- * the caller's to keep.  Element addresses are 64-bit. */
+ * time, batch and head axes; the last axis is dense.  Any strides and any
+ * alignment are taken for an input (0 repeats it), the time stride below 2^31
+ * bytes; an output must not overlap itself, which is the caller's to keep.
+ * Addresses are 64-bit. */
 typedef struct {
     void *data;
     long long time, batch, head;
@@ -63,8 +64,10 @@ lstm_status lstm_linear_attention_backward_workspace_size(const lstm_linear_atte
  *   state_out    like state: the state after each row's last token, or NULL.
  *                It may be the memory of `state` (then updated in place).
  * LSTM_ERR_ARG: NULL argument, a dim outside 1..256, heads not a multiple of
- * kv_heads, a scale that is 0 or not finite; LSTM_ERR_SHAPE: T or B < 1, or
- * more than 2^31 - 1 chunks; LSTM_ERR_WORKSPACE: workspace too short. */
+ * kv_heads, a scale that is 0 or not finite; LSTM_ERR_SHAPE: T or B < 1, B *
+ * heads above 2^20, a time stride of 2^31 bytes; LSTM_ERR_WORKSPACE: workspace
+ * too short.  Sequences run in chunks of 32 tokens: a value that is not finite
+ * spoils its row's later outputs and may spoil earlier ones of its chunk. */
 lstm_status lstm_linear_attention_forward(const lstm_linear_attention_shape *shape, const lstm_view *q,
                                           const lstm_view *k, const lstm_view *v, const float *log_decay,
                                           const int *lengths, const float *state, const lstm_view *o,

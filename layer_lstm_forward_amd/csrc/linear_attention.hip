@@ -53,22 +53,23 @@ __device__ inline void la_put(const LaOut &o, int t, int b, int h, int d, float 
         reinterpret_cast<typename DT::S *>(o.p)[at] = round_to<DT>(v);
 }
 
-// N neighbouring columns of a token from element offset `at`, `left` of them in range.
-template <class DT, int N, class V>
-__device__ inline void la_write(const LaOut &o, long long at, V v, int left) {
-    if (left <= 0) return;
-    if (o.f32 || sizeof(typename DT::S) == 4) {
-        float *q = reinterpret_cast<float *>(o.p) + at;
-        if (left >= N)
+// N neighbouring columns of a token from element offset `at`; unless all are
+// known to be, `left` of them are in range.
+template <class DT, int N, bool ALL, class V>
+__device__ inline void la_write(char *o, bool f32, long long at, V v, int left) {
+    if (sizeof(typename DT::S) == 4 || f32) {
+        float *q = reinterpret_cast<float *>(o) + at;
+        if (ALL || left >= N)
             __builtin_memcpy(q, &v, sizeof(v));
         else
+#pragma unroll
             for (int x = 0; x < N; ++x)
                 if (x < left) q[x] = v[x];
     } else {
-        typename DT::S *q = reinterpret_cast<typename DT::S *>(o.p) + at, tmp[N];
+        typename DT::S *q = reinterpret_cast<typename DT::S *>(o) + at, tmp[N];
 #pragma unroll
         for (int x = 0; x < N; ++x) tmp[x] = round_to<DT>(v[x]);
-        if (left >= N)
+        if (ALL || left >= N)
             __builtin_memcpy(q, tmp, sizeof(tmp));
         else
 #pragma unroll
@@ -125,53 +126,78 @@ struct LaTile {
     }
 };
 
-// 16 bytes of row p at element d, zero past dim.  No alignment is assumed: the
-// hardware splits what is not aligned.
-template <class DT>
-__device__ inline u32x4 la_load(const typename DT::S *p, int d, int dim) {
-    using S = typename DT::S;
-    u32x4 v = {0, 0, 0, 0};
-    if (d + DT::PER16 <= dim) {
-        __builtin_memcpy(&v, p + d, 16);
-    } else if (d < dim) {
-        S tmp[DT::PER16];
-#pragma unroll
-        for (int e = 0; e < DT::PER16; ++e) tmp[e] = d + e < dim ? p[d + e] : (S)0;
-        v = __builtin_bit_cast(u32x4, tmp);
-    }
-    return v;
+// How a call's rows are read, by its dims (LaEdge).  No path branches around a
+// load (a branch makes the compiler wait for the load where the paths join):
+// tokens past the end read the last valid one again, whose weight is 0.
+//   WHOLE  every 16-byte piece of a tile lies in the row
+//   EDGES  a piece that reaches past the row's end is read further left, so
+//          that it ends with the row, and shifted into place (zeros follow)
+//   SHORT  a dim below one piece: element by element
+// No alignment is assumed: the hardware splits what is not aligned.
+enum LaEdge { WHOLE = 0, EDGES = 1, SHORT = 2 };
+
+// v shifted down by n bits (0..128, a multiple of the element's bits).
+__device__ inline u32x4 la_shift(u32x4 v, int n) {
+    const int w = n >> 5, b = n & 31;
+    const u32x4 x = w & 1 ? u32x4{v.y, v.z, v.w, 0} : v;
+    const u32x4 y = w & 2 ? u32x4{x.z, x.w, 0, 0} : x;
+    const u32x4 z = w & 4 ? u32x4{0, 0, 0, 0} : y;
+    return u32x4{__builtin_amdgcn_alignbit(z.y, z.x, b), __builtin_amdgcn_alignbit(z.z, z.y, b),
+                 __builtin_amdgcn_alignbit(z.w, z.z, b), z.w >> b};
 }
 
 // Tokens of one tensor on their way from memory to LDS: piece p of a thread is
 // row tid / R + p * (THREADS / R), 16-byte piece tid % R.
-template <class DT, class TL, int R, int P>
+template <class DT, class TL, int R, int P, int EDGE>
 struct LaStage {
-    const typename DT::S *base;  // the thread's first row
-    long long step;              // elements between tokens, signed by direction
-    int row, piece, dim;
+    using S = typename DT::S;
+    static constexpr int RS = TL::THREADS / R;
+    const char *base;  // the row's first token in the pass's order
+    int step;          // bytes between tokens, signed by direction
+    int row, piece, off, shift, dim;
     u32x4 v[P];
 
     __device__ void init(const LaTensor &x, int b, int h, int t0, int dir, int d0, int dim_) {
         row = threadIdx.x / R;
         piece = threadIdx.x % R;
         dim = dim_ - d0;
-        step = x.t * dir;
-        base = reinterpret_cast<const typename DT::S *>(x.p) + (long long)t0 * x.t + (long long)b * x.b +
-               (long long)(h / x.hdiv) * x.h + d0 + row * step;
-    }
-    // tokens i0.. of which n are valid
-    __device__ void load(int i0, int n) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            constexpr int RS = TL::THREADS / R;
-            v[p] = u32x4{0, 0, 0, 0};
-            if (row + p * RS < n) v[p] = la_load<DT>(base + (i0 + p * RS) * step, piece * TL::PER, dim);
+        step = (int)(x.t * (long long)sizeof(S)) * dir;
+        base = x.p + ((long long)t0 * x.t + (long long)b * x.b + (long long)(h / x.hdiv) * x.h + d0) *
+                         (long long)sizeof(S);
+        const int d = piece * TL::PER, rest = dim - d;
+        off = d * (int)sizeof(S);
+        shift = 0;
+        if (EDGE == EDGES && rest < TL::PER) {
+            off = (dim - TL::PER) * (int)sizeof(S);
+            shift = rest > 0 ? (TL::PER - rest) * 8 * (int)sizeof(S) : 128;
         }
     }
-    __device__ void store(typename DT::S *lds) const {
+    // tokens i0.. of which n >= 1 are valid
+    __device__ void load(int i0, int n) {
+        const char *at = base + (long long)i0 * step;
+        if (EDGE != SHORT) at += off;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const char *q = at + (long long)min(row + p * RS, n - 1) * step;
+            if constexpr (EDGE != SHORT) {
+                __builtin_memcpy(&v[p], q, 16);
+            } else {
+                S tmp[TL::PER];
+#pragma unroll
+                for (int e = 0; e < TL::PER; ++e) {
+                    const int d = piece * TL::PER + e;
+                    const S x = reinterpret_cast<const S *>(q)[max(min(d, dim - 1), 0)];
+                    tmp[e] = d < dim ? x : (S)0;
+                }
+                v[p] = __builtin_bit_cast(u32x4, tmp);
+            }
+        }
+    }
+    __device__ void store(S *lds) const {
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            *reinterpret_cast<u32x4 *>(lds + TL::template at<R>(row + p * (TL::THREADS / R), piece)) = v[p];
+            *reinterpret_cast<u32x4 *>(lds + TL::template at<R>(row + p * RS, piece)) =
+                EDGE == EDGES ? la_shift(v[p], shift) : v[p];
     }
 };
 
@@ -292,7 +318,7 @@ __device__ inline size_t la_seg_at(const LaCall &c, const LaWhere &w, int slabs,
     return (((row * slabs + w.slab) * TL::NW + wave) * (TL::AT * TL::NT) * 64 + lane) * 4;
 }
 
-template <class DT, class TL, bool STATE_ONLY>
+template <class DT, class TL, int EDGE, bool STATE_ONLY>
 __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     using S_t = typename DT::S;
     __shared__ __align__(16) S_t tiles[TL::BUFS][TL::ELEMS];
@@ -330,8 +356,14 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
         }
     }
 
-    LaStage<DT, TL, TL::RA, TL::PA> sa, sb;
-    LaStage<DT, TL, TL::RC, TL::PC> sc;
+    LaStage<DT, TL, TL::RA, TL::PA, EDGE> sa, sb;
+    LaStage<DT, TL, TL::RC, TL::PC, EDGE> sc;
+    const bool keep = p.s1 && !p.seg, f32 = p.o.f32;
+    const float out_scale = p.out_scale;
+    const long long ot = p.o.t * dir;
+    char *const out = p.o.p;
+    const long long o0 = (long long)first * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h + col0;
+    const int cols = p.dc - col0;
     if (!STATE_ONLY) sa.init(p.a, at.b, at.h, first, dir, 0, p.da);
     sb.init(p.b, at.b, at.h, first, dir, 0, p.da);
     sc.init(p.c, at.b, at.h, first, dir, slab0, p.dc);
@@ -422,7 +454,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                     cf[t][ju] = la_cols<DT, TL, TL::RC>(
                         lc, ju, [&](int x) { return wave * 16 * TL::NT + TL::col_of(t, 4 * x); }, lane);
             // the state after the chunk, unless nothing reads it
-            if (STATE_ONLY || more || (p.s1 && !p.seg)) {
+            if (STATE_ONLY || more || keep) {
                 LaWeighted<DT, TL> cw;
                 cw.make(cf, g2, n, e, lane);
                 const float whole = la_pow(g2, n);
@@ -459,19 +491,17 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                     }
                     const int row = TL::row_of(it, m / 4, m % 4);
                     if (row >= n) continue;
-                    const long long tok = first + (long long)dir * (i + row);
-                    const long long o = tok * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h;
+                    const long long o = o0 + (long long)(i + row) * ot;
 #pragma unroll
-                    for (int t = 0; t < TL::NT; ++t) O[it][t] *= p.out_scale;
+                    for (int t = 0; t < TL::NT; ++t) O[it][t] *= out_scale;
                     if constexpr (TL::TPK == 2 && TL::NT == 2) {  // 8 neighbouring columns
-                        const int col = col0 + 8 * g;
                         const f32x8 v = __builtin_shufflevector(O[it][0], O[it][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                        la_write<DT, 8>(p.o, o + col, v, p.dc - col);
+                        la_write<DT, 8, EDGE == WHOLE>(out, f32, o + 8 * g, v, cols - 8 * g);
                     } else {
 #pragma unroll
                         for (int t = 0; t < TL::NT; ++t) {
-                            const int col = col0 + 16 * t + 4 * g;
-                            la_write<DT, 4>(p.o, o + col, O[it][t], p.dc - col);
+                            const int col = 16 * t + 4 * g;
+                            la_write<DT, 4, EDGE == WHOLE>(out, f32, o + col, O[it][t], cols - col);
                         }
                     }
                 }
@@ -488,7 +518,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 #pragma unroll
         for (int x = 0; x < TL::AT * TL::NT; ++x) *reinterpret_cast<f32x4 *>(dst + x * 256) = S[x];
     } else {
-        if (p.s1 && !p.seg) {
+        if (keep) {
             float *dst = p.s1 + ((size_t)at.b * c.H + at.h) * p.da * p.dc;
 #pragma unroll
             for (int t = 0; t < TL::AT; ++t)
@@ -636,19 +666,30 @@ LaPlan la_plan(int da, int dc) {
     return t;
 }
 
+template <class DT, class TL, int EDGE>
+hipError_t la_launch(const LaCall &c, int slabs, hipStream_t s) {
+    const long long blocks = (long long)slabs * c.npass * c.H * c.B * c.nseg;
+    if (blocks > 0xFFFFFFFFll / TL::THREADS) return hipErrorInvalidValue;
+    if (c.nseg > 1) {
+        hipLaunchKernelGGL((k_la<DT, TL, EDGE, true>), dim3((unsigned)blocks), dim3(TL::THREADS), 0, s, c, slabs);
+        const size_t n = (size_t)c.B * c.H * slabs * TL::NW * TL::AT * TL::NT * 64;
+        hipLaunchKernelGGL((k_la_join<DT, TL>), dim3((unsigned)((n + 255) / 256), c.npass), dim3(256), 0, s, c, slabs);
+    }
+    hipLaunchKernelGGL((k_la<DT, TL, EDGE, false>), dim3((unsigned)blocks), dim3(TL::THREADS), 0, s, c, slabs);
+    return hipGetLastError();
+}
+
 template <class DT, int DA, int NW>
 hipError_t la_go(const LaCall &c, int dc, hipStream_t s) {
     using TL = LaTile<DT, DA, NW>;
     const int slabs = (dc + TL::COLS - 1) / TL::COLS;
-    const long long blocks = (long long)slabs * c.npass * c.H * c.B * c.nseg;
-    if (blocks > 0x7FFFFFFF / TL::THREADS) return hipErrorInvalidValue;
-    if (c.nseg > 1) {
-        hipLaunchKernelGGL((k_la<DT, TL, true>), dim3((unsigned)blocks), dim3(TL::THREADS), 0, s, c, slabs);
-        const size_t n = (size_t)c.B * c.H * slabs * NW * TL::AT * TL::NT * 64;
-        hipLaunchKernelGGL((k_la_join<DT, TL>), dim3((unsigned)((n + 255) / 256), c.npass), dim3(256), 0, s, c, slabs);
+    bool whole = true, pieces = true;
+    for (int i = 0; i < c.npass; ++i) {
+        whole = whole && c.pass[i].da == DA && c.pass[i].dc % TL::COLS == 0 && c.pass[i].dc == dc;
+        pieces = pieces && c.pass[i].da >= TL::PER && c.pass[i].dc >= TL::PER;
     }
-    hipLaunchKernelGGL((k_la<DT, TL, false>), dim3((unsigned)blocks), dim3(TL::THREADS), 0, s, c, slabs);
-    return hipGetLastError();
+    return whole ? la_launch<DT, TL, WHOLE>(c, slabs, s)
+                 : pieces ? la_launch<DT, TL, EDGES>(c, slabs, s) : la_launch<DT, TL, SHORT>(c, slabs, s);
 }
 
 template <class DT>

@@ -16,6 +16,8 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int kMaxDim = 256;
+constexpr long long kMaxRows = 1 << 20;  // (batch row, head) pairs
+
 
 size_t elem(int dtype) { return dtype == LSTM_BF16 ? 2 : 4; }
 
@@ -48,12 +50,18 @@ lstm_status check_shape(const lstm_linear_attention_shape *s) {
     if (s->key_dim < 1 || s->value_dim < 1 || s->key_dim > kMaxDim || s->value_dim > kMaxDim) return LSTM_ERR_ARG;
     if (!std::isfinite(s->scale) || s->scale == 0.0f) return LSTM_ERR_ARG;
     if (s->T < 1 || s->B < 1) return LSTM_ERR_SHAPE;
-    // rows * columns of a grid, and the fp32 partial sums' index, stay in range
-    if ((long long)s->B * s->heads > INT_MAX / 64) return LSTM_ERR_SHAPE;
+    // a grid of 2^32 threads holds every workgroup of three passes
+    if ((long long)s->B * s->heads > kMaxRows) return LSTM_ERR_SHAPE;
     return LSTM_OK;
 }
 
 bool view_ok(const lstm_view *v) { return v && v->data; }
+
+// Token to token the kernels step by 32-bit byte counts.
+bool steps_ok(const lstm_linear_attention_shape *s, const lstm_view *v) {
+    const long long most = INT_MAX / (long long)elem(s->dtype);
+    return v->time >= -most && v->time <= most;
+}
 
 // Every pointer of the list that is given lies on the device.
 bool all_on_device(const void *const *p, int n, int dev) {
@@ -124,6 +132,7 @@ lstm_status lstm_linear_attention_forward(const lstm_linear_attention_shape *s, 
     lstm_status rc = check_shape(s);
     if (rc != LSTM_OK) return rc;
     if (!view_ok(q) || !view_ok(k) || !view_ok(v) || !view_ok(o) || !log_decay) return LSTM_ERR_ARG;
+    if (!steps_ok(s, q) || !steps_ok(s, k) || !steps_ok(s, v)) return LSTM_ERR_SHAPE;
     LaLayout lay;
     if (!la_layout(s, false, &lay)) return LSTM_ERR_SHAPE;
     if (lay.total && (!workspace || workspace_bytes < lay.total)) return LSTM_ERR_WORKSPACE;
@@ -161,6 +170,7 @@ lstm_status lstm_linear_attention_backward(const lstm_linear_attention_shape *s,
     if (!view_ok(q) || !view_ok(k) || !view_ok(v) || !view_ok(do_) || !view_ok(dq) || !view_ok(dk) || !view_ok(dv) ||
         !log_decay)
         return LSTM_ERR_ARG;
+    if (!steps_ok(s, q) || !steps_ok(s, k) || !steps_ok(s, v) || !steps_ok(s, do_)) return LSTM_ERR_SHAPE;
     LaLayout lay;
     if (!la_layout(s, true, &lay)) return LSTM_ERR_SHAPE;
     if (lay.total && (!workspace || workspace_bytes < lay.total)) return LSTM_ERR_WORKSPACE;
