@@ -98,10 +98,14 @@ struct LaTile {
     static constexpr int RA = DA / PER, RC = COLS / PER;       // 16-byte pieces of a row in LDS
     static constexpr int PA = C * RA / THREADS, PC = C * RC / THREADS;  // pieces a thread moves
     static constexpr int ELEMS = C * (2 * DA + COLS);          // a chunk's three tensors in LDS
-    static constexpr int PT = 4 / NW;                          // tiles of A B^T a wave computes
     static constexpr int P_ELEMS = C * C;                      // and its (A B^T) . W
-    // a second LDS buffer (one barrier less a chunk) where 8 waves still fit a CU's 160 KB
-    static constexpr int BUFS = 2 * (ELEMS + P_ELEMS) * (int)sizeof(typename DT::S) * (8 / NW) <= 160 * 1024 ? 2 : 1;
+    static constexpr int PT = 4 / NW;                          // tiles of A B^T a wave computes
+    // LDS of a workgroup such that 8 waves share a CU's 160 KB, in chunks
+    static constexpr int FIT = (160 * 1024 * NW / 8 / (int)sizeof(typename DT::S) - P_ELEMS) / ELEMS;
+    // chunk buffers where the loads go through registers (a second one saves a barrier a chunk) ...
+    static constexpr int BUFS = FIT >= 2 ? 2 : 1;
+    // ... and where they write to LDS themselves, two chunks ahead of the products if it fits
+    static constexpr int RING = FIT >= 3 ? 3 : 2;
     static_assert(C * RA % THREADS == 0 && C * RC % THREADS == 0 && THREADS % RA == 0 && THREADS % RC == 0, "tile");
 
     // row (of the 16-row tile `tile`) that accumulator row 4g + r stands for
@@ -134,7 +138,8 @@ struct LaTile {
 //          that it ends with the row, and shifted into place (zeros follow)
 //   SHORT  a dim below one piece: element by element
 // No alignment is assumed: the hardware splits what is not aligned.
-enum LaEdge { WHOLE = 0, EDGES = 1, SHORT = 2 };
+//   DIRECT_LDS  as WHOLE, bf16, rows 16-byte aligned: loads that write to LDS
+enum LaEdge { WHOLE = 0, EDGES = 1, SHORT = 2, DIRECT_LDS = 3 };
 
 // v shifted down by n bits (0..128, a multiple of the element's bits).
 __device__ inline u32x4 la_shift(u32x4 v, int n) {
@@ -200,6 +205,69 @@ struct LaStage {
                 EDGE == EDGES ? la_shift(v[p], shift) : v[p];
     }
 };
+
+// The same without registers between: each wave's load writes 64 pieces of 16
+// bytes to consecutive LDS places, so the place decides which piece of which
+// row a lane fetches.  Block w + NW * i of a tensor's pieces is wave w's load i.
+// Needs whole pieces, 16-byte alignment and rows of a chunk within 32-bit
+// offsets of each other.
+template <class DT, class TL, int R>
+struct LaDirect {
+    using S = typename DT::S;
+    static constexpr int N = TL::C * R / 64 / TL::NW;  // loads of a wave
+    const char *base;
+    int step;
+    unsigned full[N];  // offsets of a chunk of C valid tokens
+
+    __device__ unsigned offset(int i, int n) const {
+        const int at = ((threadIdx.x / 64 + TL::NW * i) * 64 + threadIdx.x % 64), j = at / R;
+        const unsigned piece = (at % R) ^ TL::template key<R>(j);
+        const int k = min(j, n - 1);  // past the end: the last token again, whose weight is 0
+        return (unsigned)(step >= 0 ? k : n - 1 - k) * (unsigned)abs(step) + piece * 16u;
+    }
+    __device__ void init(const LaTensor &x, int b, int h, int t0, int dir, int d0) {
+        step = (int)(x.t * (long long)sizeof(S)) * dir;
+        base = x.p + ((long long)t0 * x.t + (long long)b * x.b + (long long)(h / x.hdiv) * x.h + d0) *
+                         (long long)sizeof(S);
+#pragma unroll
+        for (int i = 0; i < N; ++i) full[i] = offset(i, TL::C);
+    }
+    __device__ void load(S *lds, int i0, int n) const {
+        const long long low = (long long)(step >= 0 ? i0 : i0 + n - 1) * step;
+        const uint64_t p = (uint64_t)(base + low);
+        u32x4 r = {(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, 0xFFFFFFFFu, 0x00020000u};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) r[x] = (uint32_t)__builtin_amdgcn_readfirstlane((int)r[x]);
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const unsigned o = n == TL::C ? full[i] : offset(i, n);
+            const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) S *)lds +
+                                (wave + TL::NW * i) * 1024;
+            // As the builtin for it, but unknown to the compiler's counting:
+            // with the builtin it waits for every load under way before the
+            // next transposed LDS read.  The waits are la_barrier's.  Nothing
+            // else here reads m0 (it is reserved: the compiler keeps no value
+            // in it).
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                         :
+                         : "s"(to), "v"(o), "s"(r)
+                         : "memory");
+        }
+    }
+};
+
+// Waits until at most VM of this wave's memory operations and none of its LDS
+// operations are under way, then for the other waves.  (The fence of
+// __syncthreads would wait for the loads of later chunks too.)
+template <int VM>
+__device__ inline void la_barrier() {
+    static_assert(VM < 64, "vmcnt field");
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
 
 // Fragment of rows: lane (m, g) gets row tile_row(m), values KC*u + PER*g ...
 template <class DT, class TL, int R>
@@ -321,8 +389,10 @@ __device__ inline size_t la_seg_at(const LaCall &c, const LaWhere &w, int slabs,
 template <class DT, class TL, int EDGE, bool STATE_ONLY>
 __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     using S_t = typename DT::S;
-    __shared__ __align__(16) S_t tiles[TL::BUFS][TL::ELEMS];
-    __shared__ __align__(16) S_t Ps[STATE_ONLY ? 1 : TL::BUFS][2 * TL::JU][64][TL::PER];  // fragments [it][ju] of (A B^T) . W
+    constexpr bool DIRECT = EDGE == DIRECT_LDS;
+    constexpr int BUFS = DIRECT ? TL::RING : TL::BUFS;
+    __shared__ __align__(1024) S_t tiles[BUFS][TL::ELEMS];
+    __shared__ __align__(16) S_t ps[STATE_ONLY ? 1 : 2 * TL::JU][64][TL::PER];  // fragments [it][ju] of (A B^T) . W
     const LaWhere at = la_where(c, slabs);
     const LaPass &p = c.pass[at.pass];
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, m = lane % 16, g = lane / 16;
@@ -333,6 +403,55 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     const int slab0 = at.slab * TL::COLS, col0 = slab0 + wave * 16 * TL::NT;
     const bool busy = col0 < p.dc;  // else the wave only moves data and takes its part in A B^T
 
+    const bool keep = p.s1 && !p.seg, f32 = p.o.f32;
+    const float out_scale = p.out_scale;
+    const long long ot = p.o.t * dir;
+    char *const out = p.o.p;
+    const long long o0 = (long long)first * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h + col0;
+    const int cols = p.dc - col0;
+    // where a chunk's tensors lie in its buffer
+    constexpr int AT_B = TL::C * TL::DA, AT_C = 2 * TL::C * TL::DA;
+    LaStage<DT, TL, TL::RA, TL::PA, EDGE> sa, sb;
+    LaStage<DT, TL, TL::RC, TL::PC, EDGE> sc;
+    LaDirect<DT, TL, TL::RA> da, db;
+    LaDirect<DT, TL, TL::RC> dc;
+    constexpr int LOADS = (STATE_ONLY ? 1 : 2) * LaDirect<DT, TL, TL::RA>::N + LaDirect<DT, TL, TL::RC>::N;
+    if constexpr (DIRECT) {
+        if (!STATE_ONLY) da.init(p.a, at.b, at.h, first, dir, 0);
+        db.init(p.b, at.b, at.h, first, dir, 0);
+        dc.init(p.c, at.b, at.h, first, dir, slab0);
+    } else {
+        if (!STATE_ONLY) sa.init(p.a, at.b, at.h, first, dir, 0, p.da);
+        sb.init(p.b, at.b, at.h, first, dir, 0, p.da);
+        sc.init(p.c, at.b, at.h, first, dir, slab0, p.dc);
+    }
+    auto issue = [&](int i, int buf) {  // DIRECT: chunk i into its buffer
+        const int n = min(TL::C, i1 - i);
+        S_t *t = tiles[buf];
+        if (!STATE_ONLY) da.load(t, i, n);
+        db.load(t + AT_B, i, n);
+        dc.load(t + AT_C, i, n);
+    };
+    auto fetch = [&](int i) {  // else: into registers,
+        const int n = i1 - i;
+        if (!STATE_ONLY) sa.load(i, n);
+        sb.load(i, n);
+        sc.load(i, n);
+    };
+    auto put = [&](S_t *t) {  // and from there
+        if (!STATE_ONLY) sa.store(t);
+        sb.store(t + AT_B);
+        sc.store(t + AT_C);
+    };
+    if (i0 < i1) {
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int k = 0; k < TL::RING - 1; ++k)
+                if (i0 + k * TL::C < i1) issue(i0 + k * TL::C, k);
+        } else {
+            fetch(i0);
+        }
+    }
     f32x4 S[TL::AT * TL::NT];
 #pragma unroll
     for (int x = 0; x < TL::AT * TL::NT; ++x) S[x] = f32x4{0, 0, 0, 0};
@@ -355,45 +474,50 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                     }
         }
     }
-
-    LaStage<DT, TL, TL::RA, TL::PA, EDGE> sa, sb;
-    LaStage<DT, TL, TL::RC, TL::PC, EDGE> sc;
-    const bool keep = p.s1 && !p.seg, f32 = p.o.f32;
-    const float out_scale = p.out_scale;
-    const long long ot = p.o.t * dir;
-    char *const out = p.o.p;
-    const long long o0 = (long long)first * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h + col0;
-    const int cols = p.dc - col0;
-    if (!STATE_ONLY) sa.init(p.a, at.b, at.h, first, dir, 0, p.da);
-    sb.init(p.b, at.b, at.h, first, dir, 0, p.da);
-    sc.init(p.c, at.b, at.h, first, dir, slab0, p.dc);
-    auto fetch = [&](int i) {
-        const int n = i1 - i;
-        if (!STATE_ONLY) sa.load(i, n);
-        sb.load(i, n);
-        sc.load(i, n);
-    };
-    auto put = [&](S_t *t) {
-        if (!STATE_ONLY) sa.store(t);
-        sb.store(t + TL::C * TL::DA);
-        sc.store(t + 2 * TL::C * TL::DA);
-    };
-    if (i0 < i1) {
-        fetch(i0);
-        put(tiles[0]);
-    }
+    if (!DIRECT && i0 < i1) put(tiles[0]);
 
     int buf = 0;
+    f32x4 O[2][TL::NT];
+    // O's columns of its 2 x 16 tokens, out of chunk i of n tokens
+    auto flush = [&](int i, int n) {
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+            const int row = TL::row_of(it, m / 4, m % 4);
+            if (row >= n) continue;
+            const long long o = o0 + (long long)(i + row) * ot;
+            if constexpr (TL::TPK == 2 && TL::NT == 2) {  // 8 neighbouring columns
+                const f32x8 v = __builtin_shufflevector(O[it][0], O[it][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                la_write<DT, 8, EDGE == WHOLE || DIRECT>(out, f32, o + 8 * g, v, cols - 8 * g);
+            } else {
+#pragma unroll
+                for (int t = 0; t < TL::NT; ++t) {
+                    const int col = 16 * t + 4 * g;
+                    la_write<DT, 4, EDGE == WHOLE || DIRECT>(out, f32, o + col, O[it][t], cols - col);
+                }
+            }
+        }
+    };
     for (int i = i0; i < i1; i += TL::C) {
         const int n = min(TL::C, i1 - i);
         const bool more = i + TL::C < i1;
-        if (more) fetch(i + TL::C);
-        __syncthreads();  // this chunk lies in LDS
-        const S_t *la = tiles[buf], *lb = la + TL::C * TL::DA, *lc = lb + TL::C * TL::DA;
+        if constexpr (DIRECT) {
+            // this chunk lies in LDS once at most the later chunk's loads are
+            // under way (the stores of the chunk before last come before them)
+            if (TL::RING > 2 && more)
+                la_barrier<LOADS *(TL::RING - 2)>();
+            else
+                la_barrier<0>();
+            if (!STATE_ONLY && i > i0 && busy) flush(i - TL::C, TL::C);
+            const int next = i + (TL::RING - 1) * TL::C;
+            if (next < i1) issue(next, buf == 0 ? TL::RING - 1 : buf - 1);
+        } else {
+            if (more) fetch(i + TL::C);
+            __syncthreads();  // this chunk lies in LDS
+        }
+        const S_t *la = tiles[buf], *lb = la + AT_B, *lc = la + AT_C;
 
         // This wave's tiles of B A^T (rows: tokens j), weighted, as parts of
         // the fragments that the product with Cv reads.
-        S_t(*ps)[64][TL::PER] = Ps[STATE_ONLY ? 0 : buf];
         if constexpr (!STATE_ONLY) {
 #pragma unroll
             for (int x = 0; x < TL::PT; ++x) {
@@ -418,7 +542,6 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
             }
         }
 
-        f32x4 O[2][TL::NT];
         u32x4 cf[TL::NT][TL::JU];
         if (busy) {
             if constexpr (!STATE_ONLY) {
@@ -478,7 +601,11 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
         }
 
         if constexpr (!STATE_ONLY) {
-            __syncthreads();  // the fragments of (A B^T) . W lie in LDS
+            // the fragments of (A B^T) . W lie in LDS
+            if constexpr (DIRECT)
+                la_barrier<63>();
+            else
+                __syncthreads();
             if (busy) {
 #pragma unroll
                 for (int it = 0; it < 2; ++it) {
@@ -489,27 +616,19 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 #pragma unroll
                         for (int t = 0; t < TL::NT; ++t) O[it][t] = mma_chunk(DT{}, O[it][t], cf[t][ju], pf);
                     }
-                    const int row = TL::row_of(it, m / 4, m % 4);
-                    if (row >= n) continue;
-                    const long long o = o0 + (long long)(i + row) * ot;
 #pragma unroll
                     for (int t = 0; t < TL::NT; ++t) O[it][t] *= out_scale;
-                    if constexpr (TL::TPK == 2 && TL::NT == 2) {  // 8 neighbouring columns
-                        const f32x8 v = __builtin_shufflevector(O[it][0], O[it][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                        la_write<DT, 8, EDGE == WHOLE>(out, f32, o + 8 * g, v, cols - 8 * g);
-                    } else {
-#pragma unroll
-                        for (int t = 0; t < TL::NT; ++t) {
-                            const int col = 16 * t + 4 * g;
-                            la_write<DT, 4, EDGE == WHOLE>(out, f32, o + col, O[it][t], cols - col);
-                        }
-                    }
                 }
+                // DIRECT: the stores wait for the next chunk, behind whose
+                // barrier they precede loads that nobody waits for yet
+                if (!DIRECT || !more) flush(i, n);
             }
         }
-        if (TL::BUFS == 1 && more) __syncthreads();  // the chunk has been read
-        if (more) put(tiles[TL::BUFS == 2 ? buf ^ 1 : 0]);
-        if (TL::BUFS == 2) buf ^= 1;
+        if constexpr (!DIRECT) {
+            if (BUFS == 1 && more) __syncthreads();  // the chunk has been read
+            if (more) put(tiles[BUFS == 2 ? buf ^ 1 : 0]);
+        }
+        buf = buf + 1 < BUFS ? buf + 1 : 0;
     }
 
     if (!busy) return;
@@ -679,6 +798,12 @@ hipError_t la_launch(const LaCall &c, int slabs, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Every row begins on 16 bytes, and a chunk's rows lie within 32-bit offsets.
+bool la_aligned(const LaTensor &x) {
+    return (uintptr_t)x.p % 16 == 0 && x.t % 8 == 0 && x.b % 8 == 0 && x.h % 8 == 0 && x.t < (1 << 25) &&
+           x.t > -(1 << 25);
+}
+
 template <class DT, int DA, int NW>
 hipError_t la_go(const LaCall &c, int dc, hipStream_t s) {
     using TL = LaTile<DT, DA, NW>;
@@ -687,6 +812,13 @@ hipError_t la_go(const LaCall &c, int dc, hipStream_t s) {
     for (int i = 0; i < c.npass; ++i) {
         whole = whole && c.pass[i].da == DA && c.pass[i].dc % TL::COLS == 0 && c.pass[i].dc == dc;
         pieces = pieces && c.pass[i].da >= TL::PER && c.pass[i].dc >= TL::PER;
+    }
+    if constexpr (TL::TPK == 2) {
+        bool direct = whole;
+        for (int i = 0; i < c.npass; ++i)
+            direct = direct && la_aligned(c.pass[i].a) && la_aligned(c.pass[i].b) && la_aligned(c.pass[i].c);
+        if (direct) return la_launch<DT, TL, DIRECT_LDS>(c, slabs, s);
+        whole = false;
     }
     return whole ? la_launch<DT, TL, WHOLE>(c, slabs, s)
                  : pieces ? la_launch<DT, TL, EDGES>(c, slabs, s) : la_launch<DT, TL, SHORT>(c, slabs, s);
