@@ -99,9 +99,13 @@ struct LaTile {
     static constexpr int PA = C * RA / THREADS, PC = C * RC / THREADS;  // pieces a thread moves
     static constexpr int ELEMS = C * (2 * DA + COLS);          // a chunk's three tensors in LDS
     static constexpr int P_ELEMS = C * C;                      // and its (A B^T) . W
+    // 32 rows of S pass through a chunk's buffer on their way from and to memory
+    static constexpr int LD = COLS + 4;                        // floats of such a row
+    static constexpr int ROWS_ELEMS = 32 * LD * 4 / (int)sizeof(typename DT::S);
+    static constexpr int BUF_ELEMS = ELEMS > ROWS_ELEMS ? ELEMS : (ROWS_ELEMS + 511) / 512 * 512;
     static constexpr int PT = 4 / NW;                          // tiles of A B^T a wave computes
     // LDS of a workgroup such that 8 waves share a CU's 160 KB, in chunks
-    static constexpr int FIT = (160 * 1024 * NW / 8 / (int)sizeof(typename DT::S) - P_ELEMS) / ELEMS;
+    static constexpr int FIT = (160 * 1024 * NW / 8 / (int)sizeof(typename DT::S) - P_ELEMS) / BUF_ELEMS;
     // chunk buffers where the loads go through registers (a second one saves a barrier a chunk) ...
     static constexpr int BUFS = FIT >= 2 ? 2 : 1;
     // ... and where they write to LDS themselves, two chunks ahead of the products if it fits
@@ -391,7 +395,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     using S_t = typename DT::S;
     constexpr bool DIRECT = EDGE == DIRECT_LDS;
     constexpr int BUFS = DIRECT ? TL::RING : TL::BUFS;
-    __shared__ __align__(1024) S_t tiles[BUFS][TL::ELEMS];
+    __shared__ __align__(1024) S_t tiles[BUFS][TL::BUF_ELEMS];
     __shared__ __align__(16) S_t ps[STATE_ONLY ? 1 : 2 * TL::JU][64][TL::PER];  // fragments [it][ju] of (A B^T) . W
     const LaWhere at = la_where(c, slabs);
     const LaPass &p = c.pass[at.pass];
@@ -455,23 +459,63 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     f32x4 S[TL::AT * TL::NT];
 #pragma unroll
     for (int x = 0; x < TL::AT * TL::NT; ++x) S[x] = f32x4{0, 0, 0, 0};
-    if (!STATE_ONLY && busy) {
+    // S from and to memory: 32 rows at a time through LDS, so that lanes take
+    // neighbouring addresses (each lane fetching its own rows and columns took
+    // 1.2 TB/s).  The matrix may lie transposed (srow = 1).
+    constexpr int PART = 8 * TL::NT;  // elements of 32 rows that a thread moves
+    float *const rows32 = reinterpret_cast<float *>(tiles[BUFS - 1]);
+    auto place = [&](int y, int *row, int *col) {
+        const int x = y * TL::THREADS + tid;
+        *row = p.srow == 1 ? x % 32 : x / TL::COLS;
+        *col = p.srow == 1 ? x / 32 : x % TL::COLS;
+    };
+    const size_t own = ((size_t)at.b * c.H + at.h) * p.da * p.dc;
+    if constexpr (!STATE_ONLY) {
         if (p.seg) {
-            const float *src = p.seg + la_seg_at<TL>(c, at, slabs, wave, lane);
+            if (busy) {
+                const float *src = p.seg + la_seg_at<TL>(c, at, slabs, wave, lane);
 #pragma unroll
-            for (int x = 0; x < TL::AT * TL::NT; ++x) S[x] = *reinterpret_cast<const f32x4 *>(src + x * 256);
+                for (int x = 0; x < TL::AT * TL::NT; ++x) S[x] = *reinterpret_cast<const f32x4 *>(src + x * 256);
+            }
         } else if (p.s0) {
-            const float *src = p.s0 + ((size_t)at.b * c.H + at.h) * p.da * p.dc;
+            float raw[TL::DA / 32][PART];
+            // (through a buffer resource, which reads 0 past the matrix: a
+            // condition on a load becomes a branch and a wait for each)
+            const unsigned bytes = (unsigned)(p.da * p.dc) * 4u;
+            const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<float *>(p.s0 + own), (short)0, (int)bytes, 0x00020000);
 #pragma unroll
-            for (int t = 0; t < TL::AT; ++t)
+            for (int k = 0; k < TL::DA / 32; ++k)
 #pragma unroll
-                for (int n = 0; n < TL::NT; ++n)
+                for (int y = 0; y < PART; ++y) {
+                    int row, col;
+                    place(y, &row, &col);
+                    row += 32 * k;
+                    col += slab0;
+                    const bool in = EDGE == WHOLE || DIRECT || (row < p.da && col < p.dc);
+                    const unsigned off = in ? (unsigned)(row * p.srow + col * p.scol) * 4u : bytes;
+                    raw[k][y] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src, (int)off, 0, 0)) * p.in_scale;
+                }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = TL::row_of(t, g, r), col = col0 + TL::col_of(n, m);
-                        if (row < p.da && col < p.dc)
-                            S[t * TL::NT + n][r] = src[row * p.srow + col * p.scol] * p.in_scale;
-                    }
+            for (int k = 0; k < TL::DA / 32; ++k) {
+                if (k) la_barrier<63>();  // the rows before have been read
+#pragma unroll
+                for (int y = 0; y < PART; ++y) {
+                    int row, col;
+                    place(y, &row, &col);
+                    rows32[row * TL::LD + col] = raw[k][y];
+                }
+                la_barrier<63>();
+#pragma unroll
+                for (int t = 2 * k; t < 2 * k + 2; ++t)
+#pragma unroll
+                    for (int x = 0; x < TL::NT; ++x)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            S[t * TL::NT + x][r] =
+                                rows32[(TL::row_of(t, g, r) - 32 * k) * TL::LD + wave * 16 * TL::NT + TL::col_of(x, m)];
+            }
+            la_barrier<63>();  // before the buffer takes tokens
         }
     }
     if (!DIRECT && i0 < i1) put(tiles[0]);
@@ -631,25 +675,38 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
         buf = buf + 1 < BUFS ? buf + 1 : 0;
     }
 
-    if (!busy) return;
     if constexpr (STATE_ONLY) {
+        if (!busy) return;
         float *dst = p.seg + la_seg_at<TL>(c, at, slabs, wave, lane);
 #pragma unroll
         for (int x = 0; x < TL::AT * TL::NT; ++x) *reinterpret_cast<f32x4 *>(dst + x * 256) = S[x];
     } else {
         if (keep) {
-            float *dst = p.s1 + ((size_t)at.b * c.H + at.h) * p.da * p.dc;
+            float *dst = p.s1 + own;
 #pragma unroll
-            for (int t = 0; t < TL::AT; ++t)
+            for (int k = 0; k < TL::DA / 32; ++k) {
+                la_barrier<63>();  // the buffer's last readers are through
 #pragma unroll
-                for (int x = 0; x < TL::NT; ++x)
+                for (int t = 2 * k; t < 2 * k + 2; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = TL::row_of(t, g, r), col = col0 + TL::col_of(x, m);
-                        if (row < p.da && col < p.dc)
-                            dst[row * p.srow + col * p.scol] = S[t * TL::NT + x][r] * p.s1_scale;
-                    }
+                    for (int x = 0; x < TL::NT; ++x)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            rows32[(TL::row_of(t, g, r) - 32 * k) * TL::LD + wave * 16 * TL::NT + TL::col_of(x, m)] =
+                                S[t * TL::NT + x][r];
+                la_barrier<63>();
+#pragma unroll
+                for (int y = 0; y < PART; ++y) {
+                    int row, col;
+                    place(y, &row, &col);
+                    const float v = rows32[row * TL::LD + col];
+                    row += 32 * k;
+                    col += slab0;
+                    if (row < p.da && col < p.dc) dst[row * p.srow + col * p.scol] = v * p.s1_scale;
+                }
+            }
         }
+        if (!busy) return;
         // tokens past the row's end, by the segment of their own position
         const int width = min(16 * TL::NT, p.dc - col0), t1 = min(c.T, i0 + c.seg_tokens);
         for (int t = max(len, i0) + lane / 16; t < t1; t += 4)
