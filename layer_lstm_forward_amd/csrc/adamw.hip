@@ -109,26 +109,19 @@ __device__ inline void store_n(void *p, long long i, int left, bool whole, const
             if (e < left) q[e] = x[e];
 }
 
-// A workgroup takes K * 256 * VEC elements of one tensor.  Every byte is read and
-// written once: 28 bytes an element for fp32 with 32-bit states, 10 for bf16
-// with 8-bit states.
-template <class DT, bool EIGHT, int K>
-__global__ __launch_bounds__(256) void k_adamw(AdamwTable tab, AdamwHyper h) {
+// K pieces of 256 * VEC elements from element c0.  WHOLE: all of them lie in
+// the tensor and its arrays are aligned, which every load of the piece then
+// knows (a condition on each load would make each wait for the one before).
+template <class DT, bool EIGHT, int K, bool WHOLE>
+__device__ inline void adamw_part(const AdamwEntry &t, const AdamwHyper &h, long long c0, float keep, float scale) {
     using S = typename DT::S;
     constexpr int VEC = AdamwVec<DT>::VEC, LANES = AdamwVec<DT>::LANES;
-    // the entry, by all lanes at once: a loop would wait for memory each time
-    const int lane = threadIdx.x % 64;
-    const bool past = lane < tab.count && blockIdx.x >= tab.first[lane + 1];
-    const int e = __popcll(__ballot(past));
-    const AdamwEntry &t = tab.t[e];
-    const long long c0 = (long long)(blockIdx.x - tab.first[e]) * (K * 256 * VEC);
-    const float keep = 1.0f - t.lr * t.weight_decay, scale = h.grad_scale ? *h.grad_scale : 1.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const long long i = c0 + (k * 256 + threadIdx.x) * VEC;
         const long long rest = t.n - i;
-        const int left = rest < VEC ? (rest < 0 ? 0 : (int)rest) : VEC;
-        const bool whole = t.aligned && left == VEC;
+        const int left = WHOLE ? VEC : rest < VEC ? (rest < 0 ? 0 : (int)rest) : VEC;
+        constexpr bool whole = WHOLE;
         const long long blk = i / kBlock;
         S pv[VEC], gv[VEC];
         float m[VEC], v[VEC], root[VEC], w[VEC], least = 1.0f;
@@ -224,6 +217,25 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwTable tab, AdamwHyper h) {
             store_n<float, VEC>(t.v, i, left, whole, v);
         }
     }
+}
+
+// A workgroup takes K * 256 * VEC elements of one tensor.  Every byte is read and
+// written once: 28 bytes an element for fp32 with 32-bit states, 10 for bf16
+// with 8-bit states.
+template <class DT, bool EIGHT, int K>
+__global__ __launch_bounds__(256) void k_adamw(AdamwTable tab, AdamwHyper h) {
+    constexpr int VEC = AdamwVec<DT>::VEC;
+    // the entry, by all lanes at once: a loop would wait for memory each time
+    const int lane = threadIdx.x % 64;
+    const bool past = lane < tab.count && blockIdx.x >= tab.first[lane + 1];
+    const int e = __popcll(__ballot(past));
+    const AdamwEntry &t = tab.t[e];
+    const long long c0 = (long long)(blockIdx.x - tab.first[e]) * (K * 256 * VEC);
+    const float keep = 1.0f - t.lr * t.weight_decay, scale = h.grad_scale ? *h.grad_scale : 1.0f;
+    if (t.aligned && c0 + K * 256 * VEC <= t.n)
+        adamw_part<DT, EIGHT, K, true>(t, h, c0, keep, scale);
+    else
+        adamw_part<DT, EIGHT, K, false>(t, h, c0, keep, scale);
 }
 
 template <class DT, int K>
