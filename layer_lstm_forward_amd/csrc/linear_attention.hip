@@ -377,8 +377,8 @@ __device__ inline LaWhere la_where(const LaCall &c, int slabs) {
     id /= c.npass;
     w.h = id % c.H;
     id /= c.H;
-    w.seg = id % c.nseg;
-    w.b = id / c.nseg;
+    w.seg = id % c.grid_seg;
+    w.b = id / c.grid_seg;
     return w;
 }
 
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     const int slab0 = at.slab * TL::COLS, col0 = slab0 + wave * 16 * TL::NT;
     const bool busy = col0 < p.dc;  // else the wave only moves data and takes its part in A B^T
 
-    const bool keep = p.s1 && !p.seg, f32 = p.o.f32;
+    const bool keep = p.s1 && at.seg == c.nseg - 1, f32 = p.o.f32;
     const float out_scale = p.out_scale;
     const long long ot = p.o.t * dir;
     char *const out = p.o.p;
@@ -462,10 +462,14 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     // S from and to memory: 32 rows at a time through LDS, so that lanes take
     // neighbouring addresses (each lane fetching its own rows and columns took
     // 1.2 TB/s).  The matrix may lie transposed (srow = 1).
-    constexpr int PART = 8 * TL::NT;  // elements of 32 rows that a thread moves
+    constexpr int W4 = EDGE == WHOLE || DIRECT ? 4 : 1;  // neighbours in memory that a thread moves at once
+    constexpr int PART = 8 * TL::NT / W4;                // such moves of a thread for 32 rows
+    constexpr int ALL32 = (int)sizeof(tiles) / (32 * TL::LD * 4) < TL::DA / 32 ? (int)sizeof(tiles) / (32 * TL::LD * 4)
+                                                                              : TL::DA / 32;  // that fit LDS at once
     float *const rows32 = reinterpret_cast<float *>(tiles[BUFS - 1]);
+    const int across = p.srow == 1 ? TL::LD : 1;         // floats between a thread's neighbours in LDS
     auto place = [&](int y, int *row, int *col) {
-        const int x = y * TL::THREADS + tid;
+        const int x = (y * TL::THREADS + tid) * W4;
         *row = p.srow == 1 ? x % 32 : x / TL::COLS;
         *col = p.srow == 1 ? x / 32 : x % TL::COLS;
     };
@@ -478,7 +482,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                 for (int x = 0; x < TL::AT * TL::NT; ++x) S[x] = *reinterpret_cast<const f32x4 *>(src + x * 256);
             }
         } else if (p.s0) {
-            float raw[TL::DA / 32][PART];
+            float raw[TL::DA / 32][PART][W4];
             // (through a buffer resource, which reads 0 past the matrix: a
             // condition on a load becomes a branch and a wait for each)
             const unsigned bytes = (unsigned)(p.da * p.dc) * 4u;
@@ -492,9 +496,15 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                     place(y, &row, &col);
                     row += 32 * k;
                     col += slab0;
-                    const bool in = EDGE == WHOLE || DIRECT || (row < p.da && col < p.dc);
-                    const unsigned off = in ? (unsigned)(row * p.srow + col * p.scol) * 4u : bytes;
-                    raw[k][y] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src, (int)off, 0, 0)) * p.in_scale;
+                    const unsigned off = (unsigned)(row * p.srow + col * p.scol) * 4u;
+                    if constexpr (W4 == 4) {
+                        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src, (int)off, 0, 0);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) raw[k][y][e] = __uint_as_float(v[e]) * p.in_scale;
+                    } else {
+                        const int at0 = row < p.da && col < p.dc ? (int)off : (int)bytes;
+                        raw[k][y][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src, at0, 0, 0)) * p.in_scale;
+                    }
                 }
 #pragma unroll
             for (int k = 0; k < TL::DA / 32; ++k) {
@@ -503,7 +513,8 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                 for (int y = 0; y < PART; ++y) {
                     int row, col;
                     place(y, &row, &col);
-                    rows32[row * TL::LD + col] = raw[k][y];
+#pragma unroll
+                    for (int e = 0; e < W4; ++e) rows32[row * TL::LD + col + e * across] = raw[k][y][e];
                 }
                 la_barrier<63>();
 #pragma unroll
@@ -682,28 +693,36 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
         for (int x = 0; x < TL::AT * TL::NT; ++x) *reinterpret_cast<f32x4 *>(dst + x * 256) = S[x];
     } else {
         if (keep) {
-            float *dst = p.s1 + own;
+            float *dst = p.s1 + own, *rows = reinterpret_cast<float *>(tiles);
 #pragma unroll
-            for (int k = 0; k < TL::DA / 32; ++k) {
-                la_barrier<63>();  // the buffer's last readers are through
+            for (int k0 = 0; k0 < TL::DA / 32; k0 += ALL32) {
+                la_barrier<63>();  // the buffers' last readers are through
 #pragma unroll
-                for (int t = 2 * k; t < 2 * k + 2; ++t)
+                for (int t = 2 * k0; t < 2 * (k0 + ALL32) && t < TL::AT; ++t)
 #pragma unroll
                     for (int x = 0; x < TL::NT; ++x)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            rows32[(TL::row_of(t, g, r) - 32 * k) * TL::LD + wave * 16 * TL::NT + TL::col_of(x, m)] =
-                                S[t * TL::NT + x][r];
+                            rows[(TL::row_of(t, g, r) - 32 * k0) * TL::LD + wave * 16 * TL::NT + TL::col_of(x, m)] =
+                                S[t * TL::NT + x][r] * p.s1_scale;
                 la_barrier<63>();
 #pragma unroll
-                for (int y = 0; y < PART; ++y) {
-                    int row, col;
-                    place(y, &row, &col);
-                    const float v = rows32[row * TL::LD + col];
-                    row += 32 * k;
-                    col += slab0;
-                    if (row < p.da && col < p.dc) dst[row * p.srow + col * p.scol] = v * p.s1_scale;
-                }
+                for (int k = k0; k < k0 + ALL32 && k < TL::DA / 32; ++k)
+#pragma unroll
+                    for (int y = 0; y < PART; ++y) {
+                        int row, col;
+                        place(y, &row, &col);
+                        const float *v = rows + (row + 32 * (k - k0)) * TL::LD + col;
+                        row += 32 * k;
+                        col += slab0;
+                        float *q = dst + row * p.srow + col * p.scol;
+                        if constexpr (W4 == 4) {
+                            const f32x4 w = {v[0], v[across], v[2 * across], v[3 * across]};
+                            __builtin_memcpy(q, &w, 16);
+                        } else if (row < p.da && col < p.dc) {
+                            *q = *v;
+                        }
+                    }
             }
         }
         if (!busy) return;
@@ -716,7 +735,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 
 // Segments' own matrices -> the matrix before each segment, in place:
 //     run = in_scale S0;  for each s: (seg_s, run) = (run, gamma^(tokens of s) run + seg_s)
-// A thread keeps 4 rows of one column; also writes the state after the last.
+// A thread keeps 4 rows of one column.
 template <class DT, class TL>
 __global__ __launch_bounds__(256) void k_la_join(LaCall c, int slabs) {
     const LaPass &p = c.pass[blockIdx.y];
@@ -742,29 +761,47 @@ __global__ __launch_bounds__(256) void k_la_join(LaCall c, int slabs) {
     if (p.s0)
         for (int r = 0; r < 4 && row + r < p.da; ++r)
             run[r] = p.s0[own + (row + r) * p.srow + col * p.scol] * p.in_scale;
-    for (int s = 0; s < c.nseg; ++s) {
-        f32x4 *q = reinterpret_cast<f32x4 *>(p.seg + (s * rows * row_size + id) * 4);
-        const f32x4 add = *q;
-        *q = run;
-        const int tokens = min(max(len - s * c.seg_tokens, 0), c.seg_tokens);
-        run = run * la_pow(g2, tokens) + add;
+    constexpr int AHEAD = 8;  // segments read before the first is written
+    const size_t step = rows * row_size * 4;
+    float *q = p.seg + id * 4;
+    for (int s = 0; s < c.nseg; s += AHEAD) {
+        f32x4 add[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)  // the last segment has none (and is read for nothing)
+            add[k] = *reinterpret_cast<const f32x4 *>(q + min(s + k, c.nseg - 1) * step);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (s + k >= c.nseg) break;
+            *reinterpret_cast<f32x4 *>(q + (s + k) * step) = run;
+            run = run * la_pow(g2, min(max(len - (s + k) * c.seg_tokens, 0), c.seg_tokens)) + add[k];
+        }
     }
-    if (p.s1)
-        for (int r = 0; r < 4 && row + r < p.da; ++r)
-            p.s1[own + (row + r) * p.srow + col * p.scol] = run[r] * p.s1_scale;
 }
 
-template <class DT>
-__global__ __launch_bounds__(256) void k_la_share(const float *part, LaOut o, int T, int B, int H, int G, int D) {
-    const size_t n = (size_t)T * B * G * D;
-    const int per = H / G;
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
-        const int d = (int)(i % D), g = (int)(i / D % G);
-        const size_t row = i / ((size_t)D * G);  // b * T + t
-        const float *p = part + (row * H + (size_t)g * per) * D + d;
-        float sum = 0.0f;
-        for (int j = 0; j < per; ++j) sum += p[(size_t)j * D];
-        la_put<DT>(o, (int)(row % T), (int)(row / T), g, d, sum);
+// Shared heads: out head g = the sum, in order, of the fp32 partial sums of
+// its `per` query heads.  VEC neighbouring elements a thread; a workgroup takes
+// `rows` tokens; blockIdx.y chooses between the two tensors.
+template <class DT, int VEC>
+__global__ __launch_bounds__(256) void k_la_share(LaShare a, LaShare b, int T, int B, int G, int per, int rows) {
+    const LaShare &x = blockIdx.y ? b : a;
+    const unsigned D = (unsigned)x.D / VEC, row_items = D * G, items = row_items * rows;
+    const long long first = (long long)blockIdx.x * rows, all = (long long)T * B;
+    for (unsigned i = threadIdx.x; i < items; i += 256) {
+        const unsigned d = i % D * VEC, g = i / D % G;
+        const long long row = first + i / row_items;  // b * T + t
+        if (row >= all) return;
+        const float *p = x.part + (row * G + g) * per * x.D + d;
+        float sum[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e] = p[e];
+        for (int j = 1; j < per; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum[e] += p[(size_t)j * x.D + e];
+        const long long t = row % T, bt = row / T;
+        typename DT::S *o = reinterpret_cast<typename DT::S *>(x.out.p) + t * x.out.t + bt * x.out.b + g * x.out.h + d, w[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = round_to<DT>(sum[e]);
+        __builtin_memcpy(o, w, sizeof(w));
     }
 }
 
@@ -847,7 +884,10 @@ hipError_t la_launch(const LaCall &c, int slabs, hipStream_t s) {
     const long long blocks = (long long)slabs * c.npass * c.H * c.B * c.nseg;
     if (blocks > 0xFFFFFFFFll / TL::THREADS) return hipErrorInvalidValue;
     if (c.nseg > 1) {
-        hipLaunchKernelGGL((k_la<DT, TL, EDGE, true>), dim3((unsigned)blocks), dim3(TL::THREADS), 0, s, c, slabs);
+        LaCall own = c;  // the last segment's own matrix is the last pass's business
+        own.grid_seg = c.nseg - 1;
+        hipLaunchKernelGGL((k_la<DT, TL, EDGE, true>), dim3((unsigned)(blocks / c.nseg * own.grid_seg)),
+                           dim3(TL::THREADS), 0, s, own, slabs);
         const size_t n = (size_t)c.B * c.H * slabs * TL::NW * TL::AT * TL::NT * 64;
         hipLaunchKernelGGL((k_la_join<DT, TL>), dim3((unsigned)((n + 255) / 256), c.npass), dim3(256), 0, s, c, slabs);
     }
@@ -894,31 +934,46 @@ hipError_t la_any(const LaCall &c, hipStream_t s) {
 
 void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, int *nseg, int *seg_tokens,
                  size_t *seg_floats) {
-    (void)dtype;
     if (npass > 1) da = dc = da > dc ? da : dc;
     const LaPlan t = la_plan(da, dc);
     constexpr int C = 32;
     const long long slabs = (dc + t.cols - 1) / t.cols, blocks = rows * npass * slabs;
     const int chunks = (T + C - 1) / C;
-    long long want = blocks >= 256 ? 1 : 512 / blocks;
-    if (want > chunks / 2) want = chunks / 2;
-    const int per = want > 1 ? (int)((chunks + want - 1) / want) : chunks;  // chunks of a segment
+    // Microseconds, measured on heads of 128 x 128: a chunk takes `one` in the
+    // pass that writes outputs and `own` in the one that sums a segment's own
+    // matrix, however many workgroups run up to two a CU; cutting costs two
+    // more launches and moves each segment's matrix three times.  16 rows of
+    // 16384 tokens: 922 uncut, 111 in 16 segments, 100 in 32; 64 rows of 1024:
+    // 65 uncut, 43 in 4, 49 in 8; 128 rows of 512: 39 uncut, 44 in 2.
+    const double one = dtype == LSTM_BF16 ? 1.8 : 4.5, own = dtype == LSTM_BF16 ? 1.0 : 2.5;
+    const double move = blocks * (double)t.DA * t.cols * 12 / 5e6;
+    double best = one * chunks;
+    int per = chunks;  // chunks of a segment
+    for (int n = 2; n <= chunks && n * blocks <= 512; ++n) {
+        const int p = (chunks + n - 1) / n;
+        const double time = (one + own) * p + 12 + move * n;
+        if (time < best) best = time, per = p;
+    }
     *nseg = (chunks + per - 1) / per;
     *seg_tokens = per * C;
     *seg_floats = (size_t)t.DA * slabs * t.cols;
 }
 
-hipError_t launch_la(const LaCall &c, hipStream_t s) {
+hipError_t launch_la(const LaCall &call, hipStream_t s) {
+    LaCall c = call;
+    c.grid_seg = c.nseg;
     return c.dtype == LSTM_BF16 ? la_any<BF16>(c, s) : la_any<F32>(c, s);
 }
 
-hipError_t launch_la_share(const float *part, LaOut out, int T, int B, int H, int G, int D, int dtype, hipStream_t s) {
-    const size_t n = (size_t)T * B * G * D, blocks = (n + 255) / 256;
-    const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
-    if (dtype == LSTM_BF16)
-        hipLaunchKernelGGL(k_la_share<BF16>, grid, dim3(256), 0, s, part, out, T, B, H, G, D);
-    else
-        hipLaunchKernelGGL(k_la_share<F32>, grid, dim3(256), 0, s, part, out, T, B, H, G, D);
+hipError_t launch_la_share(const LaShare &a, const LaShare &b, int T, int B, int H, int G, int dtype, hipStream_t s) {
+    const bool vec = a.D % 4 == 0 && b.D % 4 == 0;
+    const int wide = G * (a.D > b.D ? a.D : b.D) / (vec ? 4 : 1), rows = wide >= 1024 ? 1 : 1024 / wide;
+    const long long all = (long long)T * B, blocks = (all + rows - 1) / rows;
+    if (blocks > 0xFFFFFFFFll / 256) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks, 2);
+    const auto k = dtype == LSTM_BF16 ? (vec ? k_la_share<BF16, 4> : k_la_share<BF16, 1>)
+                                      : (vec ? k_la_share<F32, 4> : k_la_share<F32, 1>);
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, s, a, b, T, B, G, H / G, rows);
     return hipGetLastError();
 }
 

@@ -46,6 +46,7 @@ struct LaCall {
     const int *lengths;   // or null
     int T, B, H, dtype;
     int nseg, seg_tokens; // segments of the sequence, tokens in each
+    int grid_seg;         // segments a launch covers (set by launch_la)
 };
 
 // Segments a sequence of each of `rows` (batch row, head) pairs is cut into,
@@ -54,8 +55,13 @@ struct LaCall {
 void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, int *nseg, int *seg_tokens,
                  size_t *seg_floats);
 hipError_t launch_la(const LaCall &c, hipStream_t s);
-// out head g = the sum, in order, of the fp32 partial sums [B][T][H][D] of its H / G query heads
-hipError_t launch_la_share(const float *part, LaOut out, int T, int B, int H, int G, int D, int dtype, hipStream_t s);
+// Partial sums [B][T][H][D] of the gradients of shared heads, and where their sums go.
+struct LaShare {
+    const float *part;
+    LaOut out;
+    int D;
+};
+hipError_t launch_la_share(const LaShare &a, const LaShare &b, int T, int B, int H, int G, int dtype, hipStream_t s);
 
 struct LaStep {
     LaTensor q, k, v;

@@ -211,9 +211,8 @@ lstm_status lstm_linear_attention_backward(const lstm_linear_attention_shape *s,
     hipStream_t st = static_cast<hipStream_t>(stream);
     rc = launched(launch_la(c, st));
     if (rc != LSTM_OK || group == 1) return rc;
-    rc = launched(launch_la_share(pk, output(dk), s->T, s->B, H, s->kv_heads, Dk, s->dtype, st));
-    if (rc != LSTM_OK) return rc;
-    return launched(launch_la_share(pv, output(dv), s->T, s->B, H, s->kv_heads, Dv, s->dtype, st));
+    return launched(launch_la_share(LaShare{pk, output(dk), Dk}, LaShare{pv, output(dv), Dv}, s->T, s->B, H,
+                                    s->kv_heads, s->dtype, st));
 }
 
 lstm_status lstm_linear_attention_step(const lstm_linear_attention_shape *s, const lstm_view *q, const lstm_view *k,
