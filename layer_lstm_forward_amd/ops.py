@@ -10,6 +10,7 @@ memory and streams only, and there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import layer_lstm_forward_amd as _base
 
@@ -33,6 +34,21 @@ class lstm_adamw_tensor(ctypes.Structure):
                 ("master", _vp), ("n", _ll), ("lr", _f), ("weight_decay", _f)]
 
 
+class _Struct:
+    """Argument type of a structure passed by address: its bytes, a ctypes structure, or None."""
+
+    @classmethod
+    def from_param(cls, x):
+        if x is None or isinstance(x, bytes):
+            return ctypes.c_char_p(x)
+        return ctypes.byref(x)
+
+
+# a structure's bytes cost a third of the ctypes object to make
+_pack_view = struct.Struct("@Pqqq").pack
+_pack_shape = struct.Struct("@iiiiiiif").pack
+_pack_tensor = struct.Struct("@PPPPPPPqff").pack
+
 _ready = None
 
 
@@ -41,7 +57,8 @@ def _lib():
     if _ready is not None:
         return _ready
     lib = _base.load_library()
-    shape, view, szp = (ctypes.POINTER(lstm_linear_attention_shape), ctypes.POINTER(lstm_view), ctypes.POINTER(_sz))
+    # structures travel as their bytes (see _pack_view) or as ctypes structures
+    shape, view, szp = _Struct, _Struct, ctypes.POINTER(_sz)
     for name, args in (
             ("lstm_linear_attention_workspace_size", [shape, szp]),
             ("lstm_linear_attention_backward_workspace_size", [shape, szp]),
@@ -53,7 +70,7 @@ def _lib():
             ("lstm_layer_norm_backward_workspace_size", [_ll, _i, szp]),
             ("lstm_layer_norm_backward", [_i, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _i, _vp, _vp, _vp, _vp,
                                           _sz, _vp]),
-            ("lstm_adamw_step", [_i, _i, ctypes.POINTER(lstm_adamw_tensor), _i, _d, _d, _d, _ll, _vp,
+            ("lstm_adamw_step", [_i, _i, _Struct, _i, _d, _d, _d, _ll, _vp,
                                  ctypes.c_uint, _vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = _i, args
@@ -115,7 +132,7 @@ def lstm_layer_norm_backward(dtype, dy, dy_stride, z, z_stride, mean, rstd, weig
 
 
 def lstm_adamw_step(dtype, state_bits, tensors, count, beta1, beta2, eps, step, grad_scale, seed, stream) -> int:
-    """tensors: a ctypes array of lstm_adamw_tensor."""
+    """tensors: a ctypes array of lstm_adamw_tensor, or its bytes."""
     return _lib().lstm_adamw_step(dtype, state_bits, tensors, count, beta1, beta2, eps, step, grad_scale, seed,
                                   stream)
 
@@ -129,20 +146,22 @@ def _check(rc, where):
 def _code(t, what):
     """The ABI's dtype code of a device tensor."""
     import torch
-    if not t.is_cuda or t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{what} must be a float32 or bfloat16 device tensor")
-    return _base.LSTM_BF16 if t.dtype == torch.bfloat16 else _base.LSTM_F32
+    if t.is_cuda:
+        if t.dtype == torch.bfloat16:
+            return _base.LSTM_BF16
+        if t.dtype == torch.float32:
+            return _base.LSTM_F32
+    raise ValueError(f"{what} must be a float32 or bfloat16 device tensor")
 
 
 def _same(t, like, what, shape=None):
-    if t.dtype != like.dtype or t.device != like.device or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.dtype != like.dtype or t.device != like.device or (shape is not None and t.shape != shape):
         raise ValueError(f"{what} must be of {like.dtype} on {like.device}"
                          + (f" and of shape {list(shape)}" if shape is not None else ""))
 
 
 def _dense(t, like, what, shape, dtype=None):
-    if t.device != like.device or t.dtype != (dtype or like.dtype) or tuple(t.shape) != tuple(shape) \
-            or not t.is_contiguous():
+    if t.device != like.device or t.dtype != (dtype or like.dtype) or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype or like.dtype} tensor of shape {list(shape)} "
                          f"on {like.device}")
 
@@ -155,12 +174,16 @@ class _On:
     """The stream of a call: its handle, and scratch memory that is given back to torch only when that stream has
     passed the call."""
 
+    __slots__ = ("device", "handle", "other", "_guard")
+
     def __init__(self, device, stream):
         import torch
         self.device = device
-        current = torch.cuda.current_stream(device)
-        self.handle = current.cuda_stream if stream is None else int(stream)
-        self.other = None if self.handle == current.cuda_stream else torch.cuda.ExternalStream(self.handle, device)
+        self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+        self.other = None
+        if stream is not None and int(stream) != self.handle:
+            self.handle = int(stream)
+            self.other = torch.cuda.ExternalStream(self.handle, device)
 
     def keep(self, *tensors):
         """For memory that the call allocated or copied: its user is the call's stream."""
@@ -172,7 +195,7 @@ class _On:
     def __enter__(self):
         import torch
         self._guard = None
-        if torch.cuda.current_device() != self.device.index:
+        if torch._C._cuda_getDevice() != self.device.index:
             self._guard = torch.cuda.device(self.device)
             self._guard.__enter__()
         return self
@@ -192,28 +215,36 @@ class _On:
 
 def _view(t, batch_first):
     s = t.stride()
-    return lstm_view(t.data_ptr(), s[1] if batch_first else s[0], s[0] if batch_first else s[1], s[2])
+    return _pack_view(t.data_ptr(), s[1], s[0], s[2]) if batch_first else _pack_view(t.data_ptr(), *s[:3])
 
 
-def _sequence(t, like, what, lead, heads=None, dim=None):
-    """A [*lead, heads, dim] tensor whose last axis is dense."""
-    if t.dim() != len(lead) + 2 or tuple(t.shape[:len(lead)]) != tuple(lead) \
-            or (heads is not None and t.shape[-2] != heads) or (dim is not None and t.shape[-1] != dim) \
-            or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{what} must be [{', '.join(map(str, lead))}, {heads or 'heads'}, {dim or 'dim'}] "
-                         "with a dense last axis")
-    _same(t, like, what)
+def _sequence(t, like, what, shape):
+    """A [.., heads, dim] tensor whose last axis is dense."""
+    if t.shape != shape or t.dtype != like.dtype or t.device != like.device or (shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what} must be a {like.dtype} tensor of shape {list(shape)} on {like.device}, "
+                         "its last axis dense")
 
 
-def _attention_shape(q, k, v, log_decay, scale, lead, T, B):
-    code = _code(q, "q")
-    _sequence(q, q, "q", lead)
-    _sequence(k, q, "k", lead, None, q.shape[-1])
-    _sequence(v, q, "v", lead, k.shape[-2])
-    H, G, Dk, Dv = q.shape[-2], k.shape[-2], q.shape[-1], v.shape[-1]
-    import torch
-    _dense(log_decay, q, "log_decay", (H,), torch.float32)
-    return lstm_linear_attention_shape(code, T, B, H, G, Dk, Dv, Dk ** -0.5 if scale is None else float(scale))
+class _Shape:
+    """The sizes of a call, checked against its tensors, and as the ABI takes them."""
+
+    __slots__ = ("heads", "key_dim", "value_dim", "B", "packed")
+
+    def __init__(self, q, k, v, log_decay, scale, lead, T, B):
+        import torch
+        code = _code(q, "q")
+        H, Dk = q.shape[-2:]
+        if k.dim() != q.dim() or v.dim() != q.dim():
+            raise ValueError("q, k and v must have as many axes")
+        G, Dv = v.shape[-2:]
+        _sequence(q, q, "q", lead + (H, Dk))
+        _sequence(k, q, "k", lead + (G, Dk))
+        _sequence(v, q, "v", lead + (G, Dv))
+        if log_decay.dtype != torch.float32 or log_decay.shape != (H,) or log_decay.device != q.device \
+                or not log_decay.is_contiguous():
+            raise ValueError(f"log_decay must be {H} contiguous float32 values on {q.device}")
+        self.heads, self.key_dim, self.value_dim, self.B = H, Dk, Dv, B
+        self.packed = _pack_shape(code, T, B, H, G, Dk, Dv, Dk ** -0.5 if scale is None else scale)
 
 
 def _lengths(lengths, T, B, device):
@@ -254,7 +285,7 @@ def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, b
         raise ValueError("q must be [T, B, heads, key_dim] ([B, T, heads, key_dim] with batch_first)")
     lead = tuple(q.shape[:2])
     T, B = (lead[1], lead[0]) if batch_first else lead
-    shape = _attention_shape(q, k, v, log_decay, scale, lead, T, B)
+    shape = _Shape(q, k, v, log_decay, scale, lead, T, B)
     _state_check(state, q, shape, "state")
     with _On(q.device, stream) as on:
         lens = _lengths(lengths, T, B, q.device)
@@ -264,13 +295,13 @@ def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, b
             on.keep(o, last)
         else:
             o, last = out
-            _sequence(o, q, "o", lead, shape.heads, shape.value_dim)
+            _sequence(o, q, "o", lead + (shape.heads, shape.value_dim))
             _state_check(last, q, shape, "state_out")
         if lens is not lengths:
             on.keep(lens)
-        nbytes = lstm_linear_attention_workspace_size(shape)
+        nbytes = lstm_linear_attention_workspace_size(shape.packed)
         ws = on.scratch(nbytes)
-        _check(lstm_linear_attention_forward(shape, _view(q, batch_first), _view(k, batch_first),
+        _check(lstm_linear_attention_forward(shape.packed, _view(q, batch_first), _view(k, batch_first),
                                              _view(v, batch_first), log_decay.data_ptr(), _addr(lens), _addr(state),
                                              _view(o, batch_first), _addr(last), _addr(ws), nbytes, on.handle),
                "lstm_linear_attention_forward")
@@ -288,8 +319,8 @@ def linear_attention_backward(q, k, v, log_decay, do, scale=None, state=None, ds
         raise ValueError("q must be [T, B, heads, key_dim] ([B, T, heads, key_dim] with batch_first)")
     lead = tuple(q.shape[:2])
     T, B = (lead[1], lead[0]) if batch_first else lead
-    shape = _attention_shape(q, k, v, log_decay, scale, lead, T, B)
-    _sequence(do, q, "do", lead, shape.heads, shape.value_dim)
+    shape = _Shape(q, k, v, log_decay, scale, lead, T, B)
+    _sequence(do, q, "do", lead + (shape.heads, shape.value_dim))
     _state_check(state, q, shape, "state")
     _state_check(dstate, q, shape, "dstate")
     with _On(q.device, stream) as on:
@@ -300,15 +331,15 @@ def linear_attention_backward(q, k, v, log_decay, do, scale=None, state=None, ds
         else:
             dq, dk, dv = out
             for t, like, what in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-                _sequence(t, q, what, lead, like.shape[-2], like.shape[-1])
+                _sequence(t, q, what, like.shape)
         dfirst = None if state is None else torch.empty_like(state)
         on.keep(dfirst)
         if lens is not lengths:
             on.keep(lens)
-        nbytes = lstm_linear_attention_backward_workspace_size(shape)
+        nbytes = lstm_linear_attention_backward_workspace_size(shape.packed)
         ws = on.scratch(nbytes)
         _check(lstm_linear_attention_backward(
-            shape, _view(q, batch_first), _view(k, batch_first), _view(v, batch_first), log_decay.data_ptr(),
+            shape.packed, _view(q, batch_first), _view(k, batch_first), _view(v, batch_first), log_decay.data_ptr(),
             _addr(lens), _addr(state), _view(do, batch_first), _addr(dstate), _view(dq, batch_first),
             _view(dk, batch_first), _view(dv, batch_first), _addr(dfirst), _addr(ws), nbytes, on.handle),
             "lstm_linear_attention_backward")
@@ -325,7 +356,7 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
     if q.dim() != 3:
         raise ValueError("q must be [B, heads, key_dim]")
     B = q.shape[0]
-    shape = _attention_shape(q, k, v, log_decay, scale, (B,), 1, B)
+    shape = _Shape(q, k, v, log_decay, scale, (B,), 1, B)
     if state.dim() != 4:
         raise ValueError("state must be [n, heads, key_dim, value_dim]")
     _dense(state, q, "state", (state.shape[0], shape.heads, shape.key_dim, shape.value_dim), torch.float32)
@@ -336,22 +367,24 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
             out = torch.empty(B, shape.heads, shape.value_dim, dtype=q.dtype, device=q.device)
             on.keep(out)
         else:
-            _sequence(out, q, "o", (B,), shape.heads, shape.value_dim)
-        views = [lstm_view(t.data_ptr(), 0, t.stride(0), t.stride(1)) for t in (q, k, v, out)]
-        _check(lstm_linear_attention_step(shape, views[0], views[1], views[2], log_decay.data_ptr(), _addr(slots),
-                                          state.shape[0], state.data_ptr(), views[3], on.handle),
+            _sequence(out, q, "o", (B, shape.heads, shape.value_dim))
+        views = [_pack_view(t.data_ptr(), 0, *t.stride()[:2]) for t in (q, k, v, out)]
+        _check(lstm_linear_attention_step(shape.packed, views[0], views[1], views[2], log_decay.data_ptr(),
+                                          _addr(slots), state.shape[0], state.data_ptr(), views[3], on.handle),
                "lstm_linear_attention_step")
     return out
 
 
-def _rows(t, what, keep=False):
-    """(address, row stride, rows) of a tensor whose leading axes are rows, evenly spaced; copied if they are not."""
-    width = t.shape[-1]
-    if t.dim() == 0 or width == 0:
+def _rows(t, what):
+    """A tensor whose leading axes are rows, evenly spaced, with the spacing and their number; copied if they are not."""
+    if t.dim() == 0 or t.shape[-1] == 0:
         raise ValueError(f"{what} must have a last axis")
+    width = t.shape[-1]
+    if t.is_contiguous():
+        return t, width, t.numel() // width
     if t.dim() != 2 or (width > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < width):
-        t = t.contiguous().view(-1, width) if t.numel() else t.reshape(-1, width)
-    return t, max(t.stride(0), width) if t.shape[0] > 1 else width
+        return t.contiguous(), width, t.numel() // width
+    return t, max(t.stride(0), width), t.shape[0]
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, stream=None):
@@ -365,16 +398,16 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, stream=None):
     for t, what in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _dense(t, x, what, (width,))
-    xr, xs = _rows(x, "x")
+    xr, xs, rows = _rows(x, "x")
     rr, rs = None, width
     if residual is not None:
         _same(residual, x, "residual", x.shape)
-        rr, rs = _rows(residual, "residual")
-    rows = xr.shape[0]
+        rr, rs, _ = _rows(residual, "residual")
     with _On(x.device, stream) as on:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        z = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else x
-        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) for _ in range(2))
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        z = torch.empty_like(y) if residual is not None else x
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
         on.keep(y, mean, rstd, xr if xr is not x else None, rr if rr is not residual else None,
                 z if residual is not None else None)
         _check(lstm_layer_norm_forward(code, xr.data_ptr(), xs, _addr(rr), rs, _addr(weight), _addr(bias), rows,
@@ -398,13 +431,13 @@ def layer_norm_backward(dy, z, mean, rstd, weight=None, dsum=None, stream=None):
         _dense(weight, z, "weight", (width,))
     if dsum is not None:
         _same(dsum, z, "dsum", z.shape)
-    yr, ys = _rows(dy, "dy")
-    zr, zs = _rows(z, "z")
-    rows = zr.shape[0]
+    yr, ys, rows = _rows(dy, "dy")
+    zr, zs, _ = _rows(z, "z")
     with _On(z.device, stream) as on:
         sr = dsum.contiguous() if dsum is not None else None
-        dz = torch.empty(z.shape, dtype=z.dtype, device=z.device)
-        dw, db = (torch.empty(width, dtype=z.dtype, device=z.device) for _ in range(2))
+        dz = torch.empty_like(z, memory_format=torch.contiguous_format)
+        dw = torch.empty(width, dtype=z.dtype, device=z.device)
+        db = torch.empty_like(dw)
         nbytes = lstm_layer_norm_backward_workspace_size(rows, width)
         ws = on.scratch(nbytes)
         on.keep(dz, dw, db, yr if yr is not dy else None, zr if zr is not z else None, sr if sr is not dsum else None)
@@ -451,23 +484,26 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1
     wds = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [float(weight_decay)] * n
     if any(len(x) != n for x in (grads, m, v, ms, vs, masters, lrs, wds)):
         raise ValueError("every list must have one entry for each parameter")
-    table = (lstm_adamw_tensor * n)()
-    for e, p, g, a, b, sa, sb, w, r, d in zip(table, params, grads, m, v, ms, vs, masters, lrs, wds):
-        _dense(p, like, "params", p.shape)
-        _dense(g, like, "grads", p.shape)
-        _dense(a, like, "m", p.shape, kind)
-        _dense(b, like, "v", p.shape, kind)
+    device, dtype = like.device, like.dtype
+    parts = []
+    for p, g, a, b, sa, sb, w, r, d in zip(params, grads, m, v, ms, vs, masters, lrs, wds):
+        size = p.shape
+        if not (p.dtype == dtype == g.dtype and a.dtype == kind == b.dtype and g.shape == size == a.shape
+                and b.shape == size and p.device == device == g.device and a.device == device == b.device
+                and p.is_contiguous() and g.is_contiguous() and a.is_contiguous() and b.is_contiguous()):
+            raise ValueError(f"params and grads must be contiguous {dtype} tensors on {device}, m and v contiguous "
+                             f"{kind} tensors, each of its parameter's shape")
         count = p.numel()
         if bits == 8:
             blocks = (-(-count // LSTM_ADAMW_BLOCK),)
             _dense(sa, like, "scales", blocks, torch.float32)
             _dense(sb, like, "scales", blocks, torch.float32)
-            e.m_scale, e.v_scale = sa.data_ptr(), sb.data_ptr()
         if w is not None:
-            _dense(w, like, "masters", p.shape, torch.float32)
-            e.master = w.data_ptr()
-        e.param, e.grad, e.m, e.v = p.data_ptr(), g.data_ptr(), a.data_ptr(), b.data_ptr()
-        e.n, e.lr, e.weight_decay = count, r, d
+            _dense(w, like, "masters", size, torch.float32)
+        parts.append(_pack_tensor(p.data_ptr(), g.data_ptr(), a.data_ptr(), b.data_ptr(),
+                                  0 if sa is None else sa.data_ptr(), 0 if sb is None else sb.data_ptr(),
+                                  0 if w is None else w.data_ptr(), count, r, d))
+    table = b"".join(parts)
     if grad_scale is not None:
         _dense(grad_scale, like, "grad_scale", grad_scale.shape, torch.float32)
         if grad_scale.numel() != 1:
