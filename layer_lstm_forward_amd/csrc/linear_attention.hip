@@ -321,13 +321,16 @@ __device__ inline u32x4 la_pack(const f32x4 *acc, int stride) {
 }
 
 // The state update's operand: column fragments times gamma^(n-1-j+1-e) for the
-// chunk's n valid tokens.  bf16: the weighted value is kept as a sum of two
-// bf16, so that S is exact to about 2^-17 a term (one bf16 would leave 2^-9
-// in a state that is an fp32 result and is carried from call to call).
+// chunk's n valid tokens.  bf16: the weighted value is kept as a sum of bf16
+// terms, rounded, so that S keeps what fp32 arithmetic would.  Two terms leave
+// 2^-17 of a value (2.7e-6 rms, measured against fp64), enough where S only
+// enters bf16 results; a state that is returned in fp32 and carried from call
+// to call gets the third (3e-7, as fp32 products have).
 template <class DT, class TL>
 struct LaWeighted {
-    u32x4 hi[TL::NT][TL::JU], lo[TL::NT][TL::JU];
-    __device__ void make(const u32x4 (*cf)[TL::JU], float g2, int n, int e, int lane) {
+    static constexpr int TERMS = TL::TPK == 2 ? 3 : 1;
+    u32x4 part[TERMS][TL::NT][TL::JU];
+    __device__ void make(const u32x4 (*cf)[TL::JU], float g2, int n, int e, int lane, bool third) {
         const int g = lane / 16;
 #pragma unroll
         for (int ju = 0; ju < TL::JU; ++ju) {
@@ -344,14 +347,17 @@ struct LaWeighted {
                     f32x8 f = __builtin_convertvector(v, f32x8);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) f[x] *= w[x];
-                    const bf16x8 h = __builtin_convertvector(f, bf16x8);
-                    f -= __builtin_convertvector(h, f32x8);
-                    hi[t][ju] = __builtin_bit_cast(u32x4, h);
-                    lo[t][ju] = __builtin_bit_cast(u32x4, __builtin_convertvector(f, bf16x8));
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        if (k == 2 && !third) break;
+                        const bf16x8 h = __builtin_convertvector(f, bf16x8);
+                        part[k][t][ju] = __builtin_bit_cast(u32x4, h);
+                        if (k < 2) f -= __builtin_convertvector(h, f32x8);
+                    }
                 } else {
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        hi[t][ju][x] = __float_as_uint(__uint_as_float(cf[t][ju][x]) * w[x]);
+                        part[0][t][ju][x] = __float_as_uint(__uint_as_float(cf[t][ju][x]) * w[x]);
                 }
             }
         }
@@ -407,7 +413,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     const int slab0 = at.slab * TL::COLS, col0 = slab0 + wave * 16 * TL::NT;
     const bool busy = col0 < p.dc;  // else the wave only moves data and takes its part in A B^T
 
-    const bool keep = p.s1 && at.seg == c.nseg - 1, f32 = p.o.f32;
+    const bool third = p.s1, keep = third && at.seg == c.nseg - 1, f32 = p.o.f32;
     const float out_scale = p.out_scale;
     const long long ot = p.o.t * dir;
     char *const out = p.o.p;
@@ -634,7 +640,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
             // the state after the chunk, unless nothing reads it
             if (STATE_ONLY || more || keep) {
                 LaWeighted<DT, TL> cw;
-                cw.make(cf, g2, n, e, lane);
+                cw.make(cf, g2, n, e, lane, third);
                 const float whole = la_pow(g2, n);
 #pragma unroll
                 for (int t = 0; t < TL::AT; ++t) {
@@ -646,10 +652,15 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                             lb, ju, [&](int x) { return TL::row_of(t, x, 0); }, lane);
 #pragma unroll
                         for (int x = 0; x < TL::NT; ++x) {
-                            S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.hi[x][ju]);
+                            S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.part[0][x][ju]);
                             if constexpr (TL::TPK == 2)
-                                S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.lo[x][ju]);
+                                S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.part[1][x][ju]);
                         }
+                        if (TL::TPK == 2 && third)
+#pragma unroll
+                            for (int x = 0; x < TL::NT; ++x)
+                                S[t * TL::NT + x] =
+                                    mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.part[LaWeighted<DT, TL>::TERMS - 1][x][ju]);
                     }
                 }
             }
