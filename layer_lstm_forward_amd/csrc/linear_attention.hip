@@ -87,30 +87,31 @@ __device__ inline void la_write(char *o, bool f32, long long at, V v, int left) 
 // pair of accumulators is the fragment of 32u + 8g.. without a move between
 // lanes.  The same holds for the chunk's products A B^T, whose tiles become
 // the operand of the product with Cv.
-template <class DT, int DA_, int NW_>
+template <class DT, int DA_, int NW_, int NT_>
 struct LaTile {
-    static constexpr int DA = DA_, NW = NW_, NT = DA_ > 128 ? 1 : 2;
+    static constexpr int DA = DA_, NW = NW_, NT = NT_;
     static constexpr int PER = DT::PER16, KC = DT::KC, TPK = KC / 16;
     static constexpr int C = 32;                               // tokens of a chunk
     static constexpr int NU = DA / KC, JU = C / KC, AT = DA / 16;
     static constexpr int COLS = NW * 16 * NT;                  // columns of a workgroup
     static constexpr int THREADS = 64 * NW;
     static constexpr int RA = DA / PER, RC = COLS / PER;       // 16-byte pieces of a row in LDS
-    static constexpr int PA = C * RA / THREADS, PC = C * RC / THREADS;  // pieces a thread moves
+    static constexpr int PA = C * RA > THREADS ? C * RA / THREADS : 1;  // pieces a thread moves
+    static constexpr int PC = C * RC > THREADS ? C * RC / THREADS : 1;
     static constexpr int ELEMS = C * (2 * DA + COLS);          // a chunk's three tensors in LDS
     static constexpr int P_ELEMS = C * C;                      // and its (A B^T) . W
     // 32 rows of S pass through a chunk's buffer on their way from and to memory
     static constexpr int LD = COLS + 4;                        // floats of such a row
     static constexpr int ROWS_ELEMS = 32 * LD * 4 / (int)sizeof(typename DT::S);
     static constexpr int BUF_ELEMS = ELEMS > ROWS_ELEMS ? ELEMS : (ROWS_ELEMS + 511) / 512 * 512;
-    static constexpr int PT = 4 / NW;                          // tiles of A B^T a wave computes
-    // LDS of a workgroup such that 8 waves share a CU's 160 KB, in chunks
-    static constexpr int FIT = (160 * 1024 * NW / 8 / (int)sizeof(typename DT::S) - P_ELEMS) / BUF_ELEMS;
+    static constexpr int PT = NW < 4 ? 4 / NW : 1;             // tiles of A B^T a wave computes
+    // chunks in the LDS of a workgroup such that 8 waves, and two workgroups, share a CU's 160 KB
+    static constexpr int FIT = (160 * 1024 / (NW < 4 ? 4 : 2) / (int)sizeof(typename DT::S) - P_ELEMS) / BUF_ELEMS;
     // chunk buffers where the loads go through registers (a second one saves a barrier a chunk) ...
     static constexpr int BUFS = FIT >= 2 ? 2 : 1;
     // ... and where they write to LDS themselves, two chunks ahead of the products if it fits
     static constexpr int RING = FIT >= 3 ? 3 : 2;
-    static_assert(C * RA % THREADS == 0 && C * RC % THREADS == 0 && THREADS % RA == 0 && THREADS % RC == 0, "tile");
+    static_assert(THREADS % RA == 0 && THREADS % RC == 0, "tile");
 
     // row (of the 16-row tile `tile`) that accumulator row 4g + r stands for
     __device__ static int row_of(int tile, int g, int r) {
@@ -203,6 +204,7 @@ struct LaStage {
         }
     }
     __device__ void store(S *lds) const {
+        if (RS > TL::C && row >= TL::C) return;  // more threads than pieces
 #pragma unroll
         for (int p = 0; p < P; ++p)
             *reinterpret_cast<u32x4 *>(lds + TL::template at<R>(row + p * RS, piece)) =
@@ -218,13 +220,15 @@ struct LaStage {
 template <class DT, class TL, int R>
 struct LaDirect {
     using S = typename DT::S;
-    static constexpr int N = TL::C * R / 64 / TL::NW;  // loads of a wave
+    static constexpr int BLOCKS = TL::C * R / 64;  // of 64 pieces
+    // loads of a wave; with fewer blocks than waves some load the same block
+    static constexpr int N = BLOCKS > TL::NW ? BLOCKS / TL::NW : 1;
     const char *base;
     int step;
     unsigned full[N];  // offsets of a chunk of C valid tokens
 
     __device__ unsigned offset(int i, int n) const {
-        const int at = ((threadIdx.x / 64 + TL::NW * i) * 64 + threadIdx.x % 64), j = at / R;
+        const int at = (threadIdx.x / 64 + TL::NW * i) % BLOCKS * 64 + threadIdx.x % 64, j = at / R;
         const unsigned piece = (at % R) ^ TL::template key<R>(j);
         const int k = min(j, n - 1);  // past the end: the last token again, whose weight is 0
         return (unsigned)(step >= 0 ? k : n - 1 - k) * (unsigned)abs(step) + piece * 16u;
@@ -247,7 +251,7 @@ struct LaDirect {
         for (int i = 0; i < N; ++i) {
             const unsigned o = n == TL::C ? full[i] : offset(i, n);
             const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) S *)lds +
-                                (wave + TL::NW * i) * 1024;
+                                (wave + TL::NW * i) % BLOCKS * 1024;
             // As the builtin for it, but unknown to the compiler's counting:
             // with the builtin it waits for every load under way before the
             // next transposed LDS read.  The waits are la_barrier's.  Nothing
@@ -577,12 +581,13 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
         }
         const S_t *la = tiles[buf], *lb = la + AT_B, *lc = la + AT_C;
 
-        // This wave's tiles of B A^T (rows: tokens j), weighted, as parts of
+        // This wave's tiles of four of B A^T (rows: tokens j), weighted, as parts of
         // the fragments that the product with Cv reads.
         if constexpr (!STATE_ONLY) {
 #pragma unroll
             for (int x = 0; x < TL::PT; ++x) {
-                const int it = TL::NW == 4 ? wave % 2 : wave, jt = TL::NW == 4 ? wave / 2 : x;
+                if (TL::NW > 4 && wave >= 4) break;
+                const int it = wave % 2, jt = TL::NW == 2 ? x : wave / 2;
                 f32x4 P = {0, 0, 0, 0};
                 if (TL::TPK == 2 || jt <= it) {
 #pragma unroll
@@ -877,17 +882,21 @@ __global__ __launch_bounds__(256) void k_la_step(LaStep c, int slabs) {
 
 namespace {
 
-// Tile of a call: the contraction dim padded to 64, 128 or 256, and the waves
-// of a workgroup: 4, or 2 where no pass has more columns than two waves take.
+// Tile of a call: the contraction dim padded to 64, 128 or 256, the waves of a
+// workgroup, and the 16-column tiles of a wave.  bf16 takes two tiles a wave:
+// every wave reads all of A and B from LDS, which one tile a wave makes twice
+// as much of (512 x 256 tokens, heads of 128: 505 us against 630).  fp32 is
+// bound by its matrix instructions and by registers, and takes one (64 x 512
+// tokens: 423 us against 530, which spilled).
 struct LaPlan {
-    int DA, NW, cols;
+    int DA, NW, NT;
+    int cols() const { return NW * NT * 16; }
 };
-LaPlan la_plan(int da, int dc) {
-    LaPlan t;
-    t.DA = da <= 64 ? 64 : da <= 128 ? 128 : 256;
-    t.NW = t.DA == 64 && dc <= 64 ? 2 : 4;
-    t.cols = t.NW * 16 * (t.DA > 128 ? 1 : 2);
-    return t;
+LaPlan la_plan(int da, int dc, int dtype) {
+    const int DA = da <= 64 ? 64 : da <= 128 ? 128 : 256;
+    if (dtype != LSTM_BF16) return LaPlan{DA, dc <= 64 ? 4 : 8, 1};
+    if (DA == 256) return LaPlan{DA, 4, 1};
+    return LaPlan{DA, DA == 64 && dc <= 64 ? 2 : 4, 2};
 }
 
 template <class DT, class TL, int EDGE>
@@ -912,9 +921,9 @@ bool la_aligned(const LaTensor &x) {
            x.t > -(1 << 25);
 }
 
-template <class DT, int DA, int NW>
+template <class DT, int DA, int NW, int NT>
 hipError_t la_go(const LaCall &c, int dc, hipStream_t s) {
-    using TL = LaTile<DT, DA, NW>;
+    using TL = LaTile<DT, DA, NW, NT>;
     const int slabs = (dc + TL::COLS - 1) / TL::COLS;
     bool whole = true, pieces = true;
     for (int i = 0; i < c.npass; ++i) {
@@ -936,9 +945,15 @@ template <class DT>
 hipError_t la_any(const LaCall &c, hipStream_t s) {
     const int da = c.npass > 1 ? max(c.pass[0].da, c.pass[0].dc) : c.pass[0].da;
     const int dc = c.npass > 1 ? da : c.pass[0].dc;
-    const LaPlan t = la_plan(da, dc);
-    if (t.DA == 64) return t.NW == 2 ? la_go<DT, 64, 2>(c, dc, s) : la_go<DT, 64, 4>(c, dc, s);
-    return t.DA == 128 ? la_go<DT, 128, 4>(c, dc, s) : la_go<DT, 256, 4>(c, dc, s);
+    const LaPlan t = la_plan(da, dc, c.dtype);
+    if constexpr (sizeof(typename DT::S) == 2) {
+        if (t.DA == 64) return t.NW == 2 ? la_go<DT, 64, 2, 2>(c, dc, s) : la_go<DT, 64, 4, 2>(c, dc, s);
+        return t.DA == 128 ? la_go<DT, 128, 4, 2>(c, dc, s) : la_go<DT, 256, 4, 1>(c, dc, s);
+    } else {
+        if (t.DA == 64) return t.NW == 4 ? la_go<DT, 64, 4, 1>(c, dc, s) : la_go<DT, 64, 8, 1>(c, dc, s);
+        if (t.DA == 128) return t.NW == 4 ? la_go<DT, 128, 4, 1>(c, dc, s) : la_go<DT, 128, 8, 1>(c, dc, s);
+        return t.NW == 4 ? la_go<DT, 256, 4, 1>(c, dc, s) : la_go<DT, 256, 8, 1>(c, dc, s);
+    }
 }
 
 }  // namespace
@@ -946,9 +961,9 @@ hipError_t la_any(const LaCall &c, hipStream_t s) {
 void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, int *nseg, int *seg_tokens,
                  size_t *seg_floats) {
     if (npass > 1) da = dc = da > dc ? da : dc;
-    const LaPlan t = la_plan(da, dc);
+    const LaPlan t = la_plan(da, dc, dtype);
     constexpr int C = 32;
-    const long long slabs = (dc + t.cols - 1) / t.cols, blocks = rows * npass * slabs;
+    const long long slabs = (dc + t.cols() - 1) / t.cols(), blocks = rows * npass * slabs;
     const int chunks = (T + C - 1) / C;
     // Microseconds, measured on heads of 128 x 128: a chunk takes `one` in the
     // pass that writes outputs and `own` in the one that sums a segment's own
@@ -957,7 +972,7 @@ void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, in
     // 16384 tokens: 922 uncut, 111 in 16 segments, 100 in 32; 64 rows of 1024:
     // 65 uncut, 43 in 4, 49 in 8; 128 rows of 512: 39 uncut, 44 in 2.
     const double one = dtype == LSTM_BF16 ? 1.8 : 4.5, own = dtype == LSTM_BF16 ? 1.0 : 2.5;
-    const double move = blocks * (double)t.DA * t.cols * 12 / 5e6;
+    const double move = blocks * (double)t.DA * t.cols() * 12 / 5e6;
     double best = one * chunks;
     int per = chunks;  // chunks of a segment
     for (int n = 2; n <= chunks && n * blocks <= 512; ++n) {
@@ -967,7 +982,7 @@ void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, in
     }
     *nseg = (chunks + per - 1) / per;
     *seg_tokens = per * C;
-    *seg_floats = (size_t)t.DA * slabs * t.cols;
+    *seg_floats = (size_t)t.DA * slabs * t.cols();
 }
 
 hipError_t launch_la(const LaCall &call, hipStream_t s) {
