@@ -53,12 +53,12 @@ __device__ inline void la_put(const LaOut &o, int t, int b, int h, int d, float 
         reinterpret_cast<typename DT::S *>(o.p)[at] = round_to<DT>(v);
 }
 
-// N neighbouring columns of a token from element offset `at`; unless all are
-// known to be, `left` of them are in range.
+// N neighbouring columns of a token; unless all are known to be, `left` of them
+// are in range.
 template <class DT, int N, bool ALL, class V>
-__device__ inline void la_write(char *o, bool f32, long long at, V v, int left) {
+__device__ inline void la_write(char *o, bool f32, V v, int left) {
     if (sizeof(typename DT::S) == 4 || f32) {
-        float *q = reinterpret_cast<float *>(o) + at;
+        float *q = reinterpret_cast<float *>(o);
         if (ALL || left >= N)
             __builtin_memcpy(q, &v, sizeof(v));
         else
@@ -66,7 +66,7 @@ __device__ inline void la_write(char *o, bool f32, long long at, V v, int left) 
             for (int x = 0; x < N; ++x)
                 if (x < left) q[x] = v[x];
     } else {
-        typename DT::S *q = reinterpret_cast<typename DT::S *>(o) + at, tmp[N];
+        typename DT::S *q = reinterpret_cast<typename DT::S *>(o), tmp[N];
 #pragma unroll
         for (int x = 0; x < N; ++x) tmp[x] = round_to<DT>(v[x]);
         if (ALL || left >= N)
@@ -324,8 +324,7 @@ __device__ inline u32x4 la_pack(const f32x4 *acc, int stride) {
     }
 }
 
-// The state update's operand: column fragments times gamma^(n-1-j+1-e) for the
-// chunk's n valid tokens.  bf16: the weighted value is kept as a sum of bf16
+// The state update's operand: column fragments times their tokens' weights.  bf16: the weighted value is kept as a sum of bf16
 // terms, rounded, so that S keeps what fp32 arithmetic would.  Two terms leave
 // 2^-17 of a value (2.7e-6 rms, measured against fp64), enough where S only
 // enters bf16 results; a state that is returned in fp32 and carried from call
@@ -334,16 +333,10 @@ template <class DT, class TL>
 struct LaWeighted {
     static constexpr int TERMS = TL::TPK == 2 ? 3 : 1;
     u32x4 part[TERMS][TL::NT][TL::JU];
-    __device__ void make(const u32x4 (*cf)[TL::JU], float g2, int n, int e, int lane, bool third) {
-        const int g = lane / 16;
+    __device__ void make(const u32x4 (*cf)[TL::JU], const float (*weight)[TL::PER], bool third) {
 #pragma unroll
         for (int ju = 0; ju < TL::JU; ++ju) {
-            float w[TL::PER];
-#pragma unroll
-            for (int x = 0; x < TL::PER; ++x) {
-                const int j = TL::KC * ju + TL::PER * g + x;
-                w[x] = j < n ? la_pow(g2, n - j - e) : 0.0f;
-            }
+            const float *w = weight[ju];
 #pragma unroll
             for (int t = 0; t < TL::NT; ++t) {
                 if constexpr (TL::TPK == 2) {
@@ -419,9 +412,15 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 
     const bool third = p.s1, keep = third && at.seg == c.nseg - 1, f32 = p.o.f32;
     const float out_scale = p.out_scale;
-    const long long ot = p.o.t * dir;
-    char *const out = p.o.p;
-    const long long o0 = (long long)first * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h + col0;
+    const int osize = f32 ? 4 : (int)sizeof(S_t);
+    // where this lane's columns of the chunk's two tokens go
+    const int col_at = TL::TPK == 2 && TL::NT == 2 ? 8 * g : 4 * g;
+    const long long ostep = p.o.t * dir * osize;
+    char *op[2];
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+        op[it] = p.o.p + ((long long)first * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h + col0 + col_at) * osize +
+                 (i0 + TL::row_of(it, m / 4, m % 4)) * ostep;
     const int cols = p.dc - col0;
     // where a chunk's tensors lie in its buffer
     constexpr int AT_B = TL::C * TL::DA, AT_C = 2 * TL::C * TL::DA;
@@ -543,25 +542,48 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 
     int buf = 0;
     f32x4 O[2][TL::NT];
-    // O's columns of its 2 x 16 tokens, out of chunk i of n tokens
-    auto flush = [&](int i, int n) {
+    // O's columns of its 2 x 16 tokens, n of the 32 valid; on to the next chunk
+    auto flush = [&](int n) {
 #pragma unroll
         for (int it = 0; it < 2; ++it) {
-            const int row = TL::row_of(it, m / 4, m % 4);
-            if (row >= n) continue;
-            const long long o = o0 + (long long)(i + row) * ot;
+            char *const o = op[it];
+            op[it] += TL::C * ostep;
+            if (TL::row_of(it, m / 4, m % 4) >= n) continue;
             if constexpr (TL::TPK == 2 && TL::NT == 2) {  // 8 neighbouring columns
                 const f32x8 v = __builtin_shufflevector(O[it][0], O[it][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                la_write<DT, 8, EDGE == WHOLE || DIRECT>(out, f32, o + 8 * g, v, cols - 8 * g);
+                la_write<DT, 8, EDGE == WHOLE || DIRECT>(o, f32, v, cols - col_at);
             } else {
 #pragma unroll
-                for (int t = 0; t < TL::NT; ++t) {
-                    const int col = 16 * t + 4 * g;
-                    la_write<DT, 4, EDGE == WHOLE || DIRECT>(out, f32, o + col, O[it][t], cols - col);
-                }
+                for (int t = 0; t < TL::NT; ++t)
+                    la_write<DT, 4, EDGE == WHOLE || DIRECT>(o + 16 * t * osize, f32, O[it][t], cols - 16 * t - col_at);
             }
         }
     };
+    // S is kept as S / gamma^lag while gamma^128 is above 2^-20: its products
+    // with gamma then come due every fourth chunk only, and the powers of
+    // gamma stand with the tokens' weights, which are multiplied anyway.
+    const bool slow = g2 >= -20.0f / 128.0f;
+    int lag = 0;
+    // gamma^(i+e) of this lane's tokens, gamma^(i-j) of its part of W, and the
+    // weights of the tokens j in the state's update over a whole chunk:
+    // gamma^-(j+e) where gamma is slow, else gamma^(C-j-e)
+    float row_w[2], mask_w[TL::PT][4], tok_w[TL::JU][TL::PER];
+#pragma unroll
+    for (int it = 0; it < 2; ++it) row_w[it] = la_pow(g2, TL::row_of(it, m / 4, m % 4) + e) * out_scale;
+#pragma unroll
+    for (int x = 0; x < TL::PT; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int it = wave % 2, jt = TL::NW == 2 ? x : wave / 2 % 2;
+            mask_w[x][r] = la_pow(g2, max(TL::row_of(it, m / 4, m % 4) - TL::row_of(jt, g, r), 0)) * out_scale;
+        }
+#pragma unroll
+    for (int ju = 0; ju < TL::JU; ++ju)
+#pragma unroll
+        for (int x = 0; x < TL::PER; ++x) {
+            const int j = TL::KC * ju + TL::PER * g + x;
+            tok_w[ju][x] = la_pow(g2, slow ? -(j + e) : TL::C - j - e);
+        }
     for (int i = i0; i < i1; i += TL::C) {
         const int n = min(TL::C, i1 - i);
         const bool more = i + TL::C < i1;
@@ -572,7 +594,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                 la_barrier<LOADS *(TL::RING - 2)>();
             else
                 la_barrier<0>();
-            if (!STATE_ONLY && i > i0 && busy) flush(i - TL::C, TL::C);
+            if (!STATE_ONLY && i > i0 && busy) flush(TL::C);
             const int next = i + (TL::RING - 1) * TL::C;
             if (next < i1) issue(next, buf == 0 ? TL::RING - 1 : buf - 1);
         } else {
@@ -597,8 +619,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                     const int ri = TL::row_of(it, m / 4, m % 4);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int d = ri - TL::row_of(jt, g, r);
-                        P[r] = d >= 0 ? P[r] * la_pow(g2, d) : 0.0f;
+                        P[r] = ri >= TL::row_of(jt, g, r) ? P[r] * mask_w[x][r] : 0.0f;
                     }
                 }
                 if constexpr (TL::TPK == 2)
@@ -629,9 +650,10 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                         for (int it = 0; it < 2; ++it) O[it][t] = mma_chunk(DT{}, O[it][t], sf, af[it]);
                     }
                 }
+                const float lag_w = la_pow(g2, lag);
 #pragma unroll
                 for (int it = 0; it < 2; ++it) {
-                    const float w = la_pow(g2, TL::row_of(it, m / 4, m % 4) + e);
+                    const float w = row_w[it] * lag_w;
 #pragma unroll
                     for (int t = 0; t < TL::NT; ++t) O[it][t] *= w;
                 }
@@ -644,13 +666,34 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                         lc, ju, [&](int x) { return wave * 16 * TL::NT + TL::col_of(t, 4 * x); }, lane);
             // the state after the chunk, unless nothing reads it
             if (STATE_ONLY || more || keep) {
+                const bool due = !slow || lag >= 3 * TL::C;
+                float w[TL::JU][TL::PER];
+                const float by = due ? la_pow(g2, n) : la_pow(g2, -lag);
+#pragma unroll
+                for (int ju = 0; ju < TL::JU; ++ju)
+#pragma unroll
+                    for (int x = 0; x < TL::PER; ++x) w[ju][x] = slow ? tok_w[ju][x] * by : tok_w[ju][x];
+                if (n < TL::C)  // the last chunk
+#pragma unroll
+                    for (int ju = 0; ju < TL::JU; ++ju)
+#pragma unroll
+                        for (int x = 0; x < TL::PER; ++x) {
+                            const int j = TL::KC * ju + TL::PER * g + x;
+                            if (!slow) w[ju][x] = la_pow(g2, max(n - j - e, 0));
+                            if (j >= n) w[ju][x] = 0.0f;
+                        }
                 LaWeighted<DT, TL> cw;
-                cw.make(cf, g2, n, e, lane, third);
-                const float whole = la_pow(g2, n);
+                cw.make(cf, w, third);
+                if (due) {
+                    const float whole = la_pow(g2, lag + n);
+#pragma unroll
+                    for (int x = 0; x < TL::AT * TL::NT; ++x) S[x] *= whole;
+                    lag = 0;
+                } else {
+                    lag += n;
+                }
 #pragma unroll
                 for (int t = 0; t < TL::AT; ++t) {
-#pragma unroll
-                    for (int x = 0; x < TL::NT; ++x) S[t * TL::NT + x] *= whole;
 #pragma unroll
                     for (int ju = 0; ju < TL::JU; ++ju) {
                         const u32x4 bt = la_cols<DT, TL, TL::RA>(
@@ -687,12 +730,10 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 #pragma unroll
                         for (int t = 0; t < TL::NT; ++t) O[it][t] = mma_chunk(DT{}, O[it][t], cf[t][ju], pf);
                     }
-#pragma unroll
-                    for (int t = 0; t < TL::NT; ++t) O[it][t] *= out_scale;
                 }
                 // DIRECT: the stores wait for the next chunk, behind whose
                 // barrier they precede loads that nobody waits for yet
-                if (!DIRECT || !more) flush(i, n);
+                if (!DIRECT || !more) flush(n);
             }
         }
         if constexpr (!DIRECT) {
@@ -702,11 +743,12 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
         buf = buf + 1 < BUFS ? buf + 1 : 0;
     }
 
+    const float rest = la_pow(g2, lag);
     if constexpr (STATE_ONLY) {
         if (!busy) return;
         float *dst = p.seg + la_seg_at<TL>(c, at, slabs, wave, lane);
 #pragma unroll
-        for (int x = 0; x < TL::AT * TL::NT; ++x) *reinterpret_cast<f32x4 *>(dst + x * 256) = S[x];
+        for (int x = 0; x < TL::AT * TL::NT; ++x) *reinterpret_cast<f32x4 *>(dst + x * 256) = S[x] * rest;
     } else {
         if (keep) {
             float *dst = p.s1 + own, *rows = reinterpret_cast<float *>(tiles);
@@ -720,7 +762,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             rows[(TL::row_of(t, g, r) - 32 * k0) * TL::LD + wave * 16 * TL::NT + TL::col_of(x, m)] =
-                                S[t * TL::NT + x][r] * p.s1_scale;
+                                S[t * TL::NT + x][r] * (rest * p.s1_scale);
                 la_barrier<63>();
 #pragma unroll
                 for (int k = k0; k < k0 + ALL32 && k < TL::DA / 32; ++k)
