@@ -929,15 +929,19 @@ namespace {
 // every wave reads all of A and B from LDS, which one tile a wave makes twice
 // as much of (512 x 256 tokens, heads of 128: 505 us against 630).  fp32 is
 // bound by its matrix instructions and by registers, and takes one (64 x 512
-// tokens: 423 us against 530, which spilled).
+// tokens: 423 us against 530, which spilled).  Few and short sequences of bf16
+// take one too, half a head a workgroup, so that more CUs share the work: 128
+// rows of 1024 tokens 57 us against 70, 64 rows 45 against 51; 128 rows of 2048
+// would lose (119 against 107, in segments).
 struct LaPlan {
     int DA, NW, NT;
     int cols() const { return NW * NT * 16; }
 };
-LaPlan la_plan(int da, int dc, int dtype) {
+LaPlan la_plan(int da, int dc, int dtype, long long rows, int T) {
     const int DA = da <= 64 ? 64 : da <= 128 ? 128 : 256;
     if (dtype != LSTM_BF16) return LaPlan{DA, dc <= 64 ? 4 : 8, 1};
     if (DA == 256) return LaPlan{DA, 4, 1};
+    if (DA == 128 && dc > 64 && rows <= 192 && T <= 1024) return LaPlan{DA, 4, 1};
     return LaPlan{DA, DA == 64 && dc <= 64 ? 2 : 4, 2};
 }
 
@@ -987,10 +991,11 @@ template <class DT>
 hipError_t la_any(const LaCall &c, hipStream_t s) {
     const int da = c.npass > 1 ? max(c.pass[0].da, c.pass[0].dc) : c.pass[0].da;
     const int dc = c.npass > 1 ? da : c.pass[0].dc;
-    const LaPlan t = la_plan(da, dc, c.dtype);
+    const LaPlan t = la_plan(da, dc, c.dtype, (long long)c.B * c.H * c.npass, c.T);
     if constexpr (sizeof(typename DT::S) == 2) {
         if (t.DA == 64) return t.NW == 2 ? la_go<DT, 64, 2, 2>(c, dc, s) : la_go<DT, 64, 4, 2>(c, dc, s);
-        return t.DA == 128 ? la_go<DT, 128, 4, 2>(c, dc, s) : la_go<DT, 256, 4, 1>(c, dc, s);
+        if (t.DA == 128) return t.NT == 1 ? la_go<DT, 128, 4, 1>(c, dc, s) : la_go<DT, 128, 4, 2>(c, dc, s);
+        return la_go<DT, 256, 4, 1>(c, dc, s);
     } else {
         if (t.DA == 64) return t.NW == 4 ? la_go<DT, 64, 4, 1>(c, dc, s) : la_go<DT, 64, 8, 1>(c, dc, s);
         if (t.DA == 128) return t.NW == 4 ? la_go<DT, 128, 4, 1>(c, dc, s) : la_go<DT, 128, 8, 1>(c, dc, s);
@@ -1003,7 +1008,7 @@ hipError_t la_any(const LaCall &c, hipStream_t s) {
 void la_segments(int T, long long rows, int npass, int da, int dc, int dtype, int *nseg, int *seg_tokens,
                  size_t *seg_floats) {
     if (npass > 1) da = dc = da > dc ? da : dc;
-    const LaPlan t = la_plan(da, dc, dtype);
+    const LaPlan t = la_plan(da, dc, dtype, rows * npass, T);
     constexpr int C = 32;
     const long long slabs = (dc + t.cols() - 1) / t.cols(), blocks = rows * npass * slabs;
     const int chunks = (T + C - 1) / C;
