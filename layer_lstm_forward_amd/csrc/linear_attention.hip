@@ -603,6 +603,39 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
         }
         const S_t *la = tiles[buf], *lb = la + AT_B, *lc = la + AT_C;
 
+        // bf16: fragments are read well before their products, all at once (left
+        // to itself the compiler reads a few, waits for LDS, and so on: about
+        // 20 round trips a chunk).
+        constexpr bool AHEAD = TL::TPK == 2 && TL::NU <= 4;
+        u32x4 pa[TL::NU], pb[TL::NU], af[2][TL::NU], cf[TL::NT][TL::JU], bt[TL::AT];
+        auto read_cf = [&]() {
+#pragma unroll
+            for (int t = 0; t < TL::NT; ++t)
+#pragma unroll
+                for (int ju = 0; ju < TL::JU; ++ju)
+                    cf[t][ju] = la_cols<DT, TL, TL::RC>(
+                        lc, ju, [&](int x) { return wave * 16 * TL::NT + TL::col_of(t, 4 * x); }, lane);
+        };
+        auto read_bt = [&](int t, int ju) {
+            return la_cols<DT, TL, TL::RA>(lb, ju, [&](int x) { return TL::row_of(t, x, 0); }, lane);
+        };
+        if constexpr (AHEAD) {
+            if constexpr (!STATE_ONLY) {
+                const int it = wave % 2, jt = wave / 2 % 2;
+#pragma unroll
+                for (int u = 0; u < TL::NU; ++u) {
+                    pb[u] = la_frag<DT, TL, TL::RA>(lb, jt, u, lane);
+                    pa[u] = la_frag<DT, TL, TL::RA>(la, it, u, lane);
+                }
+#pragma unroll
+                for (int u = 0; u < TL::NU; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) af[k][u] = la_frag<DT, TL, TL::RA>(la, k, u, lane);
+            }
+            read_cf();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+
         // This wave's tiles of four of B A^T (rows: tokens j), weighted, as parts of
         // the fragments that the product with Cv reads.
         if constexpr (!STATE_ONLY) {
@@ -613,9 +646,11 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                 f32x4 P = {0, 0, 0, 0};
                 if (TL::TPK == 2 || jt <= it) {
 #pragma unroll
-                    for (int u = 0; u < TL::NU; ++u)
-                        P = mma_chunk(DT{}, P, la_frag<DT, TL, TL::RA>(lb, jt, u, lane),
-                                      la_frag<DT, TL, TL::RA>(la, it, u, lane));
+                    for (int u = 0; u < TL::NU; ++u) {
+                        // (x: a second tile of the same rows)
+                        const u32x4 b = AHEAD && x == 0 ? pb[u] : la_frag<DT, TL, TL::RA>(lb, jt, u, lane);
+                        P = mma_chunk(DT{}, P, b, AHEAD ? pa[u] : la_frag<DT, TL, TL::RA>(la, it, u, lane));
+                    }
                     const int ri = TL::row_of(it, m / 4, m % 4);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -629,7 +664,6 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
             }
         }
 
-        u32x4 cf[TL::NT][TL::JU];
         if (busy) {
             if constexpr (!STATE_ONLY) {
                 // O = diag(gamma^(i+e)) A S, held transposed (rows: columns of
@@ -640,14 +674,14 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                     for (int t = 0; t < TL::NT; ++t) O[it][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int u = 0; u < TL::NU; ++u) {
-                    u32x4 af[2];
+                    if constexpr (!AHEAD)
 #pragma unroll
-                    for (int it = 0; it < 2; ++it) af[it] = la_frag<DT, TL, TL::RA>(la, it, u, lane);
+                        for (int it = 0; it < 2; ++it) af[it][u] = la_frag<DT, TL, TL::RA>(la, it, u, lane);
 #pragma unroll
                     for (int t = 0; t < TL::NT; ++t) {
                         const u32x4 sf = la_pack<DT, TL>(&S[u * TL::TPK * TL::NT + t], TL::NT);
 #pragma unroll
-                        for (int it = 0; it < 2; ++it) O[it][t] = mma_chunk(DT{}, O[it][t], sf, af[it]);
+                        for (int it = 0; it < 2; ++it) O[it][t] = mma_chunk(DT{}, O[it][t], sf, af[it][u]);
                     }
                 }
                 const float lag_w = la_pow(g2, lag);
@@ -658,14 +692,14 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                     for (int t = 0; t < TL::NT; ++t) O[it][t] *= w;
                 }
             }
-#pragma unroll
-            for (int t = 0; t < TL::NT; ++t)
-#pragma unroll
-                for (int ju = 0; ju < TL::JU; ++ju)
-                    cf[t][ju] = la_cols<DT, TL, TL::RC>(
-                        lc, ju, [&](int x) { return wave * 16 * TL::NT + TL::col_of(t, 4 * x); }, lane);
+            if (!AHEAD) read_cf();
             // the state after the chunk, unless nothing reads it
             if (STATE_ONLY || more || keep) {
+                if constexpr (AHEAD) {
+#pragma unroll
+                    for (int t = 0; t < TL::AT; ++t) bt[t] = read_bt(t, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
                 const bool due = !slow || lag >= 3 * TL::C;
                 float w[TL::JU][TL::PER];
                 const float by = due ? la_pow(g2, n) : la_pow(g2, -lag);
@@ -696,19 +730,18 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                 for (int t = 0; t < TL::AT; ++t) {
 #pragma unroll
                     for (int ju = 0; ju < TL::JU; ++ju) {
-                        const u32x4 bt = la_cols<DT, TL, TL::RA>(
-                            lb, ju, [&](int x) { return TL::row_of(t, x, 0); }, lane);
+                        const u32x4 kf = AHEAD ? bt[t] : read_bt(t, ju);
 #pragma unroll
                         for (int x = 0; x < TL::NT; ++x) {
-                            S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.part[0][x][ju]);
+                            S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], kf, cw.part[0][x][ju]);
                             if constexpr (TL::TPK == 2)
-                                S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.part[1][x][ju]);
+                                S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], kf, cw.part[1][x][ju]);
                         }
                         if (TL::TPK == 2 && third)
 #pragma unroll
                             for (int x = 0; x < TL::NT; ++x)
                                 S[t * TL::NT + x] =
-                                    mma_chunk(DT{}, S[t * TL::NT + x], bt, cw.part[LaWeighted<DT, TL>::TERMS - 1][x][ju]);
+                                    mma_chunk(DT{}, S[t * TL::NT + x], kf, cw.part[LaWeighted<DT, TL>::TERMS - 1][x][ju]);
                     }
                 }
             }
