@@ -77,7 +77,7 @@ lstm_status lstm_linear_attention_forward(const lstm_linear_attention_shape *sha
  * state_out, or NULL (zeros); dq, dk, dv: views with the heads of q, k, v,
  * written; dstate: gradient of state, or NULL (not wanted).  The decay is a
  * constant of the layer and gets no gradient.  Tokens past a row's length get
- * zero gradients.  A key or value head shared by several query heads gets the
+ * zero gradients.  Outputs must not overlap inputs.  A key or value head shared by several query heads gets the
  * sum of their gradients, in head order. */
 lstm_status lstm_linear_attention_backward(const lstm_linear_attention_shape *shape, const lstm_view *q,
                                            const lstm_view *k, const lstm_view *v, const float *log_decay,
@@ -107,7 +107,7 @@ lstm_status lstm_linear_attention_step(const lstm_linear_attention_shape *shape,
  *   weight, bias [width] dtype, or NULL (1 and 0)
  *   sum          receives z, or NULL
  *   mean, rstd   [rows] float32, or NULL
- * rows >= 0 (0 does nothing), width >= 1, eps >= 0 and finite.  y may be x's
+ * rows >= 0 (0 does nothing), width in 1..2^28, eps >= 0 and finite.  y may be x's
  * memory, and sum may be residual's or x's, where the rows are dense. */
 lstm_status lstm_layer_norm_forward(int dtype, const void *x, long long x_stride, const void *residual,
                                     long long residual_stride, const void *weight, const void *bias,

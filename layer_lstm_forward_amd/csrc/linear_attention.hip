@@ -196,7 +196,8 @@ struct LaStage {
 #pragma unroll
                 for (int e = 0; e < TL::PER; ++e) {
                     const int d = piece * TL::PER + e;
-                    const S x = reinterpret_cast<const S *>(q)[max(min(d, dim - 1), 0)];
+                    // (a slab past this tensor's columns has dim <= 0: still in the row)
+                    const S x = reinterpret_cast<const S *>(q)[min(d, dim - 1)];
                     tmp[e] = d < dim ? x : (S)0;
                 }
                 v[p] = __builtin_bit_cast(u32x4, tmp);

@@ -16,6 +16,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int kMaxDim = 256;
+constexpr int kMaxWidth = 1 << 28;         // of a normalised row
 constexpr long long kMaxRows = 1 << 20;  // (batch row, head) pairs
 
 
@@ -237,7 +238,7 @@ lstm_status lstm_layer_norm_forward(int dtype, const void *x, long long x_stride
                                     int width, float eps, void *y, void *sum, float *mean, float *rstd,
                                     void *stream) {
     if (dtype != LSTM_F32 && dtype != LSTM_BF16) return LSTM_ERR_DTYPE;
-    if (rows < 0 || width < 1 || x_stride < width || (residual && residual_stride < width)) return LSTM_ERR_SHAPE;
+    if (rows < 0 || width < 1 || width > kMaxWidth || x_stride < width || (residual && residual_stride < width)) return LSTM_ERR_SHAPE;
     if (!(eps >= 0.0f) || !std::isfinite(eps) || (!residual && sum)) return LSTM_ERR_ARG;
     if (rows == 0) return LSTM_OK;
     if (!x || !y) return LSTM_ERR_ARG;
@@ -254,7 +255,7 @@ lstm_status lstm_layer_norm_forward(int dtype, const void *x, long long x_stride
 
 lstm_status lstm_layer_norm_backward_workspace_size(long long rows, int width, size_t *bytes) {
     if (!bytes) return LSTM_ERR_ARG;
-    if (rows < 0 || width < 1) return LSTM_ERR_SHAPE;
+    if (rows < 0 || width < 1 || width > kMaxWidth) return LSTM_ERR_SHAPE;
     *bytes = (size_t)ln_parts(rows, width) * 2 * (size_t)width * sizeof(float);
     return LSTM_OK;
 }
@@ -264,7 +265,7 @@ lstm_status lstm_layer_norm_backward(int dtype, const void *dy, long long dy_str
                                      const void *dsum, long long rows, int width, void *dx, void *dweight,
                                      void *dbias, void *workspace, size_t workspace_bytes, void *stream) {
     if (dtype != LSTM_F32 && dtype != LSTM_BF16) return LSTM_ERR_DTYPE;
-    if (rows < 0 || width < 1 || dy_stride < width || z_stride < width) return LSTM_ERR_SHAPE;
+    if (rows < 0 || width < 1 || width > kMaxWidth || dy_stride < width || z_stride < width) return LSTM_ERR_SHAPE;
     if (rows > 0 && (!dy || !z || !mean || !rstd || !dx)) return LSTM_ERR_ARG;
     size_t need = 0;
     lstm_status rc = lstm_layer_norm_backward_workspace_size(rows, width, &need);

@@ -190,3 +190,13 @@ def test_oracle_layer_norm_gradients_are_differences():
     for i, got in enumerate((dz, dw, db)):
         want = _differences(lambda x: loss(*args[:i], x, *args[i + 1:]), args[i], range(args[i].size))
         np.testing.assert_allclose(got.reshape(-1), want, rtol=0, atol=1e-6)
+
+
+@needs_lib
+def test_limits():
+    assert ops.lstm_layer_norm_forward(0, FAKE, 1 << 30, 0, 0, 0, 0, 1, (1 << 28) + 1, 1e-5, FAKE, 0, 0, 0, 0) == -2
+    # steps from token to token are 32-bit byte counts
+    far = ops.lstm_view(FAKE, 1 << 30, 1, 1)
+    assert ops.lstm_linear_attention_forward(_shape(), far, _v(), _v(), FAKE, 0, 0, _v(), 0, FAKE, 1 << 50, 0) == -2
+    assert ops.lstm_linear_attention_backward(_shape(), _v(), _v(), far, FAKE, 0, 0, _v(), 0, _v(), _v(), _v(), 0, FAKE,
+                                              1 << 50, 0) == -2
