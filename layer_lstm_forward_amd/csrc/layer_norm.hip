@@ -4,7 +4,9 @@
 //     dw = sum over rows of dy u,  db = sum over rows of dy
 // Both directions are bound by memory: a row is read once, into registers,
 // and its sums are taken from there (the variance from the differences, in a
-// second look at the registers).
+// second look at the registers).  131072 rows of 2048 bf16 with a residual:
+// forward 397 us, backward 396 + 5 us, 5.4 TB/s each, as a copy.  A wave a row
+// needs no barrier: with a workgroup a row the backward took 722 us.
 #include "device.h"
 #include "ops.h"
 #include "ops_dev.h"

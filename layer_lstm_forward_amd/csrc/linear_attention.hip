@@ -394,6 +394,19 @@ __device__ inline size_t la_seg_at(const LaCall &c, const LaWhere &w, int slabs,
     return (((row * slabs + w.slab) * TL::NW + wave) * (TL::AT * TL::NT) * 64 + lane) * 4;
 }
 
+// One workgroup: the columns of a slab of one (pass, batch row, head), one
+// segment of its tokens, chunk by chunk; STATE_ONLY: only the segment's own
+// matrix, from zero, into the workspace.
+//
+// What bounds it.  bf16, heads of 128, 512 x 256 tokens with a state in and out
+// (2.7 GB): 552 us, 4.9 TB/s, what a large copy reaches.  A chunk of 32 tokens
+// costs a wave about 380 vector and 56 matrix instructions (72 where the state
+// is returned), which with two waves a SIMD is two thirds of that time; the
+// loads run two chunks ahead.  Chunks of 64 spilled (2.65 ms); every wave
+// computing all of A B^T instead of its quarter took 1.5 times as many matrix
+// instructions.  fp32: the matrix instructions themselves, 401 us for 512 x 64
+// tokens of 16 heads of 128, about 140 of the 157 TFLOP/s with the products
+// inside the chunks counted.
 template <class DT, class TL, int EDGE, bool STATE_ONLY>
 __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     using S_t = typename DT::S;
@@ -966,14 +979,16 @@ namespace {
 // tokens: 423 us against 530, which spilled).  Few and short sequences of bf16
 // take one too, half a head a workgroup, so that more CUs share the work: 128
 // rows of 1024 tokens 57 us against 70, 64 rows 45 against 51; 128 rows of 2048
-// would lose (119 against 107, in segments).
+// would lose (119 against 107, in segments).  fp32 does the same at any length
+// (30 rows of 333 tokens 40 us against 47, 64 of 512 61 against 73; the three
+// passes of 64 rows lost, 110 against 97).
 struct LaPlan {
     int DA, NW, NT;
     int cols() const { return NW * NT * 16; }
 };
 LaPlan la_plan(int da, int dc, int dtype, long long rows, int T) {
     const int DA = da <= 64 ? 64 : da <= 128 ? 128 : 256;
-    if (dtype != LSTM_BF16) return LaPlan{DA, dc <= 64 ? 4 : 8, 1};
+    if (dtype != LSTM_BF16) return LaPlan{DA, dc <= 64 || rows <= 128 ? 4 : 8, 1};
     if (DA == 256) return LaPlan{DA, 4, 1};
     if (DA == 128 && dc > 64 && rows <= 192 && T <= 1024) return LaPlan{DA, 4, 1};
     return LaPlan{DA, DA == 64 && dc <= 64 ? 2 : 4, 2};
