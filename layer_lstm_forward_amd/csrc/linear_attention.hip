@@ -424,7 +424,8 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     const int slab0 = at.slab * TL::COLS, col0 = slab0 + wave * 16 * TL::NT;
     const bool busy = col0 < p.dc;  // else the wave only moves data and takes its part in A B^T
 
-    const bool third = p.s1, keep = third && at.seg == c.nseg - 1, f32 = p.o.f32;
+    // the matrix is a result: after the last segment here, or joined from the segments' own
+    const bool keep = p.s1 && at.seg == c.nseg - 1, third = STATE_ONLY ? p.s1 != nullptr : keep, f32 = p.o.f32;
     const float out_scale = p.out_scale;
     const int osize = f32 ? 4 : (int)sizeof(S_t);
     // where this lane's columns of the chunk's two tokens go
