@@ -19,6 +19,14 @@ _vp, _i, _sz, _ll, _f, _d = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, cty
 
 LSTM_ADAMW_BLOCK = 256
 
+torch = None  # imported by the first call of a torch wrapper, as everywhere in this package
+
+
+def _need_torch():
+    global torch
+    import torch as t
+    torch = t
+
 
 class lstm_view(ctypes.Structure):
     _fields_ = [("data", _vp), ("time", _ll), ("batch", _ll), ("head", _ll)]
@@ -145,7 +153,6 @@ def _check(rc, where):
 
 def _code(t, what):
     """The ABI's dtype code of a device tensor."""
-    import torch
     if t.is_cuda:
         if t.dtype == torch.bfloat16:
             return _base.LSTM_BF16
@@ -177,7 +184,6 @@ class _On:
     __slots__ = ("device", "handle", "other", "_guard")
 
     def __init__(self, device, stream):
-        import torch
         self.device = device
         self.handle = torch._C._cuda_getCurrentRawStream(device.index)
         self.other = None
@@ -186,14 +192,12 @@ class _On:
             self.other = torch.cuda.ExternalStream(self.handle, device)
 
     def keep(self, *tensors):
-        """For memory that the call allocated or copied: its user is the call's stream."""
-        if self.other is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.other)
+        """For memory that the call allocated or copied: its user is the call's stream (where that is `other`)."""
+        for t in tensors:
+            if t is not None:
+                t.record_stream(self.other)
 
     def __enter__(self):
-        import torch
         self._guard = None
         if torch._C._cuda_getDevice() != self.device.index:
             self._guard = torch.cuda.device(self.device)
@@ -205,11 +209,11 @@ class _On:
             self._guard.__exit__(*exc)
 
     def scratch(self, nbytes):
-        import torch
         if nbytes == 0:
             return None
         t = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        self.keep(t)
+        if self.other is not None:
+            t.record_stream(self.other)
         return t
 
 
@@ -231,7 +235,6 @@ class _Shape:
     __slots__ = ("heads", "key_dim", "value_dim", "B", "packed")
 
     def __init__(self, q, k, v, log_decay, scale, lead, T, B):
-        import torch
         code = _code(q, "q")
         H, Dk = q.shape[-2:]
         if k.dim() != q.dim() or v.dim() != q.dim():
@@ -249,7 +252,6 @@ class _Shape:
 
 def _lengths(lengths, T, B, device):
     """None, B host ints (each checked), or an int32 device tensor (each clamped to 0..T on the device)."""
-    import torch
     if lengths is None:
         return None
     if isinstance(lengths, torch.Tensor) and lengths.is_cuda:
@@ -264,7 +266,6 @@ def _lengths(lengths, T, B, device):
 
 
 def _state_check(state, q, shape, what):
-    import torch
     if state is not None:
         _dense(state, q, what, (shape.B, shape.heads, shape.key_dim, shape.value_dim), torch.float32)
 
@@ -280,7 +281,8 @@ def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, b
     lengths: None, B host ints in 0..T, or an int32 device tensor; tokens past a row's length are not read.
     out: None or (o, state_out) to write into; state_out may be `state`.
     Returns (o, state_out)."""
-    import torch
+    if torch is None:
+        _need_torch()
     if q.dim() != 4:
         raise ValueError("q must be [T, B, heads, key_dim] ([B, T, heads, key_dim] with batch_first)")
     lead = tuple(q.shape[:2])
@@ -292,13 +294,15 @@ def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, b
         if out is None:
             o = torch.empty(*lead, shape.heads, shape.value_dim, dtype=q.dtype, device=q.device)
             last = torch.empty(B, shape.heads, shape.key_dim, shape.value_dim, dtype=torch.float32, device=q.device)
-            on.keep(o, last)
+            if on.other is not None:
+                on.keep(o, last)
         else:
             o, last = out
             _sequence(o, q, "o", lead + (shape.heads, shape.value_dim))
             _state_check(last, q, shape, "state_out")
         if lens is not lengths:
-            on.keep(lens)
+            if on.other is not None:
+                on.keep(lens)
         nbytes = lstm_linear_attention_workspace_size(shape.packed)
         ws = on.scratch(nbytes)
         _check(lstm_linear_attention_forward(shape.packed, _view(q, batch_first), _view(k, batch_first),
@@ -314,7 +318,8 @@ def linear_attention_backward(q, k, v, log_decay, do, scale=None, state=None, ds
 
     do: gradient of o; dstate: gradient of the returned state, or None.  out: None or (dq, dk, dv) to write into.
     The last result is the gradient of `state`, or None where there was none."""
-    import torch
+    if torch is None:
+        _need_torch()
     if q.dim() != 4:
         raise ValueError("q must be [T, B, heads, key_dim] ([B, T, heads, key_dim] with batch_first)")
     lead = tuple(q.shape[:2])
@@ -327,15 +332,18 @@ def linear_attention_backward(q, k, v, log_decay, do, scale=None, state=None, ds
         lens = _lengths(lengths, T, B, q.device)
         if out is None:
             dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
-            on.keep(dq, dk, dv)
+            if on.other is not None:
+                on.keep(dq, dk, dv)
         else:
             dq, dk, dv = out
             for t, like, what in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
                 _sequence(t, q, what, like.shape)
         dfirst = None if state is None else torch.empty_like(state)
-        on.keep(dfirst)
+        if on.other is not None:
+            on.keep(dfirst)
         if lens is not lengths:
-            on.keep(lens)
+            if on.other is not None:
+                on.keep(lens)
         nbytes = lstm_linear_attention_backward_workspace_size(shape.packed)
         ws = on.scratch(nbytes)
         _check(lstm_linear_attention_backward(
@@ -352,7 +360,8 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
     q [B, heads, key_dim], k and v with kv_heads heads.  state [n, heads, key_dim, value_dim] float32 is updated in
     place.  slots: None (row b is state[b]) or B int32 values on the device: row b is state[slots[b]], and a value
     outside 0..n-1 marks an idle row, whose o is 0; no two rows may name the same slot."""
-    import torch
+    if torch is None:
+        _need_torch()
     if q.dim() != 3:
         raise ValueError("q must be [B, heads, key_dim]")
     B = q.shape[0]
@@ -365,7 +374,8 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
     with _On(q.device, stream) as on:
         if out is None:
             out = torch.empty(B, shape.heads, shape.value_dim, dtype=q.dtype, device=q.device)
-            on.keep(out)
+            if on.other is not None:
+                on.keep(out)
         else:
             _sequence(out, q, "o", (B, shape.heads, shape.value_dim))
         views = [_pack_view(t.data_ptr(), 0, *t.stride()[:2]) for t in (q, k, v, out)]
@@ -392,7 +402,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, stream=None):
 
     Returns (y, mean, rstd, z): y and z in x's dtype and shape (z is x itself without a residual), mean and rstd
     float32 over the leading axes; z, mean and rstd are what layer_norm_backward reads."""
-    import torch
+    if torch is None:
+        _need_torch()
     code = _code(x, "x")
     width = x.shape[-1]
     for t, what in ((weight, "weight"), (bias, "bias")):
@@ -408,8 +419,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, stream=None):
         z = torch.empty_like(y) if residual is not None else x
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
-        on.keep(y, mean, rstd, xr if xr is not x else None, rr if rr is not residual else None,
-                z if residual is not None else None)
+        if on.other is not None:
+            on.keep(y, mean, rstd, xr if xr is not x else None, rr if rr is not residual else None,
+                    z if residual is not None else None)
         _check(lstm_layer_norm_forward(code, xr.data_ptr(), xs, _addr(rr), rs, _addr(weight), _addr(bias), rows,
                                        width, float(eps), y.data_ptr(), z.data_ptr() if residual is not None else None,
                                        mean.data_ptr(), rstd.data_ptr(), on.handle), "lstm_layer_norm_forward")
@@ -421,7 +433,8 @@ def layer_norm_backward(dy, z, mean, rstd, weight=None, dsum=None, stream=None):
 
     dz is the gradient of x and of the residual.  dsum: gradient that reaches z from elsewhere, added to dz.
     dweight and dbias are given without a weight too (the gradients of one that is all ones, and of a zero bias)."""
-    import torch
+    if torch is None:
+        _need_torch()
     code = _code(z, "z")
     width = z.shape[-1]
     _same(dy, z, "dy", z.shape)
@@ -440,7 +453,9 @@ def layer_norm_backward(dy, z, mean, rstd, weight=None, dsum=None, stream=None):
         db = torch.empty_like(dw)
         nbytes = lstm_layer_norm_backward_workspace_size(rows, width)
         ws = on.scratch(nbytes)
-        on.keep(dz, dw, db, yr if yr is not dy else None, zr if zr is not z else None, sr if sr is not dsum else None)
+        if on.other is not None:
+            on.keep(dz, dw, db, yr if yr is not dy else None, zr if zr is not z else None,
+                    sr if sr is not dsum else None)
         _check(lstm_layer_norm_backward(code, yr.data_ptr(), ys, zr.data_ptr(), zs, mean.data_ptr(), rstd.data_ptr(),
                                         _addr(weight), _addr(sr), rows, width, dz.data_ptr(), dw.data_ptr(),
                                         db.data_ptr(), _addr(ws), nbytes, on.handle), "lstm_layer_norm_backward")
@@ -450,7 +465,8 @@ def layer_norm_backward(dy, z, mean, rstd, weight=None, dsum=None, stream=None):
 def adamw_states(params, bits=32):
     """Zero states for adamw_step: (m, v, scales), lists like params; scales is None for states of 32 bits, else the
     pair of lists of block scales."""
-    import torch
+    if torch is None:
+        _need_torch()
     if bits not in (8, 32):
         raise ValueError("states have 8 or 32 bits")
     kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
@@ -470,7 +486,8 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1
     tensor.  masters: None or a list of float32 copies of bf16 parameters (None entries: no copy).
     grad_scale: None or one float32 on the device that every gradient is multiplied by.
     seed: states of 8 bits are rounded by chance with bits from it; give each step another."""
-    import torch
+    if torch is None:
+        _need_torch()
     n = len(params)
     if n == 0:
         return
