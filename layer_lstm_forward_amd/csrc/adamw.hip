@@ -180,7 +180,8 @@ __device__ inline void adamw_part(const AdamwEntry &t, const AdamwHyper &h, long
                 am = av = 0;
 #pragma unroll
                 for (int x = 0; x < VEC; ++x) {
-                    const unsigned bm = __float_as_uint(m[x]) & 0x7FFFFFFFu, bv = __float_as_uint(root[x]) & 0x7FFFFFFFu;
+                    const unsigned bm = __float_as_uint(m[x]) & 0x7FFFFFFFu;
+                    const unsigned bv = __float_as_uint(root[x]) & 0x7FFFFFFFu;
                     if (x < left && bm < 0x7F800000u) am = max(am, bm);
                     if (x < left && bv < 0x7F800000u) av = max(av, bv);
                 }

@@ -325,8 +325,8 @@ __device__ inline u32x4 la_pack(const f32x4 *acc, int stride) {
     }
 }
 
-// The state update's operand: column fragments times their tokens' weights.  bf16: the weighted value is kept as a sum of bf16
-// terms, rounded, so that S keeps what fp32 arithmetic would.  Two terms leave
+// The state update's operand: column fragments times their tokens' weights.
+// bf16: the weighted value is kept as a sum of bf16 terms, rounded, so that S keeps what fp32 arithmetic would.  Two terms leave
 // 2^-17 of a value (2.7e-6 rms, measured against fp64), enough where S only
 // enters bf16 results; a state that is returned in fp32 and carried from call
 // to call gets the third (3e-7, as fp32 products have).
@@ -434,7 +434,8 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     char *op[2];
 #pragma unroll
     for (int it = 0; it < 2; ++it)
-        op[it] = p.o.p + ((long long)first * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h + col0 + col_at) * osize +
+        op[it] = p.o.p +
+                 ((long long)first * p.o.t + (long long)at.b * p.o.b + (long long)at.h * p.o.h + col0 + col_at) * osize +
                  (i0 + TL::row_of(it, m / 4, m % 4)) * ostep;
     const int cols = p.dc - col0;
     // where a chunk's tensors lie in its buffer
@@ -527,7 +528,8 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                         for (int e = 0; e < 4; ++e) raw[k][y][e] = __uint_as_float(v[e]) * p.in_scale;
                     } else {
                         const int at0 = row < p.da && col < p.dc ? (int)off : (int)bytes;
-                        raw[k][y][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src, at0, 0, 0)) * p.in_scale;
+                        const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(src, at0, 0, 0);
+                        raw[k][y][0] = __uint_as_float(v) * p.in_scale;
                     }
                 }
 #pragma unroll
@@ -755,8 +757,8 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                         if (TL::TPK == 2 && third)
 #pragma unroll
                             for (int x = 0; x < TL::NT; ++x)
-                                S[t * TL::NT + x] =
-                                    mma_chunk(DT{}, S[t * TL::NT + x], kf, cw.part[LaWeighted<DT, TL>::TERMS - 1][x][ju]);
+                                S[t * TL::NT + x] = mma_chunk(DT{}, S[t * TL::NT + x], kf,
+                                                              cw.part[LaWeighted<DT, TL>::TERMS - 1][x][ju]);
                     }
                 }
             }
@@ -850,7 +852,8 @@ __global__ __launch_bounds__(256) void k_la_join(LaCall c, int slabs) {
     const size_t row_size = (size_t)slabs * TL::NW * PER_ROW, rows = (size_t)c.B * c.H;
     if (id >= rows * row_size) return;
     const int bh = (int)(id / row_size), x = (int)(id % row_size);
-    const int lane = x % 64, tile = x / 64 % (TL::AT * TL::NT), wave = x / PER_ROW % TL::NW, slab = x / PER_ROW / TL::NW;
+    const int lane = x % 64, tile = x / 64 % (TL::AT * TL::NT), wave = x / PER_ROW % TL::NW;
+    const int slab = x / PER_ROW / TL::NW;
     const int b = bh / c.H, h = bh % c.H, n = tile % TL::NT;
     const int col = slab * TL::COLS + wave * 16 * TL::NT + TL::col_of(n, lane % 16);
     const int row = TL::row_of(tile / TL::NT, lane / 16, 0);  // rows row .. row + 3
@@ -904,7 +907,8 @@ __global__ __launch_bounds__(256) void k_la_share(LaShare a, LaShare b, int T, i
 #pragma unroll
             for (int e = 0; e < VEC; ++e) sum[e] += p[(size_t)j * x.D + e];
         const long long t = row % T, bt = row / T;
-        typename DT::S *o = reinterpret_cast<typename DT::S *>(x.out.p) + t * x.out.t + bt * x.out.b + g * x.out.h + d, w[VEC];
+        typename DT::S *o = reinterpret_cast<typename DT::S *>(x.out.p) + t * x.out.t + bt * x.out.b + g * x.out.h + d;
+        typename DT::S w[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) w[e] = round_to<DT>(sum[e]);
         __builtin_memcpy(o, w, sizeof(w));

@@ -238,7 +238,8 @@ lstm_status lstm_layer_norm_forward(int dtype, const void *x, long long x_stride
                                     int width, float eps, void *y, void *sum, float *mean, float *rstd,
                                     void *stream) {
     if (dtype != LSTM_F32 && dtype != LSTM_BF16) return LSTM_ERR_DTYPE;
-    if (rows < 0 || width < 1 || width > kMaxWidth || x_stride < width || (residual && residual_stride < width)) return LSTM_ERR_SHAPE;
+    if (rows < 0 || width < 1 || width > kMaxWidth || x_stride < width || (residual && residual_stride < width))
+        return LSTM_ERR_SHAPE;
     if (!(eps >= 0.0f) || !std::isfinite(eps) || (!residual && sum)) return LSTM_ERR_ARG;
     if (rows == 0) return LSTM_OK;
     if (!x || !y) return LSTM_ERR_ARG;

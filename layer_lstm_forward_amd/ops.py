@@ -272,7 +272,7 @@ def _state_check(state, q, shape, what):
 
 def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, batch_first=False, out=None,
                      stream=None):
-    """S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale q_t S_t for whole sequences (lstm_linear_attention_forward).
+    """S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale q_t S_t over sequences (lstm_linear_attention_forward).
 
     q [T, B, heads, key_dim] ([B, T, heads, key_dim] with batch_first), k and v with kv_heads heads, which may be
     fewer: each is then shared by heads / kv_heads query heads.  Any strides with a dense last axis (slices of one
@@ -386,7 +386,7 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
 
 
 def _rows(t, what):
-    """A tensor whose leading axes are rows, evenly spaced, with the spacing and their number; copied if they are not."""
+    """A tensor whose leading axes are evenly spaced rows (copied if they are not), the spacing, and their number."""
     if t.dim() == 0 or t.shape[-1] == 0:
         raise ValueError(f"{what} must have a last axis")
     width = t.shape[-1]

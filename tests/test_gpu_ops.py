@@ -296,7 +296,8 @@ def test_layer_norm(dtype, rows, width, residual, affine):
     dz, dw, db = pkg.layer_norm_backward(t(dy), total, mean, rstd, t(w), dsum=t(ds))
     wz, wdw, wdb = ref.layer_norm_backward(dy, z, w, dsum=ds)
     g = np.abs(dy * ww)
-    A = wr[:, None] * (g + g.mean(1, keepdims=True) + (np.abs(unit) + 1) * (g * (np.abs(unit) + 1)).mean(1, keepdims=True))
+    A = wr[:, None] * (g + g.mean(1, keepdims=True)
+                       + (np.abs(unit) + 1) * (g * (np.abs(unit) + 1)).mean(1, keepdims=True))
     extra = 0 if ds is None else 4 * U32 * np.abs(ds)
     close(dz, wz, 4 * rel[:, None] * A + extra + half * np.abs(wz), "dz")
     close(dw, wdw, (np.abs(dy) * (np.abs(unit) + 1) * (2 * rel + rows * U32)[:, None]).sum(0) + half * np.abs(wdw),
@@ -585,3 +586,64 @@ def test_wrapper_refusals():
         pkg.adamw_step([x], [x], [x], [x], step=0)
     assert ops.lstm_layer_norm_forward(0, x.cpu().data_ptr(), 8, 0, 8, 0, 0, 3, 8, 1e-5, x.data_ptr(), 0, 0, 0,
                                        0) == -4
+
+
+# -------------------------------------------------- offsets past 32 bits
+def test_linear_attention_offsets_past_32_bits():
+    """Tokens 2^27 elements apart, batch rows past 2^32 elements: the same results as from dense copies."""
+    import torch
+    T, B, D = 20, 2, 64
+    far = 1 << 27
+    wide = torch.empty(2 * T * far + 3 * D, dtype=torch.bfloat16, device=DEV)  # 10.7 GB
+    rng = np.random.default_rng(13)
+    parts = [torch.as_strided(wide, (T, B, 1, D), (far, T * far, D, 1), i * D) for i in range(3)]
+    dense = [dev(draw(rng, (T, B, 1, D), "bf16", 0.3), "bf16") for _ in range(3)]
+    for x, y in zip(parts, dense):
+        x.copy_(y)
+    g = dev(np.array([-0.05], np.float32))
+    for a, b in zip(pkg.linear_attention(*parts, g), pkg.linear_attention(*dense, g)):
+        assert torch.equal(a, b)
+    do = dev(draw(rng, (T, B, 1, D), "bf16"), "bf16")
+    for a, b in zip(pkg.linear_attention_backward(*parts, g, do)[:3],
+                    pkg.linear_attention_backward(*dense, g, do)[:3]):
+        assert torch.equal(a, b)
+    # outputs that far apart
+    last = torch.empty(B, 1, D, D, device=DEV)
+    want = pkg.linear_attention(*dense, g)[0]
+    assert torch.equal(pkg.linear_attention(*dense, g, out=(parts[2], last))[0], want)
+
+
+def test_step_pool_past_32_bits():
+    import torch
+    n, D = 66000, 256
+    pool = torch.empty(n, 1, D, D, device=DEV)  # 17.3 GB
+    rng = np.random.default_rng(14)
+    at = torch.tensor([n - 1, 3], dtype=torch.int32, device=DEV)
+    small = dev(draw(rng, (2, 1, D, D), "f32"))
+    pool[at.long()] = small
+    q, k, v = (dev(draw(rng, (2, 1, D), "f32")) for _ in range(3))
+    g = dev(np.array([-0.1], np.float32))
+    a = pkg.linear_attention_step(q, k, v, g, pool, slots=at)
+    b = pkg.linear_attention_step(q, k, v, g, small)
+    assert torch.equal(a, b) and torch.equal(pool[at.long()], small)
+
+
+def test_layer_norm_and_adamw_past_32_bits():
+    import torch
+    rows, width = (1 << 20) + 3, 4100
+    x = torch.zeros(rows, width, dtype=torch.bfloat16, device=DEV)  # 8.6 GB
+    rng = np.random.default_rng(15)
+    tail = dev(draw(rng, (3, width), "bf16"), "bf16")
+    x[-3:] = tail
+    y, mean, rstd, _ = pkg.layer_norm(x)
+    wy, wm, wr, _ = pkg.layer_norm(tail)
+    assert torch.equal(y[-3:], wy) and torch.equal(mean[-3:], wm) and torch.equal(rstd[-3:], wr)
+    assert not y[:-3].any()
+    dz, _, _ = pkg.layer_norm_backward(x, x, mean, rstd)
+    assert torch.equal(dz[-3:], pkg.layer_norm_backward(tail, tail, wm, wr)[0])
+    del x, y, dz
+    n = (1 << 31) + 5000
+    p, g = torch.zeros(n, device=DEV), torch.ones(n, device=DEV)
+    m, v, _ = pkg.adamw_states([p])
+    pkg.adamw_step([p], [g], m, v, step=1, lr=0.5, weight_decay=0.0)
+    assert bool((p == p[0]).all()) and abs(float(p[0]) + 0.5) < 1e-5 and bool((m[0] == m[0][0]).all())
