@@ -138,7 +138,7 @@ struct LaTile {
 // How a call's rows are read, by its dims (LaEdge).  No path branches around a
 // load (a branch makes the compiler wait for the load where the paths join):
 // tokens past the end read the last valid one again, whose weight is 0.
-//   WHOLE  every 16-byte piece of a tile lies in the row
+//   WHOLE  every 16-byte piece of a tile lies in the row (fp32)
 //   EDGES  a piece that reaches past the row's end is read further left, so
 //          that it ends with the row, and shifted into place (zeros follow)
 //   SHORT  a dim below one piece: element by element
@@ -326,10 +326,11 @@ __device__ inline u32x4 la_pack(const f32x4 *acc, int stride) {
 }
 
 // The state update's operand: column fragments times their tokens' weights.
-// bf16: the weighted value is kept as a sum of bf16 terms, rounded, so that S keeps what fp32 arithmetic would.  Two terms leave
-// 2^-17 of a value (2.7e-6 rms, measured against fp64), enough where S only
-// enters bf16 results; a state that is returned in fp32 and carried from call
-// to call gets the third (3e-7, as fp32 products have).
+// bf16: the weighted value is kept as a sum of bf16 terms, rounded, so that S
+// keeps what fp32 arithmetic would.  Two terms leave 2^-17 of a value (2.7e-6
+// rms, measured against fp64), enough where S only enters bf16 results; a
+// state that is returned in fp32 and carried from call to call gets the third
+// (4e-7; fp32 products have 3e-7).
 template <class DT, class TL>
 struct LaWeighted {
     static constexpr int TERMS = TL::TPK == 2 ? 3 : 1;
@@ -1035,10 +1036,10 @@ hipError_t la_go(const LaCall &c, int dc, hipStream_t s) {
         for (int i = 0; i < c.npass; ++i)
             direct = direct && la_aligned(c.pass[i].a) && la_aligned(c.pass[i].b) && la_aligned(c.pass[i].c);
         if (direct) return la_launch<DT, TL, DIRECT_LDS>(c, slabs, s);
-        whole = false;
+    } else {
+        if (whole) return la_launch<DT, TL, WHOLE>(c, slabs, s);
     }
-    return whole ? la_launch<DT, TL, WHOLE>(c, slabs, s)
-                 : pieces ? la_launch<DT, TL, EDGES>(c, slabs, s) : la_launch<DT, TL, SHORT>(c, slabs, s);
+    return pieces ? la_launch<DT, TL, EDGES>(c, slabs, s) : la_launch<DT, TL, SHORT>(c, slabs, s);
 }
 
 template <class DT>
