@@ -269,7 +269,7 @@ def ln_tol(z, w, unit, rstd, dtype):
 @pytest.mark.parametrize("rows,width,residual,affine", [
     (1, 1, False, True), (3, 2, True, True), (4, 1024, True, True), (5, 7, False, False), (17, 63, True, True),
     (2, 64, False, True), (33, 65, True, False), (9, 511, False, True), (6, 1001, True, True), (3, 4096, True, True),
-    (2, 5000, False, True), (2, 8192, True, True), (1, 20011, True, True), (300, 256, False, True),
+    (2, 5000, False, True), (2, 8192, True, True), (1, 20011, True, True), (3, 12001, False, True), (300, 256, False, True),
     (1030, 130, True, True)])
 def test_layer_norm(dtype, rows, width, residual, affine):
     rng = np.random.default_rng(rows * 31 + width)
