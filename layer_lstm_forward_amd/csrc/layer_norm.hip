@@ -392,8 +392,9 @@ hipError_t ln_backward(const LnBackward &c, hipStream_t s) {
             },
             [&]() {
                 parts = ln_parts(c.rows, c.width);
-                hipLaunchKernelGGL(k_ln_dx_wide<DT>, dim3(blocks_of(c.rows, 1, 65536)), dim3(256), 0, s, c);
+                // the sums first: dx may lie over dy
                 if (c.part) hipLaunchKernelGGL(k_ln_dw_wide<DT>, dim3(parts), dim3(256), 0, s, c);
+                hipLaunchKernelGGL(k_ln_dx_wide<DT>, dim3(blocks_of(c.rows, 1, 65536)), dim3(256), 0, s, c);
             });
     if (c.dw || c.db)
         hipLaunchKernelGGL(k_ln_join<DT>, dim3((2 * c.width + 31) / 32), dim3(256), 0, s, c, parts);
