@@ -4,8 +4,11 @@ layer norm, and the AdamW step over many tensors.
 The ``lstm_*`` functions carry the C ABI's names and take integer device
 addresses (0 = NULL).  The functions below them take and return torch tensors
 and run on the current stream of the tensors' device, or on ``stream`` (an
-integer ``hipStream_t``).  As everywhere in this package torch provides device
-memory and streams only, and there is no fallback.
+integer ``hipStream_t``): a call with ``stream`` is one made with that stream
+as torch's current one, copies and allocations included.  The arguments have to
+be ready on that stream and are the caller's to keep until it has passed the
+call.  As everywhere in this package torch provides device memory and streams
+only, and there is no fallback.
 """
 from __future__ import annotations
 
@@ -178,10 +181,11 @@ def _addr(t):
 
 
 class _On:
-    """The stream of a call: its handle, and scratch memory that is given back to torch only when that stream has
-    passed the call."""
+    """The stream of a call.  Where it is not torch's current one it becomes that for the call (a `with` block), so
+    that copies and memory of the call come in the kernels' order: a block that torch hands out for the current stream
+    may still be in use there, and a copy made there may run before its source is written or after it is read."""
 
-    __slots__ = ("device", "handle", "other", "_guard")
+    __slots__ = ("device", "handle", "other", "_current", "_guard")
 
     def __init__(self, device, stream):
         self.device = device
@@ -190,17 +194,15 @@ class _On:
         if stream is not None and int(stream) != self.handle:
             self.handle = int(stream)
             self.other = torch.cuda.ExternalStream(self.handle, device)
-
-    def keep(self, *tensors):
-        """For memory that the call allocated or copied: its user is the call's stream (where that is `other`)."""
-        for t in tensors:
-            if t is not None:
-                t.record_stream(self.other)
+            self._current = torch.cuda.current_stream(device)
 
     def __enter__(self):
         self._guard = None
-        if torch._C._cuda_getDevice() != self.device.index:
+        if self.other is not None:
+            self._guard = torch.cuda.stream(self.other)
+        elif torch._C._cuda_getDevice() != self.device.index:
             self._guard = torch.cuda.device(self.device)
+        if self._guard is not None:
             self._guard.__enter__()
         return self
 
@@ -208,13 +210,15 @@ class _On:
         if self._guard is not None:
             self._guard.__exit__(*exc)
 
+    def give(self, *results):
+        """For results of a call on another stream: the caller's work on the current one may read them, too, so their
+        memory is not handed out again before that stream has passed what it had queued when they were dropped."""
+        for t in results:
+            if t is not None:
+                t.record_stream(self._current)
+
     def scratch(self, nbytes):
-        if nbytes == 0:
-            return None
-        t = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        if self.other is not None:
-            t.record_stream(self.other)
-        return t
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
 
 
 def _view(t, batch_first):
@@ -295,14 +299,11 @@ def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, b
             o = torch.empty(*lead, shape.heads, shape.value_dim, dtype=q.dtype, device=q.device)
             last = torch.empty(B, shape.heads, shape.key_dim, shape.value_dim, dtype=torch.float32, device=q.device)
             if on.other is not None:
-                on.keep(o, last)
+                on.give(o, last)
         else:
             o, last = out
             _sequence(o, q, "o", lead + (shape.heads, shape.value_dim))
             _state_check(last, q, shape, "state_out")
-        if lens is not lengths:
-            if on.other is not None:
-                on.keep(lens)
         nbytes = lstm_linear_attention_workspace_size(shape.packed)
         ws = on.scratch(nbytes)
         _check(lstm_linear_attention_forward(shape.packed, _view(q, batch_first), _view(k, batch_first),
@@ -333,17 +334,14 @@ def linear_attention_backward(q, k, v, log_decay, do, scale=None, state=None, ds
         if out is None:
             dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
             if on.other is not None:
-                on.keep(dq, dk, dv)
+                on.give(dq, dk, dv)
         else:
             dq, dk, dv = out
             for t, like, what in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
                 _sequence(t, q, what, like.shape)
         dfirst = None if state is None else torch.empty_like(state)
         if on.other is not None:
-            on.keep(dfirst)
-        if lens is not lengths:
-            if on.other is not None:
-                on.keep(lens)
+            on.give(dfirst)
         nbytes = lstm_linear_attention_backward_workspace_size(shape.packed)
         ws = on.scratch(nbytes)
         _check(lstm_linear_attention_backward(
@@ -375,7 +373,7 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
         if out is None:
             out = torch.empty(B, shape.heads, shape.value_dim, dtype=q.dtype, device=q.device)
             if on.other is not None:
-                on.keep(out)
+                on.give(out)
         else:
             _sequence(out, q, "o", (B, shape.heads, shape.value_dim))
         views = [_pack_view(t.data_ptr(), 0, *t.stride()[:2]) for t in (q, k, v, out)]
@@ -409,19 +407,19 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, stream=None):
     for t, what in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _dense(t, x, what, (width,))
-    xr, xs, rows = _rows(x, "x")
-    rr, rs = None, width
     if residual is not None:
         _same(residual, x, "residual", x.shape)
-        rr, rs, _ = _rows(residual, "residual")
     with _On(x.device, stream) as on:
+        xr, xs, rows = _rows(x, "x")
+        rr, rs = None, width
+        if residual is not None:
+            rr, rs, _ = _rows(residual, "residual")
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
         z = torch.empty_like(y) if residual is not None else x
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
         if on.other is not None:
-            on.keep(y, mean, rstd, xr if xr is not x else None, rr if rr is not residual else None,
-                    z if residual is not None else None)
+            on.give(y, mean, rstd, z if residual is not None else None)
         _check(lstm_layer_norm_forward(code, xr.data_ptr(), xs, _addr(rr), rs, _addr(weight), _addr(bias), rows,
                                        width, float(eps), y.data_ptr(), z.data_ptr() if residual is not None else None,
                                        mean.data_ptr(), rstd.data_ptr(), on.handle), "lstm_layer_norm_forward")
@@ -444,9 +442,9 @@ def layer_norm_backward(dy, z, mean, rstd, weight=None, dsum=None, stream=None):
         _dense(weight, z, "weight", (width,))
     if dsum is not None:
         _same(dsum, z, "dsum", z.shape)
-    yr, ys, rows = _rows(dy, "dy")
-    zr, zs, _ = _rows(z, "z")
     with _On(z.device, stream) as on:
+        yr, ys, rows = _rows(dy, "dy")
+        zr, zs, _ = _rows(z, "z")
         sr = dsum.contiguous() if dsum is not None else None
         dz = torch.empty_like(z, memory_format=torch.contiguous_format)
         dw = torch.empty(width, dtype=z.dtype, device=z.device)
@@ -454,8 +452,7 @@ def layer_norm_backward(dy, z, mean, rstd, weight=None, dsum=None, stream=None):
         nbytes = lstm_layer_norm_backward_workspace_size(rows, width)
         ws = on.scratch(nbytes)
         if on.other is not None:
-            on.keep(dz, dw, db, yr if yr is not dy else None, zr if zr is not z else None,
-                    sr if sr is not dsum else None)
+            on.give(dz, dw, db)
         _check(lstm_layer_norm_backward(code, yr.data_ptr(), ys, zr.data_ptr(), zs, mean.data_ptr(), rstd.data_ptr(),
                                         _addr(weight), _addr(sr), rows, width, dz.data_ptr(), dw.data_ptr(),
                                         db.data_ptr(), _addr(ws), nbytes, on.handle), "lstm_layer_norm_backward")

@@ -55,3 +55,62 @@ def test_layer_norm_results_over_inputs(width, dtype):
         t = [dy.clone(), ds.clone()]
         for p, q, what in zip(want, backward(t[0], t[1], t[over]), ("dx", "dweight", "dbias")):
             assert torch.equal(p, q), (what, "over", ("dy", "dsum")[over])
+
+
+# ------------------------------------------------------------ other streams
+def _busy():
+    """Some milliseconds of work queued on the current stream."""
+    import torch
+    torch.cuda._sleep(20_000_000)
+
+
+def test_copies_on_another_stream_come_after_their_source():
+    """Rows that are not evenly spaced are copied: after the work that is queued on the call's stream."""
+    import torch
+    rng = np.random.default_rng(31)
+    x, res, dy, ds = (dev(draw(rng, (40, 6, 500), "f32")) for _ in range(4))
+    w = dev(draw(rng, (500,), "f32"))
+    cut = lambda t: t.transpose(0, 1)  # noqa: E731
+    y, mean, rstd, z = pkg.layer_norm(cut(x), w, residual=cut(res))
+    want = [y, z, *pkg.layer_norm_backward(cut(dy), cut(x), mean, rstd, w, dsum=cut(ds))]
+    bufs = [torch.zeros_like(t) for t in (x, res, dy, ds)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        _busy()
+        for b, t in zip(bufs, (x, res, dy, ds)):
+            b.copy_(t)
+    bx, bres, bdy, bds = (cut(b) for b in bufs)
+    y, _, _, z = pkg.layer_norm(bx, w, residual=bres, stream=side.cuda_stream)
+    got = [y, z, *pkg.layer_norm_backward(bdy, bx, mean, rstd, w, dsum=bds, stream=side.cuda_stream)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_memory_on_another_stream_is_free_there():
+    """Tensors that were dropped while the current stream still reads them are not written by a call on another."""
+    import torch
+    c = La(T=2000, B=1, H=2, G=1, Dk=64, Dv=64, dtype="bf16")  # in segments, with a workspace
+    rng = np.random.default_rng(32)
+    x = dev(draw(rng, (3000, 500), "f32"))
+    want = [*c.forward(), *c.backward(), *pkg.layer_norm(x)[:3]]
+    dropped = [torch.full_like(t, i + 1.0) for i, t in enumerate(want) for _ in range(3)]
+    n = ops.lstm_linear_attention_backward_workspace_size(
+        ops.lstm_linear_attention_shape(1, 2000, 1, 2, 1, 64, 64, 0.125))
+    dropped += [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    copies = [torch.empty_like(t) for t in dropped]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy()
+    for a, b in zip(copies, dropped):
+        a.copy_(b)
+    values = [i + 1.0 for i in range(len(want)) for _ in range(3)] + [7] * 3
+    del dropped, b
+    got = [*c.forward(stream=side.cuda_stream), *c.backward(stream=side.cuda_stream),
+           *pkg.layer_norm(x, stream=side.cuda_stream)[:3]]
+    torch.cuda.synchronize()
+    for t, value in zip(copies, values):
+        assert bool((t == value).all())
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
