@@ -142,6 +142,9 @@ lstm_status lstm_layer_norm_backward(int dtype, const void *dy, long long dy_str
  * proportion (nearest rounding would stand still, since one step changes v by
  * about a thousandth), with bits from a hash of the element's index in its
  * tensor and `seed`; sqrt(v) of a positive v is at least the smallest code.
+ * What is not finite does not count for the scale and is stored as the format's
+ * NaN; for sqrt(v) that NaN is read as infinity, so that an element whose g^2
+ * left the fp32 range keeps its step of 0, as with states of 32 bits.
  * The update of p uses m and v before they are stored.  A bf16 parameter with
  * a float32 master copy is updated there and stored as its rounding. */
 #define LSTM_ADAMW_BLOCK 256

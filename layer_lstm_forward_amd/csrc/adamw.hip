@@ -67,10 +67,13 @@ __device__ inline void values_of(const unsigned char *c, float *f) {
 
 // sqrt(v) for v >= 2^-96 or 0: the hardware's reciprocal root and one Newton
 // step on the remainder v - s^2, half the instructions of the full sqrtf,
-// which also serves the smallest floats.
+// which also serves the smallest floats.  0, infinity and NaN are their own
+// roots (the Newton step would make infinity, which a g^2 past the fp32 range
+// leaves in v, a NaN).
 __device__ inline float root_of(float v) {
     const float y = __builtin_amdgcn_rsqf(v), s = v * y;
-    return v > 0.0f ? fmaf(fmaf(-s, s, v), 0.5f * y, s) : v;
+    constexpr int kPositive = 1 << 7 | 1 << 8;  // and finite: denormal, normal
+    return __builtin_amdgcn_classf(v, kPositive) ? fmaf(fmaf(-s, s, v), 0.5f * y, s) : v;
 }
 
 // The states' update, each operation rounded by itself: a state that is stored
@@ -140,7 +143,7 @@ __device__ inline void adamw_part(const AdamwEntry &t, const AdamwHyper &h, long
 #pragma unroll
             for (int x = 0; x < VEC; ++x) {
                 m[x] *= sm;
-                root[x] *= sv;
+                root[x] = fminf(root[x] * sv, INFINITY);  // (NaN becomes infinity)
                 v[x] = root[x] * root[x];
             }
         } else {
@@ -201,7 +204,7 @@ __device__ inline void adamw_part(const AdamwEntry &t, const AdamwHyper &h, long
                 cm[x] = (unsigned char)(a | ((__float_as_uint(m[x]) >> 24) & 0x80u));
                 cv[x] = (unsigned char)b;
             }
-            if (odd)  // infinity or NaN: the format's NaN
+            if (odd)  // infinity or NaN: the format's NaN (which it reads as infinity for sqrt(v))
 #pragma unroll
                 for (int x = 0; x < VEC; ++x) {
                     if ((__float_as_uint(m[x]) & 0x7FFFFFFFu) >= 0x7F800000u) cm[x] = 0x7F;

@@ -114,3 +114,29 @@ def test_memory_on_another_stream_is_free_there():
         assert bool((t == value).all())
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------- the ends of fp32's range
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype,master", [("f32", False), ("bf16", False), ("bf16", True)])
+def test_adamw_second_moment_overflows(dtype, master, bits):
+    """|g| = 1e20: g^2 is infinite in fp32, m is finite, so the step is m / inf = 0, then and in later steps."""
+    import torch
+    rng = np.random.default_rng(21)
+    p = draw(rng, (700,), dtype)
+    g = draw(rng, (700,), dtype, 1e-2)
+    bad = [5, 256, 511, 699]
+    g[bad] = np.float32(1e20)
+    tp, lr, wd = [dev(p, dtype)], 1e-2, 0.1
+    masters = [dev(p)] if master else None
+    m, v, scales = pkg.adamw_states(tp, bits=bits)
+    want = p[bad].astype(np.float64)
+    tol = np.zeros(len(bad))
+    for t in (1, 2, 3):
+        pkg.adamw_step(tp, [dev(g if t == 1 else g * 0, dtype)], m, v, step=t, lr=lr, weight_decay=wd, scales=scales,
+                       masters=masters, seed=t)
+        want *= 1 - lr * wd
+        # 1 - lr wd and its product: three roundings; a stored bf16 one more
+        tol += (4 * U32 + (U16 if dtype == "bf16" and not master else 0)) * np.abs(want)
+        close((masters or tp)[0][bad], want, tol, f"param after step {t}")
+    assert bool(torch.isfinite(tp[0]).all())
