@@ -40,7 +40,7 @@ typedef struct {
 
 typedef struct {
     int dtype;               /* lstm_dtype of q, k, v, o and their gradients */
-    int T, B;                /* >= 1 */
+    int T, B;                /* >= 1; T at most 2^31 - 2^15 - 1 */
     int heads, kv_heads;     /* >= 1, heads a multiple of kv_heads */
     int key_dim, value_dim;  /* 1..256 */
     float scale;             /* finite, not 0 */
@@ -64,10 +64,11 @@ lstm_status lstm_linear_attention_backward_workspace_size(const lstm_linear_atte
  *   state_out    like state: the state after each row's last token, or NULL.
  *                It may be the memory of `state` (then updated in place).
  * LSTM_ERR_ARG: NULL argument, a dim outside 1..256, heads not a multiple of
- * kv_heads, a scale that is 0 or not finite; LSTM_ERR_SHAPE: T or B < 1, B *
- * heads above 2^20, a time stride of 2^31 bytes; LSTM_ERR_WORKSPACE: workspace
- * too short.  Sequences run in chunks of 32 tokens: a value that is not finite
- * spoils its row's later outputs and may spoil earlier ones of its chunk. */
+ * kv_heads, a scale that is 0 or not finite; LSTM_ERR_SHAPE: T or B < 1, T
+ * above its limit, B * heads above 2^20, a time stride of 2^31 bytes;
+ * LSTM_ERR_WORKSPACE: workspace too short.  Sequences run in chunks of 32
+ * tokens: a value that is not finite spoils its row's later outputs and may
+ * spoil earlier ones of its chunk. */
 lstm_status lstm_linear_attention_forward(const lstm_linear_attention_shape *shape, const lstm_view *q,
                                           const lstm_view *k, const lstm_view *v, const float *log_decay,
                                           const int *lengths, const float *state, const lstm_view *o,

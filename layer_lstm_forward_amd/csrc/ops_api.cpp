@@ -18,7 +18,10 @@ constexpr size_t kAlign = 256;
 constexpr int kMaxDim = 256;
 constexpr int kMaxWidth = 1 << 28;         // of a normalised row
 constexpr long long kMaxRows = 1 << 20;  // (batch row, head) pairs
-
+// Tokens: the kernels count in int, up to the end of the last segment (of at
+// most 512, each of whole chunks of 32: less than 2^14 past T) and the two
+// chunks loaded ahead.
+constexpr int kMaxTokens = INT_MAX - (1 << 15);
 
 size_t elem(int dtype) { return dtype == LSTM_BF16 ? 2 : 4; }
 
@@ -50,7 +53,7 @@ lstm_status check_shape(const lstm_linear_attention_shape *s) {
     if (s->heads < 1 || s->kv_heads < 1 || s->heads % s->kv_heads != 0) return LSTM_ERR_ARG;
     if (s->key_dim < 1 || s->value_dim < 1 || s->key_dim > kMaxDim || s->value_dim > kMaxDim) return LSTM_ERR_ARG;
     if (!std::isfinite(s->scale) || s->scale == 0.0f) return LSTM_ERR_ARG;
-    if (s->T < 1 || s->B < 1) return LSTM_ERR_SHAPE;
+    if (s->T < 1 || s->T > kMaxTokens || s->B < 1) return LSTM_ERR_SHAPE;
     // a grid of 2^32 threads holds every workgroup of three passes
     if ((long long)s->B * s->heads > kMaxRows) return LSTM_ERR_SHAPE;
     return LSTM_OK;
