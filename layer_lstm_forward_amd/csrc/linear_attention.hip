@@ -427,7 +427,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 
     // the matrix is a result: after the last segment here, or joined from the segments' own
     const bool keep = p.s1 && at.seg == c.nseg - 1, third = STATE_ONLY ? p.s1 != nullptr : keep, f32 = p.o.f32;
-    const float out_scale = p.out_scale;
+    const float chunk_scale = p.row_scale * p.sum_scale;
     const int osize = f32 ? 4 : (int)sizeof(S_t);
     // where this lane's columns of the chunk's two tokens go
     const int col_at = TL::TPK == 2 && TL::NT == 2 ? 8 * g : 4 * g;
@@ -526,11 +526,11 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                     if constexpr (W4 == 4) {
                         const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src, (int)off, 0, 0);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) raw[k][y][e] = __uint_as_float(v[e]) * p.in_scale;
+                        for (int e = 0; e < 4; ++e) raw[k][y][e] = __uint_as_float(v[e]);
                     } else {
                         const int at0 = row < p.da && col < p.dc ? (int)off : (int)bytes;
                         const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(src, at0, 0, 0);
-                        raw[k][y][0] = __uint_as_float(v) * p.in_scale;
+                        raw[k][y][0] = __uint_as_float(v);
                     }
                 }
 #pragma unroll
@@ -587,20 +587,20 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
     // gamma^-(j+e) where gamma is slow, else gamma^(C-j-e)
     float row_w[2], mask_w[TL::PT][4], tok_w[TL::JU][TL::PER];
 #pragma unroll
-    for (int it = 0; it < 2; ++it) row_w[it] = la_pow(g2, TL::row_of(it, m / 4, m % 4) + e) * out_scale;
+    for (int it = 0; it < 2; ++it) row_w[it] = la_pow(g2, TL::row_of(it, m / 4, m % 4) + e) * p.row_scale;
 #pragma unroll
     for (int x = 0; x < TL::PT; ++x)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int it = wave % 2, jt = TL::NW == 2 ? x : wave / 2 % 2;
-            mask_w[x][r] = la_pow(g2, max(TL::row_of(it, m / 4, m % 4) - TL::row_of(jt, g, r), 0)) * out_scale;
+            mask_w[x][r] = la_pow(g2, max(TL::row_of(it, m / 4, m % 4) - TL::row_of(jt, g, r), 0)) * chunk_scale;
         }
 #pragma unroll
     for (int ju = 0; ju < TL::JU; ++ju)
 #pragma unroll
         for (int x = 0; x < TL::PER; ++x) {
             const int j = TL::KC * ju + TL::PER * g + x;
-            tok_w[ju][x] = la_pow(g2, slow ? -(j + e) : TL::C - j - e);
+            tok_w[ju][x] = la_pow(g2, slow ? -(j + e) : TL::C - j - e) * p.sum_scale;
         }
     for (int i = i0; i < i1; i += TL::C) {
         const int n = min(TL::C, i1 - i);
@@ -731,7 +731,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 #pragma unroll
                         for (int x = 0; x < TL::PER; ++x) {
                             const int j = TL::KC * ju + TL::PER * g + x;
-                            if (!slow) w[ju][x] = la_pow(g2, max(n - j - e, 0));
+                            if (!slow) w[ju][x] = la_pow(g2, max(n - j - e, 0)) * p.sum_scale;
                             if (j >= n) w[ju][x] = 0.0f;
                         }
                 LaWeighted<DT, TL> cw;
@@ -813,7 +813,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             rows[(TL::row_of(t, g, r) - 32 * k0) * TL::LD + wave * 16 * TL::NT + TL::col_of(x, m)] =
-                                S[t * TL::NT + x][r] * (rest * p.s1_scale);
+                                S[t * TL::NT + x][r] * rest;
                 la_barrier<63>();
 #pragma unroll
                 for (int k = k0; k < k0 + ALL32 && k < TL::DA / 32; ++k)
@@ -843,7 +843,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
 }
 
 // Segments' own matrices -> the matrix before each segment, in place:
-//     run = in_scale S0;  for each s: (seg_s, run) = (run, gamma^(tokens of s) run + seg_s)
+//     run = S0;  for each s: (seg_s, run) = (run, gamma^(tokens of s) run + seg_s)
 // A thread keeps 4 rows of one column.
 template <class DT, class TL>
 __global__ __launch_bounds__(256) void k_la_join(LaCall c, int slabs) {
@@ -870,7 +870,7 @@ __global__ __launch_bounds__(256) void k_la_join(LaCall c, int slabs) {
     f32x4 run = {0, 0, 0, 0};
     if (p.s0)
         for (int r = 0; r < 4 && row + r < p.da; ++r)
-            run[r] = p.s0[own + (row + r) * p.srow + col * p.scol] * p.in_scale;
+            run[r] = p.s0[own + (row + r) * p.srow + col * p.scol];
     constexpr int AHEAD = 8;  // segments read before the first is written
     const size_t step = rows * row_size * 4;
     float *q = p.seg + id * 4;

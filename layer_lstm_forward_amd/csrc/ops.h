@@ -11,13 +11,17 @@ namespace lstm_amd {
 
 // ---------------------------------------------------------- linear attention
 // One pass of the operator over every (batch row, head):
-//     out_i = out_scale * (sum over j <= i of gamma^(i-j) (a_i . b_j) c_j + gamma^(i + e) a_i S0 * in_scale)
+//     out_i = row_scale gamma^(i + e) a_i S0 + chunk_scale sum over j <= i of gamma^(i-j) (a_i . b_j) c_j
 // in token order (e = 1), or, reversed, in the order of falling token index
 // (i counts from the row's last token, e = 0: the carried state then is the
 // gradient that arrives at a token from the one after it).  The carried
-// matrix is S [da][dc].  Forward: (a, b, c) = (q, k, v).  The gradients are
-// three more passes: dq from (do, v, k), dk reversed from (v, do, q), dv
-// reversed from (k, q, do).
+// matrix is S [da][dc], the decayed S0 and sum_scale times the b_j c_j^T, and
+// chunk_scale = row_scale sum_scale.  Forward: (a, b, c) = (q, k, v).  The
+// gradients are three more passes: dq from (do, v, k), dk reversed from (v,
+// do, q), dv reversed from (k, q, do).  The call's scale stands with what
+// reads the state in the forward and in dq (row_scale), and with what is added
+// to its gradient in the other two (sum_scale): S is in the state's own units
+// in every pass, for any scale.
 struct LaTensor {
     const char *p;
     long long t, b, h;  // strides in elements
@@ -35,7 +39,7 @@ struct LaPass {
     const float *s0;      // [B][H][Dk][Dv] or null; element (r, c) at r * srow + c * scol
     float *s1;            // the carried matrix after the last token, or null
     int srow, scol;
-    float in_scale, out_scale, s1_scale;
+    float row_scale, sum_scale;
     int reverse;
     float *seg;           // matrices before the segments (workspace), or null (one segment)
 };

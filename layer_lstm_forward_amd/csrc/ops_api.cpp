@@ -149,7 +149,7 @@ lstm_status lstm_linear_attention_forward(const lstm_linear_attention_shape *s, 
     LaCall c{};
     c.npass = 1;
     c.pass[0] = LaPass{tensor(q, 1), tensor(k, group), tensor(v, group), output(o), s->key_dim, s->value_dim, state,
-                       state_out, s->value_dim, 1, 1.0f, s->scale, 1.0f, 0,
+                       state_out, s->value_dim, 1, s->scale, 1.0f, 0,
                        lay.nseg > 1 ? reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.seg[0])
                                     : nullptr};
     c.log_decay = log_decay;
@@ -199,11 +199,9 @@ lstm_status lstm_linear_attention_backward(const lstm_linear_attention_shape *s,
     const float sc = s->scale;
     LaCall c{};
     c.npass = 3;
-    // The carried matrix of the reversed passes is dS / scale, so that one
-    // factor at the output serves both of its terms.
-    c.pass[0] = LaPass{td, tv, tk, output(dq), Dv, Dk, state, nullptr, 1, Dv, 1.0f, sc, 1.0f, 0, seg[0]};
-    c.pass[1] = LaPass{tv, td, tq, ok, Dv, Dk, dstate_out, nullptr, 1, Dv, 1.0f / sc, sc, 1.0f, 1, seg[1]};
-    c.pass[2] = LaPass{tk, tq, td, ov, Dk, Dv, dstate_out, dstate, Dv, 1, 1.0f / sc, sc, sc, 1, seg[2]};
+    c.pass[0] = LaPass{td, tv, tk, output(dq), Dv, Dk, state, nullptr, 1, Dv, sc, 1.0f, 0, seg[0]};
+    c.pass[1] = LaPass{tv, td, tq, ok, Dv, Dk, dstate_out, nullptr, 1, Dv, 1.0f, sc, 1, seg[1]};
+    c.pass[2] = LaPass{tk, tq, td, ov, Dk, Dv, dstate_out, dstate, Dv, 1, 1.0f, sc, 1, seg[2]};
     c.log_decay = log_decay;
     c.lengths = lengths;
     c.T = s->T;

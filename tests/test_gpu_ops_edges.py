@@ -140,3 +140,16 @@ def test_adamw_second_moment_overflows(dtype, master, bits):
         tol += (4 * U32 + (U16 if dtype == "bf16" and not master else 0)) * np.abs(want)
         close((masters or tp)[0][bad], want, tol, f"param after step {t}")
     assert bool(torch.isfinite(tp[0]).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale,size", [(1e-30, 1e10), (1e-39, 1.0), (1e25, 1e-10)])
+def test_linear_attention_gradients_at_any_scale(scale, size, dtype):
+    """The gradient of the state does not depend on the scale: a row of no tokens passes it on as it is."""
+    import torch
+    c = La(T=50, B=3, H=2, G=1, Dk=32, Dv=40, dtype=dtype, lengths=[50, 0, 33], scale=scale)
+    c.dS = c.dS * np.float32(size)
+    c.tdS = dev(c.dS)
+    grads = c.backward()
+    c.check_backward(grads)
+    assert torch.equal(grads[3][1], c.tdS[1])
