@@ -7,8 +7,10 @@
 //     O  = diag(gamma^(i+e)) A S + ((A B^T) . W) Cv,   W_ij = gamma^(i-j) for i >= j, else 0
 //     S' = gamma^C S + B^T diag(gamma^(C-j-e)) Cv
 // with e = 1; in a reversed pass e = 0 and tokens count from the row's end.
-// Every power has an exponent of at least 0, so nothing overflows however
-// small gamma is.
+// Every power has an exponent of at least 0, so that nothing overflows however
+// small gamma is, but for a gamma near 1 (2^(+-20/128) at most), whose S is
+// carried as S / gamma^lag, lag up to 128: values above 2^108 leave the fp32
+// range there.
 #include "device.h"
 #include "ops.h"
 #include "ops_dev.h"
@@ -577,10 +579,11 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
             }
         }
     };
-    // S is kept as S / gamma^lag while gamma^128 is above 2^-20: its products
-    // with gamma then come due every fourth chunk only, and the powers of
-    // gamma stand with the tokens' weights, which are multiplied anyway.
-    const bool slow = g2 >= -20.0f / 128.0f;
+    // S is kept as S / gamma^lag while gamma^128 lies within 2^-20 and 2^20: its
+    // products with gamma then come due every fourth chunk only, and the powers
+    // of gamma stand with the tokens' weights, which are multiplied anyway.
+    // (A gamma far above 1 would take the weights to 0 and gamma^128 to infinity.)
+    const bool slow = fabsf(g2) <= 20.0f / 128.0f;
     int lag = 0;
     // gamma^(i+e) of this lane's tokens, gamma^(i-j) of its part of W, and the
     // weights of the tokens j in the state's update over a whole chunk:

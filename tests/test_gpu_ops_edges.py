@@ -143,6 +143,16 @@ def test_adamw_second_moment_overflows(dtype, master, bits):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_attention_growing_state(dtype):
+    """gamma above 1.  The first tokens have zero keys, so that the state stays small although gamma^T leaves the fp32
+    range."""
+    c = La(T=140, B=2, H=4, G=4, Dk=20, Dv=24, dtype=dtype, decays=[1.0, 0.3, 0.12, 0.05], state=False)
+    c.k[:, :80] = 0
+    c.tk = dev(c.seq(c.k), dtype)
+    c.check_forward(c.forward())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("scale,size", [(1e-30, 1e10), (1e-39, 1.0), (1e25, 1e-10)])
 def test_linear_attention_gradients_at_any_scale(scale, size, dtype):
     """The gradient of the state does not depend on the scale: a row of no tokens passes it on as it is."""
