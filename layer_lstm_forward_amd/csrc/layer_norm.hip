@@ -188,7 +188,8 @@ __global__ __launch_bounds__(TL::THREADS) void k_ln_backward(LnBackward c) {
         for (int v = 0; v < TL::NV; ++v)
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
-                u[v][e] = (u[v][e] - mean) * rstd;  // past the row's end: times a dy of 0
+                // (0 past the row's end, not a dy of 0 times a mean that rstd may have made infinite)
+                u[v][e] = (v * TL::TPR + t) * PER + e < W ? (u[v][e] - mean) * rstd : 0.0f;
                 if (on) {
                     dw[v][e] += g[v][e] * u[v][e];
                     db[v][e] += g[v][e];

@@ -163,3 +163,17 @@ def test_linear_attention_gradients_at_any_scale(scale, size, dtype):
     grads = c.backward()
     c.check_backward(grads)
     assert torch.equal(grads[3][1], c.tdS[1])
+
+
+def test_layer_norm_gradient_of_a_large_constant_row():
+    """The variance is 0 and mean * rstd leaves the fp32 range; the row's own values are all 0 after the norm."""
+    rng = np.random.default_rng(23)
+    z, dy = np.full((3, 8), 1e37, np.float32), draw(rng, (3, 8), "f32")
+    z[1] = draw(rng, (8,), "f32")
+    y, mean, rstd, total = pkg.layer_norm(dev(z))
+    dz, dw, db = pkg.layer_norm_backward(dev(dy), total, mean, rstd)
+    wz, wdw, wdb = ref.layer_norm_backward(dy, z.astype(np.float64))
+    wr = ref.layer_norm(z.astype(np.float64))[2][:, None]
+    close(dz, wz, 64 * U32 * wr * (np.abs(dy) + np.abs(dy).mean(1, keepdims=True)) * 8, "dz")
+    close(dw, wdw, 64 * U32 * 8 * np.abs(dy).sum(0), "dweight")
+    close(db, wdb, 8 * U32 * np.abs(dy).sum(0), "dbias")
