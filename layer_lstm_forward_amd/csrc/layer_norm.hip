@@ -58,16 +58,20 @@ __device__ inline float row_sum(float v, float *lds) {
     return v;
 }
 
-// One 16-byte piece widened, zeros past the row's end; any alignment.
-template <class DT>
-__device__ inline void ln_load(const typename DT::S *p, int i, int W, float *f) {
+// One 16-byte piece widened, zeros past the row's end, or with PAST that value
+// in the storage type; any alignment.
+template <class DT, bool PAST = false>
+__device__ inline void ln_load(const typename DT::S *p, int i, int W, float *f, float past = 0.0f) {
     using S = typename DT::S;
     S t[DT::PER16];
-    if (i + DT::PER16 <= W)
+    if (i + DT::PER16 <= W) {
         __builtin_memcpy(t, p + i, 16);
-    else
+    } else {
+        // (bf16: not rounded ahead, which would wait for it before any load)
+        if (PAST && sizeof(S) == 2) asm volatile("" : "+v"(past));
 #pragma unroll
-        for (int e = 0; e < DT::PER16; ++e) t[e] = i + e < W ? p[i + e] : (S)0;
+        for (int e = 0; e < DT::PER16; ++e) t[e] = i + e < W ? p[i + e] : PAST ? round_to<DT>(past) : (S)0;
+    }
 #pragma unroll
     for (int e = 0; e < DT::PER16; ++e) f[e] = DT::to_f(t[e]);
 }
@@ -179,7 +183,9 @@ __global__ __launch_bounds__(TL::THREADS) void k_ln_backward(LnBackward c) {
         for (int v = 0; v < TL::NV; ++v) {
             const int i = (v * TL::TPR + t) * PER;
             ln_load<DT>(dy, i, W, g[v]);
-            ln_load<DT>(z, i, W, u[v]);
+            // (The mean past the end, not 0: a constant row of large values has an
+            // infinite mean rstd, whose product with a dy of 0 would be NaN.)
+            ln_load<DT, true>(z, i, W, u[v], mean);
 #pragma unroll
             for (int e = 0; e < PER; ++e) add[v][e] = 0.0f;
             if (ds) ln_load<DT>(ds, i, W, add[v]);
@@ -188,8 +194,7 @@ __global__ __launch_bounds__(TL::THREADS) void k_ln_backward(LnBackward c) {
         for (int v = 0; v < TL::NV; ++v)
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
-                // (0 past the row's end, not a dy of 0 times a mean that rstd may have made infinite)
-                u[v][e] = (v * TL::TPR + t) * PER + e < W ? (u[v][e] - mean) * rstd : 0.0f;
+                u[v][e] = (u[v][e] - mean) * rstd;  // past the row's end: times a dy of 0
                 if (on) {
                     dw[v][e] += g[v][e] * u[v][e];
                     db[v][e] += g[v][e];
