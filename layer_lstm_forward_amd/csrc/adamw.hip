@@ -162,7 +162,7 @@ __device__ inline void adamw_part(const AdamwEntry &t, const AdamwHyper &h, long
             for (int x = 0; x < VEC; ++x) root[x] = sqrtf(v[x]);
 #pragma unroll
         for (int x = 0; x < VEC; ++x) {
-            const float step = m[x] * h.inv_bc1 * __builtin_amdgcn_rcpf(fmaf(root[x], h.inv_sqrt_bc2, h.eps));
+            const float step = m[x] * __builtin_amdgcn_rcpf(fmaf(root[x], h.inv_sqrt_bc2, h.eps)) * h.inv_bc1;
             w[x] = w[x] * keep - t.lr * step;
             pv[x] = round_to<DT>(w[x]);
         }

@@ -103,6 +103,7 @@ hipError_t launch_ln_backward(const LnBackward &c, hipStream_t s);
 
 // ---------------------------------------------------------------------- AdamW
 struct AdamwHyper {
+    // step = m / (sqrt(v) inv_sqrt_bc2 + eps) inv_bc1; the last three may carry a common factor
     float beta1, beta2, one_beta1, one_beta2, eps, inv_bc1, inv_sqrt_bc2;
     const float *grad_scale;
     unsigned seed;

@@ -321,9 +321,13 @@ lstm_status lstm_adamw_step(int dtype, int state_bits, const lstm_adamw_tensor *
     h.beta2 = (float)beta2;
     h.one_beta1 = (float)(1.0 - beta1);
     h.one_beta2 = (float)(1.0 - beta2);
-    h.eps = (float)eps;
-    h.inv_bc1 = (float)(1.0 / (1.0 - std::pow(beta1, (double)step)));
-    h.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+    // The kernels multiply by a reciprocal, which is infinite for eps alone
+    // (v = 0) below the normal range, and 0 times it not a number: there both
+    // parts of the quotient are taken 2^30 times as large.
+    const double up = eps > 0.0 && eps < 0x1p-100 ? 0x1p30 : 1.0;
+    h.eps = eps > 0.0 ? (float)std::fmax(eps * up, 0x1p-126) : 0.0f;
+    h.inv_bc1 = (float)(up / (1.0 - std::pow(beta1, (double)step)));
+    h.inv_sqrt_bc2 = (float)(up / std::sqrt(1.0 - std::pow(beta2, (double)step)));
     h.grad_scale = grad_scale;
     h.seed = seed;
     return launched(launch_adamw(dtype, state_bits, tensors, count, h, static_cast<hipStream_t>(stream)));

@@ -142,6 +142,20 @@ def test_adamw_second_moment_overflows(dtype, master, bits):
     assert bool(torch.isfinite(tp[0]).all())
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [1e-46, 1e-40, 1e-38])
+def test_adamw_eps_below_the_normal_range(eps, dtype, bits):
+    """Elements that never had a gradient stay: their step is 0 / eps = 0 for every eps above 0."""
+    import torch
+    p = dev(draw(np.random.default_rng(22), (300,), dtype), dtype)
+    old = p.clone()
+    m, v, scales = pkg.adamw_states([p], bits=bits)
+    for t in (1, 2):
+        pkg.adamw_step([p], [torch.zeros_like(p)], m, v, step=t, eps=eps, weight_decay=0.0, scales=scales, seed=t)
+    assert torch.equal(p, old)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_linear_attention_growing_state(dtype):
     """gamma above 1.  The first tokens have zero keys, so that the state stays small although gamma^T leaves the fp32
