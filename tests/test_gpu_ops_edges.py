@@ -7,7 +7,7 @@ import pytest
 import layer_lstm_forward_amd as pkg
 from layer_lstm_forward_amd import ops
 from oracle import ops as ref
-from tests.test_gpu_ops import DEV, La, U16, U32, close, dev, draw, host, la_tol, ln_tol
+from tests.test_gpu_ops import DEV, La, U16, U32, close, dev, draw, host, ln_tol
 
 pytestmark = pytest.mark.gpu
 
@@ -191,3 +191,144 @@ def test_layer_norm_gradient_of_a_large_constant_row():
     close(dz, wz, 64 * U32 * wr * (np.abs(dy) + np.abs(dy).mean(1, keepdims=True)) * 8, "dz")
     close(dw, wdw, 64 * U32 * 8 * np.abs(dy).sum(0), "dweight")
     close(db, wdb, 8 * U32 * np.abs(dy).sum(0), "dbias")
+
+
+# ------------------------------------- every tile that the launch rules choose
+# (batch row, head) pairs, doubled or tripled by passes, and dims decide; see la_plan
+TILES = {
+    # two column tiles a wave, half of each width: above 192 pairs, or above 1024 tokens
+    "pairs-direct": dict(T=70, B=50, H=4, G=2, Dk=128, Dv=128, packed=True,
+                         lengths=[70, 0, 1, 31, 32, 33, 64, 65, 69] + [70] * 41),
+    "long-direct": dict(T=1100, B=1, H=2, G=1, Dk=128, Dv=128, decays=[-0.2, -0.001]),
+    "long-direct-ragged": dict(T=1060, B=2, H=1, G=1, Dk=128, Dv=128, lengths=[700, 1060], batch_first=True),
+    "pairs-edges": dict(T=45, B=50, H=4, G=2, Dk=72, Dv=104, packed=True, lengths=[45, 0, 1, 32, 33] + [45] * 45),
+    "pairs-short": dict(T=40, B=50, H=4, G=4, Dk=100, Dv=3),
+    # eight waves for fp32: above 128 pairs and values wider than 64
+    "eight-64": dict(T=70, B=33, H=4, G=2, Dk=64, Dv=128, lengths=[70, 0, 1, 31, 32, 33, 64, 65] + [70] * 25),
+    "eight-64-odd": dict(T=40, B=66, H=2, G=1, Dk=50, Dv=90, packed=True),
+    "eight-128-odd": dict(T=40, B=33, H=4, G=1, Dk=101, Dv=127, packed=True, batch_first=True),
+    "eight-short": dict(T=40, B=33, H=4, G=4, Dk=3, Dv=100),
+    "eight-256": dict(T=35, B=65, H=2, G=2, Dk=256, Dv=256, lengths=[35, 0, 1, 32, 33] + [35] * 60),
+    "eight-256-odd": dict(T=35, B=65, H=2, G=1, Dk=200, Dv=250),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", TILES)
+def test_linear_attention_tiles(name, dtype):
+    c = La(dtype=dtype, **TILES[name])
+    print(f"case {name} {dtype} forward", flush=True)
+    c.check_forward(c.forward())
+    print(f"case {name} {dtype} backward", flush=True)
+    c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("B,H", [(1, 2), (50, 4)])
+def test_linear_attention_state_keeps_fp32_products(B, H):
+    """A state that is returned is summed from bf16 operands as if their weighted products were fp32.  Two of the three
+    bf16 terms that a weighted value is split into would leave 2^-17 of it (an rms of about 2.7e-6); fp32 sums of 400
+    terms in chunks of 32 stay near 2^-22."""
+    c = La(T=400, B=B, H=H, G=H, Dk=128, Dv=128, dtype="bf16", decays=[-0.002 * (h + 1) for h in range(H)])
+    few = [0, B - 1]
+    got, grad = host(c.forward()[1])[few], host(c.backward()[3])[few]
+    a = [x[few] for x in (c.q, c.k, c.v, c.do, c.S, c.dS)]
+    want = ref.linear_attention(a[0], a[1], a[2], c.g, c.scale, a[4])[1]
+    wgrad = ref.linear_attention_backward(a[0], a[1], a[2], c.g, c.scale, a[3], a[4], a[5])[3]
+    for x, w, what in ((got, want, "state"), (grad, wgrad, "dstate")):
+        off = np.sqrt(((x - w) ** 2).mean() / (w ** 2).mean())
+        assert off < 1e-6, (what, off)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,G,Dk,Dv", [(130, 4, 2, 40, 72), (260, 2, 2, 200, 128), (520, 1, 1, 16, 36),
+                                         (6, 2, 1, 200, 33), (300, 2, 2, 150, 30)])
+def test_linear_attention_step_tiles(B, H, G, Dk, Dv, dtype):
+    """512 states and more take wider column slabs; rows past the first 128 are a second round there."""
+    rng = np.random.default_rng(B + Dv)
+    q, k = draw(rng, (B, 1, H, Dk), dtype), draw(rng, (B, 1, G, Dk), dtype)
+    v, g = draw(rng, (B, 1, G, Dv), dtype), -rng.uniform(0, 2, H).astype(np.float32)
+    slots = rng.permutation(B + 3)[:B].astype(np.int32)
+    slots[1] = -1
+    busy = slots >= 0
+    pool = draw(rng, (B + 3, H, Dk, Dv), "f32")
+    at = np.where(busy, slots, 0)
+    wo, ws = ref.linear_attention(q, k, v, g, Dk ** -0.5, pool[at])
+    Ao, As = ref.linear_attention(np.abs(q), np.abs(k), np.abs(v), g, Dk ** -0.5, np.abs(pool[at]))
+    tp = dev(pool)
+    o = pkg.linear_attention_step(*(dev(x[:, 0], dtype) for x in (q, k, v)), dev(g), tp, slots=dev(slots))
+    want, tol = pool.astype(np.float64), np.zeros(pool.shape)
+    want[slots[busy]], tol[slots[busy]] = ws[busy], 4 * U32 * As[busy] + 1e-30
+    close(tp, want, tol, "pool")
+    wo = np.where(busy[:, None, None, None], wo, 0.0)
+    close(o, wo[:, 0], ((Dk + 8) * U32 * Ao + (U16 * np.abs(wo) if dtype == "bf16" else 0) + 1e-30)[:, 0], "o")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,width", [(9, 1025), (700, 1536), (5, 2048), (6, 2047), (530, 2048), (5, 2049),
+                                        (260, 6001)])
+def test_layer_norm_tiles(rows, width, dtype):
+    rng = np.random.default_rng(rows + width)
+    x, res, dy, ds = (draw(rng, (rows, width), dtype) for _ in range(4))
+    w, b = draw(rng, (width,), dtype), draw(rng, (width,), dtype)
+    t = lambda a: dev(a, dtype)  # noqa: E731
+    y, mean, rstd, total = pkg.layer_norm(t(x), t(w), t(b), residual=t(res))
+    z = host(total)
+    half = U16 if dtype == "bf16" else 2 * U32
+    close(total, x.astype(np.float64) + res, half * np.abs(x.astype(np.float64) + res), "sum")
+    wy, wm, wr = ref.layer_norm(z, w, b)
+    unit = (z - wm[:, None]) * wr[:, None]
+    tol, rel = ln_tol(z, w.astype(np.float64), unit, wr, dtype)
+    close(y, wy, tol + half * np.abs(wy) + 4 * U32 * np.abs(b.astype(np.float64)) + half * 1e-30, "y")
+    close(mean, wm, (width / 64 + 16) * U32 * np.abs(z).mean(1) + 1e-30, "mean")
+    close(rstd, wr, rel * wr, "rstd")
+    dz, dw, db = pkg.layer_norm_backward(t(dy), total, mean, rstd, t(w), dsum=t(ds))
+    wz, wdw, wdb = ref.layer_norm_backward(dy, z, w, dsum=ds)
+    g = np.abs(dy.astype(np.float64) * w)
+    A = wr[:, None] * (g + g.mean(1, keepdims=True)
+                       + (np.abs(unit) + 1) * (g * (np.abs(unit) + 1)).mean(1, keepdims=True))
+    close(dz, wz, 4 * rel[:, None] * A + 4 * U32 * np.abs(ds) + half * np.abs(wz), "dz")
+    close(dw, wdw, (np.abs(dy) * (np.abs(unit) + 1) * (2 * rel + rows * U32)[:, None]).sum(0) + half * np.abs(wdw),
+          "dweight")
+    close(db, wdb, (rows + 4) * U32 * np.abs(dy.astype(np.float64)).sum(0) + half * np.abs(wdb), "dbias")
+
+
+@pytest.mark.parametrize("dtype,master,bits", [("bf16", False, 32), ("bf16", True, 32), ("f32", False, 8),
+                                               ("bf16", False, 8), ("bf16", True, 8)])
+def test_adamw_large_lists(dtype, master, bits):
+    """2^23 elements and more take four pieces a thread: whole ones, a tensor's end, and one that starts at an odd
+    element."""
+    import torch
+    rng = np.random.default_rng(24)
+    shapes = [((1 << 23) + 777, 0), (5000, 0), (20001, 1)]
+    p, g = [draw(rng, (n,), dtype) for n, _ in shapes], [draw(rng, (n,), dtype, 1e-2) for n, _ in shapes]
+
+    def put(a, dt, off):
+        t = torch.empty(a.size + off, dtype=torch.bfloat16 if dt == "bf16" else torch.float32, device=DEV)[off:]
+        t.copy_(dev(a, dt))
+        return t
+
+    tp, tg = ([put(a, dtype, off) for a, (_, off) in zip(x, shapes)] for x in (p, g))
+    masters = [put(a, "f32", off) for a, (_, off) in zip(p, shapes)] if master else None
+    m, v, scales = pkg.adamw_states(tp, bits=bits)
+    pkg.adamw_step(tp, tg, m, v, step=1, lr=1e-2, scales=scales, masters=masters, seed=5)
+    values = ref.code_values()
+    for i, (a, b) in enumerate(zip(p, g)):
+        wp, wm, wv = ref.adamw(a, b, 0.0, 0.0, 1, 1e-2, 0.9, 0.999, 1e-8, 0.01)
+        step = np.abs(1e-2 * (wm / (1 - 0.9)) / (np.sqrt(wv / (1 - 0.999)) + 1e-8))
+        tol = 16 * U32 * (np.abs(wp) + 4 * step)
+        if master:
+            close(masters[i], wp, tol, "master")
+            assert torch.equal(masters[i].to(torch.bfloat16), tp[i])
+        else:
+            close(tp[i], wp, tol + (U16 * np.abs(wp) if dtype == "bf16" else 0), "param")
+        if bits == 32:
+            close(m[i], wm, 16 * U32 * np.abs(wm), "m")
+            close(v[i], wv, 24 * U32 * np.abs(wv), "v")
+            continue
+        for got, sc, want in ((m[i], scales[0][i], wm), (v[i], scales[1][i], np.sqrt(wv))):
+            top = np.maximum.reduceat(np.abs(want), np.arange(0, want.size, 256))
+            assert np.array_equal(host(sc), np.exp2(np.maximum(np.floor(np.log2(np.maximum(top, 1e-300))) - 7, -126.0)))
+            s = np.repeat(host(sc), 256)[:want.size]
+            x = values[got.view(torch.uint8).cpu().numpy()] * s
+            unit = np.exp2(np.floor(np.log2(np.maximum(np.abs(want) / s, 2.0 ** -6))) - 3) * s
+            assert np.all(np.abs(x - want) <= unit * (1 + 1e-4))
