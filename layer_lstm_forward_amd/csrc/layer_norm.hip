@@ -321,24 +321,30 @@ __global__ __launch_bounds__(256) void k_ln_dw_wide(LnBackward c) {
 }
 
 // The workgroups' partial sums, in their order: 8 threads take every eighth of
-// a column's, then their sums are added.
+// a column's, then their sums are added.  A grid holds fewer than 2^32 threads,
+// which the widest rows would need here, so workgroups go on to further columns.
+constexpr unsigned kJoinBlocks = 1 << 20;
 template <class DT>
 __global__ __launch_bounds__(256) void k_ln_join(LnBackward c, int parts) {
     using S = typename DT::S;
     __shared__ float lds[8][32];
-    const int W2 = 2 * c.width, x = threadIdx.x % 32, y = threadIdx.x / 32, i = blockIdx.x * 32 + x;
-    float sum = 0.0f;
-    if (i < W2)
+    const int W2 = 2 * c.width, x = threadIdx.x % 32, y = threadIdx.x / 32;
+    for (int i0 = blockIdx.x * 32; i0 < W2; i0 += gridDim.x * 32) {
+        const int i = i0 + x;
+        float sum = 0.0f;
+        if (i < W2)
 #pragma unroll 8
-        for (int p = y; p < parts; p += 8) sum += c.part[(size_t)p * W2 + i];
-    lds[y][x] = sum;
-    __syncthreads();
-    if (y > 0 || i >= W2) return;
-    sum = 0.0f;
+            for (int p = y; p < parts; p += 8) sum += c.part[(size_t)p * W2 + i];
+        if (i0 != (int)blockIdx.x * 32) __syncthreads();  // the sums before have been read
+        lds[y][x] = sum;
+        __syncthreads();
+        if (y > 0 || i >= W2) continue;
+        sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += lds[k][x];
-    S *out = reinterpret_cast<S *>(i < c.width ? c.dw : c.db);
-    if (out) out[i < c.width ? i : i - c.width] = round_to<DT>(sum);
+        for (int k = 0; k < 8; ++k) sum += lds[k][x];
+        S *out = reinterpret_cast<S *>(i < c.width ? c.dw : c.db);
+        if (out) out[i < c.width ? i : i - c.width] = round_to<DT>(sum);
+    }
 }
 
 // The smallest tile that a row fits: f(LnTile) for it, else wide().
@@ -403,7 +409,7 @@ hipError_t ln_backward(const LnBackward &c, hipStream_t s) {
                 hipLaunchKernelGGL(k_ln_dx_wide<DT>, dim3(blocks_of(c.rows, 1, 65536)), dim3(256), 0, s, c);
             });
     if (c.dw || c.db)
-        hipLaunchKernelGGL(k_ln_join<DT>, dim3((2 * c.width + 31) / 32), dim3(256), 0, s, c, parts);
+        hipLaunchKernelGGL(k_ln_join<DT>, dim3(blocks_of(2ll * c.width, 32, kJoinBlocks)), dim3(256), 0, s, c, parts);
     return hipGetLastError();
 }
 

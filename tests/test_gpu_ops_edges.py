@@ -332,3 +332,25 @@ def test_adamw_large_lists(dtype, master, bits):
             x = values[got.view(torch.uint8).cpu().numpy()] * s
             unit = np.exp2(np.floor(np.log2(np.maximum(np.abs(want) / s, 2.0 ** -6))) - 3) * s
             assert np.all(np.abs(x - want) <= unit * (1 + 1e-4))
+
+
+def test_layer_norm_widest_rows():
+    """2^28 values, the limit: one row, and its weight gradients."""
+    import torch
+    width = 1 << 28
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(25)
+    x, dy = (torch.randn(1, width, generator=gen, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    y, mean, rstd, z = pkg.layer_norm(x)
+    dz, dw, db = pkg.layer_norm_backward(dy, z, mean, rstd)
+    m = x.double().mean()
+    # chains of 2^20 additions: of values of both signs they wander, by about the root of their number
+    assert abs(float(mean[0]) - float(m)) < 2 ** 10 * 24 * U32
+    assert abs(float(rstd[0]) - float((x.double() - m).square().mean() + 1e-5) ** -0.5) < 1e-3
+    unit = (x.float() - mean) * rstd
+    for a, b, what in ((y[0], unit[0], "y"), (dw, (dy.float() * unit)[0], "dweight"), (db, dy[0].float(), "dbias")):
+        # the statistics are the kernel's own: three roundings and the result's
+        assert bool(((a.float() - b).abs() <= (U16 + 4 * U32) * b.abs() + 1e-30).all()), what
+    g = dy.float()
+    want = rstd * (g - g.double().mean().float() - unit * (g * unit).double().mean().float())
+    assert bool(((dz.float() - want).abs() <= 2 * U16 * want.abs() + 1e-3).all())
