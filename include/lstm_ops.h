@@ -9,7 +9,9 @@
  * stream argument (NULL = default stream); an lstm_status from every call;
  * host checks before anything is enqueued; no exception crosses the
  * interface; nothing is allocated.  Calls may be captured into a graph.
- * Dtypes: LSTM_F32 and LSTM_BF16 (arithmetic, states and statistics fp32).
+ * Dtypes: LSTM_F32 and LSTM_BF16.  Sums, states and statistics are fp32, and
+ * so is all arithmetic but for two operands of whole bf16 sequences (see
+ * lstm_linear_attention_forward).
  */
 #ifndef LSTM_AMD_LSTM_OPS_H
 #define LSTM_AMD_LSTM_OPS_H
@@ -63,6 +65,14 @@ lstm_status lstm_linear_attention_backward_workspace_size(const lstm_linear_atte
  *   o            view with heads heads, written
  *   state_out    like state: the state after each row's last token, or NULL.
  *                It may be the memory of `state` (then updated in place).
+ * LSTM_BF16: o is rounded to bf16, and so are two operands of the matrix
+ * instructions on the way to it: the state where a chunk's tokens read it, and
+ * the decayed q k^T inside a chunk (o is off by 0.0023 of its size, rms; its
+ * own rounding alone is 0.0017).  The state itself is summed in fp32, from
+ * products to 2^-24 (to 2^-17 where it is not returned and so enters bf16
+ * results only).  The gradients are computed alike.  A single token
+ * (lstm_linear_attention_step) rounds o alone, so a prompt and its tokens one
+ * by one differ by those operands' roundings.
  * LSTM_ERR_ARG: NULL argument, a dim outside 1..256, heads not a multiple of
  * kv_heads, a scale that is 0 or not finite; LSTM_ERR_SHAPE: T or B < 1, T
  * above its limit, B * heads above 2^20, a time stride of 2^31 bytes;

@@ -125,7 +125,10 @@ struct LaTile {
     }
     // Piece p of LDS row j lies at p ^ key(j): the 16 rows that a fragment
     // read touches, and the 4 rows x 4 pieces of a transposed read, then all
-    // fall on different banks (64 banks of 4 bytes).
+    // fall on different places of 16 bytes.  A transposed read takes the same
+    // 8 bytes of every place, half of the 64 banks, so it lasts twice its
+    // minimum: conflicts are counted in half of the LDS cycles of the pass that
+    // reads only so (k_la with STATE_ONLY), which LDS does not bound.
     template <int R>
     __device__ static int key(int j) {
         if (TPK == 1) return j & 15;
@@ -315,7 +318,10 @@ __device__ inline u32x4 la_cols(const typename DT::S *lds, int ju, F col4, int l
     }
 }
 
-// Accumulators of TPK row tiles as one fragment (bf16: rounded here, once).
+// Accumulators of TPK row tiles as one fragment.  bf16: S is rounded here, once,
+// as an operand; the sum itself stays fp32.  With the rounding of (A B^T) . W
+// this takes o's error from 0.0017 of its size, rms (its own rounding), to 0.0023;
+// two terms for each operand would be 20 more matrix instructions to a chunk's 56.
 template <class DT, class TL>
 __device__ inline u32x4 la_pack(const f32x4 *acc, int stride) {
     if constexpr (TL::TPK == 2) {
@@ -678,7 +684,7 @@ __global__ __launch_bounds__(TL::THREADS, 2) void k_la(LaCall c, int slabs) {
                         P[r] = ri >= TL::row_of(jt, g, r) ? P[r] * mask_w[x][r] : 0.0f;
                     }
                 }
-                if constexpr (TL::TPK == 2)
+                if constexpr (TL::TPK == 2)  // rounded here, once, as S is in la_pack
                     *reinterpret_cast<bf16x4 *>(&ps[it][lane][4 * jt]) = __builtin_convertvector(P, bf16x4);
                 else
                     *reinterpret_cast<f32x4 *>(&ps[it * 2 + jt][lane][0]) = P;

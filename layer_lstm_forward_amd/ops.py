@@ -284,6 +284,8 @@ def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, b
     state: None or [B, heads, key_dim, value_dim] float32, from an earlier call.
     lengths: None, B host ints in 0..T, or an int32 device tensor; tokens past a row's length are not read.
     out: None or (o, state_out) to write into; state_out may be `state`.
+    bfloat16: the state, where tokens read it, and the products of a chunk's queries and keys are rounded as operands
+    (linear_attention_step rounds its result alone).
     Returns (o, state_out)."""
     if torch is None:
         _need_torch()
