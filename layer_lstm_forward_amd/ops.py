@@ -251,7 +251,7 @@ class _Shape:
                 or not log_decay.is_contiguous():
             raise ValueError(f"log_decay must be {H} contiguous float32 values on {q.device}")
         self.heads, self.key_dim, self.value_dim, self.B = H, Dk, Dv, B
-        self.packed = _pack_shape(code, T, B, H, G, Dk, Dv, Dk ** -0.5 if scale is None else scale)
+        self.packed = _pack_shape(code, T, B, H, G, Dk, Dv, (Dk or 1) ** -0.5 if scale is None else scale)
 
 
 def _lengths(lengths, T, B, device):
@@ -385,11 +385,15 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
     return out
 
 
-def _rows(t, what):
-    """A tensor whose leading axes are evenly spaced rows (copied if they are not), the spacing, and their number."""
+def _width(t, what):
     if t.dim() == 0 or t.shape[-1] == 0:
         raise ValueError(f"{what} must have a last axis")
-    width = t.shape[-1]
+    return t.shape[-1]
+
+
+def _rows(t, what):
+    """A tensor whose leading axes are evenly spaced rows (copied if they are not), the spacing, and their number."""
+    width = _width(t, what)
     if t.is_contiguous():
         return t, width, t.numel() // width
     if t.dim() != 2 or (width > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < width):
@@ -405,7 +409,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, stream=None):
     if torch is None:
         _need_torch()
     code = _code(x, "x")
-    width = x.shape[-1]
+    width = _width(x, "x")
     for t, what in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _dense(t, x, what, (width,))
@@ -436,7 +440,7 @@ def layer_norm_backward(dy, z, mean, rstd, weight=None, dsum=None, stream=None):
     if torch is None:
         _need_torch()
     code = _code(z, "z")
-    width = z.shape[-1]
+    width = _width(z, "z")
     _same(dy, z, "dy", z.shape)
     for t, what in ((mean, "mean"), (rstd, "rstd")):
         _dense(t, z, what, z.shape[:-1], torch.float32)

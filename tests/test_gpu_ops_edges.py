@@ -354,3 +354,27 @@ def test_layer_norm_widest_rows():
     g = dy.float()
     want = rstd * (g - g.double().mean().float() - unit * (g * unit).double().mean().float())
     assert bool(((dz.float() - want).abs() <= 2 * U16 * want.abs() + 1e-3).all())
+
+
+def test_refusals_of_empty_axes():
+    import torch
+    one = torch.ones((), device=DEV)
+    with pytest.raises(ValueError):
+        pkg.layer_norm(one)
+    with pytest.raises(ValueError):
+        pkg.layer_norm_backward(one, one, one, one)
+    for shape in ((3, 0), (0,)):
+        x = torch.ones(shape, device=DEV)
+        with pytest.raises(ValueError):
+            pkg.layer_norm(x)
+    g = torch.zeros(2, device=DEV)
+    for T, B, H, D in ((0, 1, 2, 8), (3, 0, 2, 8), (3, 1, 2, 0)):
+        q, S = torch.ones(T, B, H, D, device=DEV), torch.ones(B, H, D, D, device=DEV)
+        for scale in (None, 1.0):
+            with pytest.raises((ValueError, pkg.LSTMError)):
+                pkg.linear_attention(q, q, q, g, scale=scale)
+            with pytest.raises((ValueError, pkg.LSTMError)):
+                pkg.linear_attention_backward(q, q, q, g, q, scale=scale)
+            if T:
+                with pytest.raises((ValueError, pkg.LSTMError)):
+                    pkg.linear_attention_step(q[0], q[0], q[0], g, S, scale=scale)
