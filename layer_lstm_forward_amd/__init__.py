@@ -499,3 +499,6 @@ class LSTM:
 # operators beside the recurrent layers (include/lstm_ops.h)
 from .ops import (adamw_states, adamw_step, layer_norm, layer_norm_backward, linear_attention,  # noqa: E402,F401
                   linear_attention_backward, linear_attention_step)
+# and those that make blocks of a model (include/lstm_blocks.h)
+from .block_ops import (gated_mlp, gated_mlp_backward, gated_mlp_train, gated_recurrence,  # noqa: E402,F401
+                        gated_recurrence_backward, gated_recurrence_step, rotary, rotary_backward, rotary_frequencies)

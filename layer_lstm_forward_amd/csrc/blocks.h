@@ -1,0 +1,116 @@
+// blocks.h -- launchers of the operators of include/lstm_blocks.h (host side).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+
+#include "../../include/lstm_blocks.h"
+
+namespace lstm_amd {
+
+// ----------------------------------------------------------- gated recurrence
+// A [T, B, width] tensor: element strides of time and batch, channels dense.
+struct GrView {
+    char *p;
+    long long t, b;
+};
+struct GrCall {
+    GrView x, f, i, y;     // i.p null: the input gate is 1 - the forget gate's
+    GrView dy, dx, df, di; // backward only
+    const int *lengths;    // or null
+    const float *s0;       // state before the first token, or null
+    float *s1;             // state after the last, or null
+    const float *ds1;      // gradient of s1, or null
+    float *ds0;            // gradient of s0, or null
+    float *seg;            // workspace: [2][nseg][B][width], or null (one segment)
+    int T, B, width, dtype;
+    int nseg, seg_tokens;
+};
+// Segments a sequence is cut into, and their tokens.
+void gr_segments(int T, int B, int width, int dtype, bool backward, int *nseg, int *seg_tokens);
+hipError_t launch_gr_forward(const GrCall &c, hipStream_t s);
+hipError_t launch_gr_backward(const GrCall &c, hipStream_t s);
+
+struct GrStep {
+    GrView x, f, i, y;
+    const int *slots;
+    float *pool;
+    int n_slots, B, width, dtype;
+};
+hipError_t launch_gr_step(const GrStep &c, hipStream_t s);
+
+// --------------------------------------------------------------------- rotary
+// A [T, B, heads, dim] tensor: element strides, the last axis dense.
+struct RotView {
+    char *p;
+    long long t, b, h;
+};
+struct RotSide {  // queries or keys
+    RotView x, y;   // forward: input and output; backward: input and gradient of the output
+    RotView dx;     // backward
+    const char *w;  // norm weight or null
+    char *dw;       // backward: its gradient or null
+    int heads;
+};
+struct RotCall {
+    RotSide side[2];
+    const double *freq;      // [rot / 2] radians a position
+    const int *pos;          // or null: the token's index
+    long long pos_t, pos_b;
+    float *part;             // backward: [parts][2][dim] sums of the weight gradients, or null
+    int T, B, dim, rot, pairs, norm, dtype, parts;
+    float eps, scale;
+};
+// Runs of heads that a workgroup takes of a token, and workgroups that keep sums of a run's weight gradients.
+int rot_runs(int heads);
+int rot_parts(long long tokens, int runs);
+hipError_t launch_rot_forward(const RotCall &c, hipStream_t s);
+hipError_t launch_rot_backward(const RotCall &c, hipStream_t s);
+
+// ------------------------------------------------------------------ gated MLP
+// Operands of the products are bf16: a bf16 matrix itself, or three bf16
+// matrices (planes) whose sum is an fp32 matrix to 2^-24.
+struct MlpOperand {
+    const char *p;     // first plane
+    size_t plane;      // bytes from plane to plane
+    long long ld;      // elements from row to row
+};
+// One product C[m][n] = sum over k of A[m][k] B[n][k], k running over `lists`
+// pairs of operands one after the other.  An operand is stored with k along
+// its rows (a[m][k]) or along its columns (a[k][m]), which the launch says.
+struct MlpProduct {
+    MlpOperand a[2], b[2];
+    int M, N, K, lists;
+    char *out;         // STORE: [M][ldo] of the call's dtype
+    long long ldo;
+    int vec;           // STORE: rows of out are 16-byte aligned
+    int tiles_m, tiles_n;
+};
+enum MlpEpilogue { MLP_STORE = 0, MLP_GATE = 1, MLP_DGATE = 2 };
+struct MlpCall {
+    MlpProduct p[3];
+    int count, dtype, act;
+    int epilogue, a_cols, b_cols;  // a_cols: A is stored as a[k][m]
+    // MLP_GATE: b[0] and b[1] are the weights of gate and up, products of one
+    // pass.  product receives act(g) u in planes, gate and up g and u (null: not kept).
+    // MLP_DGATE: gate and up are read, dgate and dup receive the gradients in planes.
+    char *gate, *up;
+    MlpOperand product, dgate, dup;
+    long long ld;      // of gate and up
+    float *part;       // partial sums where the contraction is split
+    int splits;
+};
+// Tile of a launch and into how many parts its contraction is split.
+struct MlpPlan {
+    int tile, splits;
+    size_t floats;  // partial sums
+};
+MlpPlan mlp_plan(const MlpCall &c);
+hipError_t launch_mlp(const MlpCall &c, hipStream_t s);
+// src [rows][cols] of dtype (ld elements from row to row) as bf16 planes (one, or three for fp32) of rows `to.ld`
+// long, the columns past cols 0.
+hipError_t launch_mlp_planes(int dtype, const void *src, long long ld, long long rows, int cols, const MlpOperand &to,
+                             hipStream_t s);
+
+}  // namespace lstm_amd

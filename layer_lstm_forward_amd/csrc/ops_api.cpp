@@ -7,14 +7,13 @@
 #include <cstdint>
 
 #include "../../include/lstm_ops.h"
-#include "host.h"
 #include "ops.h"
+#include "ops_host.h"
 
 using namespace lstm_amd;
 
 namespace {
 
-constexpr size_t kAlign = 256;
 constexpr int kMaxDim = 256;
 constexpr int kMaxWidth = 1 << 28;         // of a normalised row
 constexpr long long kMaxRows = 1 << 20;  // (batch row, head) pairs
@@ -22,30 +21,6 @@ constexpr long long kMaxRows = 1 << 20;  // (batch row, head) pairs
 // most 512, each of whole chunks of 32: less than 2^14 past T) and the two
 // chunks loaded ahead.
 constexpr int kMaxTokens = INT_MAX - (1 << 15);
-
-size_t elem(int dtype) { return dtype == LSTM_BF16 ? 2 : 4; }
-
-// acc += a * b * c * d bytes, 256-byte aligned; false on overflow.
-bool add_bytes(size_t *acc, size_t a, size_t b, size_t c, size_t d) {
-    size_t n;
-    if (__builtin_mul_overflow(a, b, &n) || __builtin_mul_overflow(n, c, &n) || __builtin_mul_overflow(n, d, &n))
-        return false;
-    if (n > SIZE_MAX / 4 - *acc) return false;
-    *acc += (n + kAlign - 1) / kAlign * kAlign;
-    return true;
-}
-
-lstm_status current_device(int *dev) {
-    if (hipGetDevice(dev) == hipSuccess) return LSTM_OK;
-    (void)hipGetLastError();
-    return LSTM_ERR_DEVICE;
-}
-
-lstm_status launched(hipError_t e) {
-    if (e == hipSuccess) return LSTM_OK;
-    (void)hipGetLastError();
-    return LSTM_ERR_LAUNCH;
-}
 
 lstm_status check_shape(const lstm_linear_attention_shape *s) {
     if (!s) return LSTM_ERR_ARG;
@@ -59,19 +34,10 @@ lstm_status check_shape(const lstm_linear_attention_shape *s) {
     return LSTM_OK;
 }
 
-bool view_ok(const lstm_view *v) { return v && v->data; }
-
 // Token to token the kernels step by 32-bit byte counts.
 bool steps_ok(const lstm_linear_attention_shape *s, const lstm_view *v) {
     const long long most = INT_MAX / (long long)elem(s->dtype);
     return v->time >= -most && v->time <= most;
-}
-
-// Every pointer of the list that is given lies on the device.
-bool all_on_device(const void *const *p, int n, int dev) {
-    for (int i = 0; i < n; ++i)
-        if (p[i] && !is_device_ptr(p[i], dev)) return false;
-    return true;
 }
 
 LaTensor tensor(const lstm_view *v, int hdiv) {
