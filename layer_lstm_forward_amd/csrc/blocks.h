@@ -76,6 +76,12 @@ struct MlpOperand {
     size_t plane;      // bytes from plane to plane
     long long ld;      // elements from row to row
 };
+// g or u as the forward keeps it: [rows][ld] fp32, or the upper 16 bits of each
+// value and `low` bytes further on eight more.
+struct MlpKept {
+    char *p;
+    size_t low;
+};
 // One product C[m][n] = sum over k of A[m][k] B[n][k], k running over `lists`
 // pairs of operands one after the other.  An operand is stored with k along
 // its rows (a[m][k]) or along its columns (a[k][m]), which the launch says.
@@ -95,15 +101,16 @@ struct MlpCall {
     // MLP_GATE: b[0] and b[1] are the weights of gate and up, products of one
     // pass.  product receives act(g) u in planes, gate and up g and u (null: not kept).
     // MLP_DGATE: gate and up are read, dgate and dup receive the gradients in planes.
-    char *gate, *up;
+    MlpKept gate, up;
     MlpOperand product, dgate, dup;
-    long long ld;      // of gate and up
+    long long ld;      // elements from row to row of all of these
     float *part;       // partial sums where the contraction is split
-    int splits;
+    int whole, splits, units;  // set by launch_mlp, as in MlpPlan
 };
-// Tile of a launch and into how many parts its contraction is split.
+// How a launch is cut up: its tile, the first `whole` tiles as they are, each of
+// the other split_tiles in `splits` parts; workgroups take `units` of these.
 struct MlpPlan {
-    int tile, splits;
+    int tile, whole, splits, split_tiles, units;
     size_t floats;  // partial sums
 };
 MlpPlan mlp_plan(const MlpCall &c);

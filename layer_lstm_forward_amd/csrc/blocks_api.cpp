@@ -135,18 +135,25 @@ struct Carver {
 };
 
 struct Reserve {
-    char *gate, *up;
+    MlpKept gate, up;
     MlpOperand product;
-    long long ld;
     size_t bytes;
     bool ok;
 };
 Reserve reserve_of(const lstm_gated_mlp_shape *s, const void *at) {
     Carver k{static_cast<char *>(const_cast<void *>(at))};
     Reserve r;
-    r.ld = padded(s->hidden);
-    r.gate = k.take((size_t)s->rows, (size_t)r.ld, elem(s->dtype));
-    r.up = k.take((size_t)s->rows, (size_t)r.ld, elem(s->dtype));
+    auto kept = [&]() {
+        MlpKept o;
+        const size_t ld = (size_t)padded(s->hidden);
+        const size_t before = k.used;
+        o.p = k.take((size_t)s->rows, ld, elem(s->dtype));
+        o.low = k.used - before;
+        if (s->dtype == LSTM_BF16) (void)k.take((size_t)s->rows, ld, 1);
+        return o;
+    };
+    r.gate = kept();
+    r.up = kept();
     r.product = k.operand(s, (size_t)s->rows, s->hidden);
     r.bytes = k.used;
     r.ok = k.ok;
@@ -227,7 +234,6 @@ MlpCall mlp_call(const lstm_gated_mlp_shape *s, int epilogue, int a_cols, int b_
     c.a_cols = a_cols;
     c.b_cols = b_cols;
     c.ld = padded(s->hidden);
-    c.splits = 1;
     return c;
 }
 
@@ -306,12 +312,13 @@ Backward backward_of(const lstm_gated_mlp_shape *s, const void *x, long long xs,
     if (dwu || sizes) f.dw.p[f.dw.count++] = stored(s, f.hidden.dup, ox, s->hidden, s->in, s->rows, dwu);
     if (dwd || sizes) f.dw.p[f.dw.count++] = stored(s, oy, r.product, s->out, s->hidden, s->rows, dwd);
     size_t floats = most(mlp_plan(f.hidden).floats, mlp_plan(f.dx).floats);
-    // a single weight's product may be split where three together are not
-    MlpCall one = f.dw;
-    for (int i = 0; i < 3 && sizes; ++i) {
-        one.count = 1;
-        one.p[0] = f.dw.p[i];
-        floats = most(floats, mlp_plan(one).floats);
+    // whichever of the weights' gradients a call asks for
+    MlpCall some = f.dw;
+    for (int wanted = 1; wanted < 8 && sizes; ++wanted) {
+        some.count = 0;
+        for (int i = 0; i < 3; ++i)
+            if (wanted >> i & 1) some.p[some.count++] = f.dw.p[i];
+        floats = most(floats, mlp_plan(some).floats);
     }
     if (f.dw.count) floats = most(floats, mlp_plan(f.dw).floats);
     f.hidden.part = f.dx.part = f.dw.part = reinterpret_cast<float *>(k.take(floats, sizeof(float), 1));

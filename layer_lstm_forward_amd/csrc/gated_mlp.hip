@@ -23,49 +23,41 @@ constexpr int KS = 64;  // of the contraction, a stage
 __device__ constexpr int kPairA[6] = {2, 1, 0, 1, 0, 0}, kPairB[6] = {0, 1, 2, 0, 1, 0};
 
 // ------------------------------------------------------------- elementwise
-struct Act {
-    float a, slope;  // act(g), act'(g)
-};
-
+// act(g) and, with SLOPE, act'(g) of eight values.
 template <bool SLOPE>
-__device__ inline Act activate(int kind, float g) {
-    Act r;
-    r.slope = 0.0f;
+__device__ inline void activate(int kind, const float *g, float *a, float *slope) {
     if (kind == LSTM_ACT_GELU) {
         // g s(2t), t = k (g + c g^3); past |g| = 32 s is 0 or 1 in fp32, and
         // the clamp keeps 0 times infinity out of the slope
         constexpr float k = 0.7978845608028654f, c = 0.044715f;
-        const float q = fminf(fmaxf(g, -32.0f), 32.0f), q2 = q * q;
-        const float t = 2.0f * k * q * (1.0f + c * q2), p = sigmoid_f(t);
-        r.a = g * p;
-        if (SLOPE) r.slope = p + q * (p * sigmoid_f(-t)) * (2.0f * k * (1.0f + 3.0f * c * q2));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = fminf(fmaxf(g[i], -32.0f), 32.0f), q2 = q * q;
+            const float t = 2.0f * k * q * (1.0f + c * q2), p = sigmoid_f(t);
+            a[i] = g[i] * p;
+            if (SLOPE) slope[i] = p + q * (p * sigmoid_f(-t)) * (2.0f * k * (1.0f + 3.0f * c * q2));
+        }
+    } else if (kind == LSTM_ACT_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] = sigmoid_f(g[i]);
+            if (SLOPE) slope[i] = a[i] * sigmoid_f(-g[i]);
+        }
     } else {
-        const float p = sigmoid_f(g), n = sigmoid_f(-g);
-        if (kind == LSTM_ACT_SIGMOID) {
-            r.a = p;
-            if (SLOPE) r.slope = p * n;
-        } else {
-            r.a = g * p;
-            if (SLOPE) r.slope = p + r.a * n;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p = sigmoid_f(g[i]);
+            a[i] = g[i] * p;
+            if (SLOPE) slope[i] = fmaf(a[i], 1.0f - p, p);
         }
     }
-    return r;
 }
+
+typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 __device__ inline u32x4 pack8(const float *v) {
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = (uint32_t)round_to<BF16>(v[2 * i]) | (uint32_t)round_to<BF16>(v[2 * i + 1]) << 16;
-    return o;
-}
-
-__device__ inline void unpack8(u32x4 x, float *v) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(x[i] << 16);
-        v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-    }
+    const bf16x8 x = __builtin_convertvector(f32x8{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}, bf16x8);
+    return __builtin_bit_cast(u32x4, x);
 }
 
 // The first term of an fp32 value, to nearest; the largest finite values, whose
@@ -75,10 +67,21 @@ __device__ inline float first_term(float v) {
     return fabsf(t) <= 3.4e38f ? t : __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
 }
 
-// Eight values as an operand's planes at element `at`.
+// Where a lane's eight values are in a matrix: element base (the same for all
+// lanes of a wave, so that it costs scalar instructions only) + off.
+struct Place {
+    size_t base;
+    unsigned off;
+    template <class T>
+    __device__ T *in(const char *p, int size) const {
+        return reinterpret_cast<T *>(const_cast<char *>(p) + base * size + off * (unsigned)size);
+    }
+};
+
+// Eight values as an operand's planes.
 template <bool F32_>
-__device__ inline void store_planes(const MlpOperand &o, size_t at, const float *v) {
-    char *p = const_cast<char *>(o.p) + at * 2;
+__device__ inline void store_planes(const MlpOperand &o, Place at, const float *v) {
+    char *p = at.in<char>(o.p, 2);
     if constexpr (!F32_) {
         *reinterpret_cast<u32x4 *>(p) = pack8(v);
     } else {
@@ -93,67 +96,114 @@ __device__ inline void store_planes(const MlpOperand &o, size_t at, const float 
     }
 }
 
-// Eight values of a matrix of the call's dtype, 16-byte aligned.
-template <bool F32_>
-__device__ inline void load8(const char *p, size_t at, float *v) {
-    if constexpr (F32_) {
-        const f32x4 *q = reinterpret_cast<const f32x4 *>(p + at * 4);
-        const f32x4 x = q[0], y = q[1];
+// Eight fp32 values, 16-byte aligned.
+__device__ inline void load8f(const float *p, float *v) {
+    const f32x4 x = reinterpret_cast<const f32x4 *>(p)[0], y = reinterpret_cast<const f32x4 *>(p)[1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = x[i], v[4 + i] = y[i];
-    } else {
-        unpack8(*reinterpret_cast<const u32x4 *>(p + at * 2), v);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = x[i], v[4 + i] = y[i];
+}
+__device__ inline void store8f(float *p, const float *v) {
+    reinterpret_cast<f32x4 *>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4 *>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
 }
 
+// g and u as they are kept for the backward call.  fp32 calls keep all bits,
+// bf16 calls the upper 24: 16, and eight more in a plane of bytes behind them.
+// (With 16 bits the gradients were off by 0.0031 of their size, rms, against
+// 0.0024 from the operands' and the results' own roundings alone.)
 template <bool F32_>
-__device__ inline void store8(char *p, size_t at, const float *v) {
-    if constexpr (F32_) {
-        f32x4 *q = reinterpret_cast<f32x4 *>(p + at * 4);
-        q[0] = f32x4{v[0], v[1], v[2], v[3]};
-        q[1] = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-        *reinterpret_cast<u32x4 *>(p + at * 2) = pack8(v);
+struct Kept {
+    u32x4 w[F32_ ? 2 : 1];
+    u32x2 low;
+    __device__ void load(const MlpKept &k, Place at) {
+        const u32x4 *q = at.in<const u32x4>(k.p, F32_ ? 4 : 2);
+        w[0] = q[0];
+        if constexpr (F32_)
+            w[1] = q[1];
+        else
+            low = *at.in<const u32x2>(k.p + k.low, 1);
     }
-}
+    __device__ void values(float *v) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (F32_)
+                v[i] = __uint_as_float(w[i / 4][i % 4]);
+            else  // bytes: 0, byte i % 4 of low, both of the half
+                v[i] = __uint_as_float(__builtin_amdgcn_perm(
+                    w[0][i / 2], low[i / 4], (i % 2 ? 0x0706000Cu : 0x0504000Cu) | (uint32_t)(i % 4) << 8));
+        }
+    }
+    static __device__ void store(const MlpKept &k, Place at, const float *v) {
+        u32x4 *q = at.in<u32x4>(k.p, F32_ ? 4 : 2);
+        uint32_t b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(v[i]);
+        if constexpr (F32_) {
+            q[0] = u32x4{b[0], b[1], b[2], b[3]};
+            q[1] = u32x4{b[4], b[5], b[6], b[7]};
+        } else {
+            u32x4 x;
+            u32x2 y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_perm(b[2 * i + 1], b[2 * i], 0x07060302u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                y[i] = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0C0C0501u) |
+                       __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x05010C0Cu);
+            q[0] = x;
+            *at.in<u32x2>(k.p + k.low, 1) = y;
+        }
+    }
+};
 
-// What follows a product: eight sums of one row, from column `col` (a multiple
-// of 8, below N) on.  GATE: v are gate's and w up's.
+// What follows a product: eight sums of one row, the first `left` of which (at
+// least one) are inside the matrix.  GATE: v are gate's and w up's.  DGATE: kg
+// and ku are g and u.
 template <int EPI, bool F32_>
-__device__ inline void finish(const MlpCall &c, const MlpProduct &p, int row, int col, float *v, float *w) {
+__device__ inline void finish(const MlpCall &c, const MlpProduct &p, Place at, int left, float *v, float *w,
+                              const Kept<F32_> &kg, const Kept<F32_> &ku) {
     if constexpr (EPI == MLP_STORE) {
         using DT = std::conditional_t<F32_, F32, BF16>;
-        if (p.vec && col + 8 <= p.N) {
-            store8<F32_>(p.out, (size_t)row * p.ldo + col, v);
+        auto *o = at.in<typename DT::S>(p.out, sizeof(typename DT::S));
+        if (p.vec && left >= 8) {
+            if constexpr (F32_)
+                store8f(o, v);
+            else
+                *reinterpret_cast<u32x4 *>(o) = pack8(v);
         } else {
-            auto *o = reinterpret_cast<typename DT::S *>(p.out) + (size_t)row * p.ldo + col;
-            for (int i = 0; i < 8 && col + i < p.N; ++i) o[i] = round_to<DT>(v[i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) o[i] = round_to<DT>(v[i]);
         }
     } else if constexpr (EPI == MLP_GATE) {
         // columns past N are 0 (the operand's rows past N read as zeros), and
         // so are act(0) 0: the next product may run over them
-        const size_t at = (size_t)row * c.ld + col;
-        if (c.gate) {
-            store8<F32_>(c.gate, at, v);
-            store8<F32_>(c.up, at, w);
+        if (c.gate.p) {
+            Kept<F32_>::store(c.gate, at, v);
+            Kept<F32_>::store(c.up, at, w);
         }
+        float a[8];
+        activate<false>(c.act, v, a, nullptr);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate<false>(c.act, v[i]).a * w[i];
-        store_planes<F32_>(c.product, (size_t)row * c.product.ld + col, v);
+        for (int i = 0; i < 8; ++i) v[i] = a[i] * w[i];
+        store_planes<F32_>(c.product, at, v);
     } else {
-        float g[8], u[8];
-        const size_t at = (size_t)row * c.ld + col;
-        load8<F32_>(c.gate, at, g);
-        load8<F32_>(c.up, at, u);
+        float g[8], u[8], a[8], slope[8];
+        kg.values(g);
+        ku.values(u);
+        activate<true>(c.act, g, a, slope);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const Act r = activate<true>(c.act, g[i]);
-            const bool in = col + i < p.N;  // past N the sums are of another row's weights
-            g[i] = in ? v[i] * u[i] * r.slope : 0.0f;
-            u[i] = in ? v[i] * r.a : 0.0f;
+            g[i] = v[i] * u[i] * slope[i];
+            u[i] = v[i] * a[i];
         }
-        store_planes<F32_>(c.dgate, (size_t)row * c.dgate.ld + col, g);
-        store_planes<F32_>(c.dup, (size_t)row * c.dup.ld + col, u);
+        if (left < 8) {  // past N the sums are of another row's weights
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                if (i >= left) g[i] = u[i] = 0.0f;
+        }
+        store_planes<F32_>(c.dgate, at, g);
+        store_planes<F32_>(c.dup, at, u);
     }
 }
 
@@ -232,7 +282,8 @@ struct Side {
                      : "memory");
     }
     // The part of a fragment's LDS offset that depends on the lane alone.
-    // Fragment: lane l gets row (column) l % 32 of a 32-wide tile, k = 8 (l / 32) + 0..7.
+    // Fragment: lane l gets row (column) l % 32 of a 32-wide tile, k = 8 (l / 32)
+    // + 0..7.
     struct Lane {
         unsigned a, key;
     };
@@ -277,111 +328,153 @@ __device__ inline void stage_barrier() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// Workgroups of consecutive numbers go to the 8 XCDs in turn: numbers are
-// regrouped so that an XCD gets a run of consecutive tiles, and the tiles run
-// down 8 rows of tiles before the next column, so the tiles under way on an XCD
-// share their operands in its L2.
-__device__ inline void tile_of(int id, int tiles_m, int tiles_n, int &tm, int &tn) {
-    const int band = 8 * tiles_n, b = id / band, r = id % band;
-    const int rows = min(8, tiles_m - 8 * b);
-    tm = 8 * b + r % rows;
-    tn = r / rows;
+// f(0), f(1), ... f(N - 1), each argument a constant: a loop that is unrolled
+// however long its body is.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each<N, I + 1>(f);
+    }
 }
 
-// -------------------------------------------------------------------- kernel
-// A BM x BN tile of a product for 4 waves, a quadrant each, as 32 x 32 tiles.
-// GATE: BN / 2 columns of gate and of up, each wave the same columns of both.
-template <int BM, int BN, int EPI, bool ACOLS, bool BCOLS, bool F32_>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
-    constexpr bool DUAL = EPI == MLP_GATE;
-    constexpr int TM = BM / 64, TN = BN / 64;           // 32 x 32 tiles of a wave
-    constexpr unsigned ABYTES = BM * KS * 2, STAGE = (BM + BN) * KS * 2;
-    constexpr int PAIRS = F32_ ? 6 : 1;
-    extern __shared__ __align__(16) char smem[];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int wm = w >> 1, wn = w & 1;
-
-    // the tile: numbers regrouped by XCD, then product by product
-    int id;
-    {
-        const int n = gridDim.x, q = n >> 3, r = n & 7, x = blockIdx.x & 7;
-        id = x * q + min(x, r) + (int)(blockIdx.x >> 3);
-    }
+// Tile `id` of a call: which product's, and where.  Tiles run down 8 rows of
+// tiles before the next column, so that neighbours share their operands.
+__device__ inline int tile_of(const MlpCall &c, int id, int &tm, int &tn) {
     int which = 0;
     while (which + 1 < c.count && id >= c.p[which].tiles_m * c.p[which].tiles_n) {
         id -= c.p[which].tiles_m * c.p[which].tiles_n;
         ++which;
     }
-    const MlpProduct &p = c.p[which];
-    int tm, tn;
-    tile_of(id, p.tiles_m, p.tiles_n, tm, tn);
-    constexpr int NCOLS = DUAL ? BN / 2 : BN;
-    const int m0 = tm * BM, n0 = tn * NCOLS;
-    const int nk = max(1, (p.K + KS - 1) / KS), total = nk * PAIRS * p.lists;
-    const int s0 = (int)((long long)total * blockIdx.y / c.splits);
-    const int s1 = (int)((long long)total * (blockIdx.y + 1) / c.splits);
+    const int tiles_n = c.p[which].tiles_n, band = 8 * tiles_n, b = id / band, r = id % band;
+    const int rows = min(8, c.p[which].tiles_m - 8 * b);
+    tm = 8 * b + r % rows;
+    tn = r / rows;
+    return which;
+}
+
+// -------------------------------------------------------------------- kernel
+// BM x BN tiles of the products for 4 waves, a quadrant each, as 32 x 32 tiles.
+// GATE: BN / 2 columns of gate and of up, each wave the same columns of both.
+// A workgroup takes one unit after the other: the first `whole` are tiles, the
+// others the parts, in k, of the tiles that would not fill a last round.  The
+// first loads of a unit go out before the one before it is finished off.
+template <int BM, int BN, int EPI, bool ACOLS, bool BCOLS, bool F32_>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
+    constexpr bool DUAL = EPI == MLP_GATE;
+    constexpr int TM = BM / 64, TN = BN / 64, TO = DUAL ? TN / 2 : TN;  // 32 x 32 tiles of a wave; of its results
+    constexpr unsigned ABYTES = BM * KS * 2, STAGE = (BM + BN) * KS * 2;
+    constexpr int PAIRS = F32_ ? 6 : 1, NCOLS = DUAL ? BN / 2 : BN;
+    constexpr bool OWN_SLAB = BM == 256;  // LDS for the results besides the stages
+    extern __shared__ __align__(16) char smem[];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wm = w >> 1, wn = w & 1;
+    const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
 
     Side<BM, ACOLS, false> sa;
     Side<BN, BCOLS, DUAL> sb;
-    sa.init((int)p.a[0].ld, p.K, lane, w);
-    sb.init((int)p.b[0].ld, p.K, lane, w);
-    int seg = s0 / nk, kt = s0 - seg * nk;  // of the stage to be loaded next
-    auto aim = [&]() {
+    const auto la = sa.lane_of(lane);
+    const auto lb = sb.lane_of(lane);
+    constexpr int LOADS = sa.PER + sb.PER;
+
+    struct Unit {
+        int which, m0, n0, part, stages;  // part: number among the partial sums, or -1
+    };
+    int seg = 0, kt = 0, nk = 1;  // of the stage to be loaded next
+    auto aim = [&](const Unit &t) {
+        const MlpProduct &p = c.p[t.which];
         const int list = seg / PAIRS, pair = seg % PAIRS;
         const int pa = F32_ ? kPairA[pair] : 0, pb = F32_ ? kPairB[pair] : 0;
-        sa.start(0, p.a[list].p + pa * p.a[list].plane, m0, p.M);
-        sb.start(0, p.b[list].p + pb * p.b[list].plane, n0, p.N);
-        if (DUAL) sb.start(1, p.b[1].p + pb * p.b[1].plane, n0, p.N);
+        sa.start(0, p.a[list].p + pa * p.a[list].plane, t.m0, p.M);
+        sb.start(0, p.b[list].p + pb * p.b[list].plane, t.n0, p.N);
+        if (DUAL) sb.start(1, p.b[1].p + pb * p.b[1].plane, t.n0, p.N);
     };
-    aim();
-    constexpr int LOADS = sa.PER + sb.PER;
-    auto load = [&](int i, int k0, unsigned buf) {
-        if (i < sa.PER)
-            sa.load(i, k0, buf, w);
-        else
-            sb.load(i - sa.PER, k0, buf + ABYTES, w);
+    auto open = [&](int id) {
+        Unit t;
+        int part = 0, parts = 1;
+        t.part = id - c.whole;
+        if (t.part >= 0) {
+            parts = c.splits;
+            part = t.part % parts;
+            id = c.whole + t.part / parts;
+        }
+        int tm, tn;
+        t.which = tile_of(c, id, tm, tn);
+        t.m0 = tm * BM;
+        t.n0 = tn * NCOLS;
+        const MlpProduct &p = c.p[t.which];
+        sa.init((int)p.a[0].ld, p.K, lane, w);
+        sb.init((int)p.b[0].ld, p.K, lane, w);
+        nk = max(1, (p.K + KS - 1) / KS);
+        const long long total = (long long)nk * PAIRS * p.lists;
+        const int s0 = (int)(total * part / parts);
+        t.stages = (int)(total * (part + 1) / parts) - s0;
+        seg = s0 / nk;
+        kt = s0 - seg * nk;
+        aim(t);
+        return t;
     };
-    auto next = [&]() {
+    auto next = [&](const Unit &t) {
         if (++kt == nk) {
             kt = 0;
             ++seg;
-            aim();
+            aim(t);
+        }
+    };
+    auto load = [&](int i, unsigned buf) {
+        if (i < sa.PER)
+            sa.load(i, kt * KS, buf, w);
+        else
+            sb.load(i - sa.PER, kt * KS, buf + ABYTES, w);
+    };
+    // the first stage's loads and half of the second's
+    auto begin = [&](const Unit &t) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load(i, lds0);
+        if (t.stages > 1) {
+            next(t);
+#pragma unroll
+            for (int i = 0; i < LOADS / 2; ++i) load(i, lds0 + STAGE);
         }
     };
 
-    f32x16 acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-
-    const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
-    const auto la = sa.lane_of(lane);
-    const auto lb = sb.lane_of(lane);
     u32x4 fa[2][TM], fb[2][TN];
     auto frags = [&](const char *buf, int k, int to) {
 #pragma unroll
         for (int i = 0; i < TM; ++i) fa[to][i] = sa.frag(buf, la, wm * (BM / 2) + 32 * i, k, lane);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int row = DUAL ? (j / (TN / 2)) * (BN / 2) + wn * (BN / 4) + 32 * (j % (TN / 2)) : wn * (BN / 2) + 32 * j;
-            fb[to][j] = sb.frag(buf + ABYTES, lb, row, k, lane);
-        }
+        for (int j = 0; j < TN; ++j)
+            fb[to][j] = sb.frag(buf + ABYTES, lb, (j / TO) * (BN / 2) + wn * (32 * TO) + 32 * (j % TO), k, lane);
     };
 
-    if (s0 < s1) {
+    // Workgroups of consecutive numbers go to the 8 XCDs in turn: a round's
+    // units are regrouped so that an XCD gets a run of consecutive ones, whose
+    // operands it keeps in its L2.
+    const int grid = gridDim.x;
+    const int first = [&]() {
+        const int q = grid >> 3, r = grid & 7, x = blockIdx.x & 7;
+        return x * q + min(x, r) + (int)(blockIdx.x >> 3);
+    }();
+    Unit t = open(first);
+    begin(t);
+    for (int id = first;;) {
+        f32x16 acc[TM][TN];
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(i, kt * KS, lds0);
-        if (s0 + 1 < s1) next();
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+        // Loads run two stages ahead: those of a stage go out behind the products
+        // of the last quarter of the stage two before it, as soon as its buffer
+        // is free, and of the first quarter of the next.
+        constexpr int EACH = (LOADS + 2 * TM - 1) / (2 * TM);
         stage_barrier();
         frags(smem, 0, 0);
-        for (int s = s0; s < s1; ++s) {
-            const unsigned here = ((s - s0) & 1) * STAGE, there = STAGE - here;
-            const bool more = s + 1 < s1;
-            // The loads of the next stage go out behind the products of this
-            // one, whose buffer the others have left at the last barrier.
+        for (int s = 0; s < t.stages; ++s) {
+            const unsigned here = (s & 1) * STAGE, there = STAGE - here;
+            const bool more = s + 1 < t.stages, more2 = s + 2 < t.stages;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (k < 3) {
@@ -393,93 +486,149 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
-                    // (operands in turn: a lane gets four columns of one row)
+                    // (operands in turn: a lane gets columns of one row)
 #pragma unroll
                     for (int j = 0; j < TN; ++j)
                         acc[i][j] = mma32_chunk(BF16{}, acc[i][j], fb[k & 1][j], fa[k & 1][i]);
-                    constexpr int HALF = (LOADS + 2 * TM - 1) / (2 * TM);
-                    if (k < 2 && more) {
+                    if (k == 0 && more) {
 #pragma unroll
-                        for (int x = 0; x < HALF; ++x)
-                            if ((k * TM + i) * HALF + x < LOADS)
-                                load((k * TM + i) * HALF + x, kt * KS, lds0 + there);
+                        for (int x = 0; x < EACH; ++x)
+                            if (LOADS / 2 + i * EACH + x < LOADS) load(LOADS / 2 + i * EACH + x, lds0 + there);
+                    }
+                    if (k == 3 && more2) {
+#pragma unroll
+                        for (int x = 0; x < EACH; ++x)
+                            if (i * EACH + x < LOADS / 2) load(i * EACH + x, lds0 + here);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (k == 1 && s + 2 < s1) next();
+                if (k == 0 && more2) next(t);
             }
         }
-    }
 
-    // The sums go through LDS in slabs of 32 rows of each row of waves, so that
-    // a thread gets eight consecutive columns of a row.
-    constexpr int PITCH = BN + 8;
-    float *slab = reinterpret_cast<float *>(smem);
-    static_assert(64 * PITCH * 4 <= 2 * STAGE, "slab");
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int col = DUAL ? (j / (TN / 2)) * (BN / 2) + wn * (BN / 4) + 32 * (j % (TN / 2)) : wn * (BN / 2) + 32 * j;
-            float *to = slab + (wm * 32 + (lane & 31)) * PITCH + col + 4 * (lane >> 5);
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                *reinterpret_cast<f32x4 *>(to + 8 * v) =
-                    f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+        // The next unit's first loads, then this one's results (with the small
+        // tiles, which keep no LDS besides the stages, the other way round).
+        const Unit done = t;
+        id += grid;
+        const bool again = id < c.units;
+        if (OWN_SLAB ? again : true) stage_barrier();  // every wave has read the last stage
+        if (OWN_SLAB && again) {
+            t = open(id);
+            begin(t);
         }
-        __syncthreads();
-        constexpr int TPR = NCOLS / 8;  // threads a row
-#pragma unroll 2
-        for (int r = threadIdx.x / TPR; r < 64; r += 256 / TPR) {
-            const int row = m0 + (r >> 5) * (BM / 2) + 32 * i + (r & 31), col = n0 + (threadIdx.x % TPR) * 8;
-            if (row >= p.M || col >= p.N) continue;
-            const float *from = slab + r * PITCH + (threadIdx.x % TPR) * 8;
-            float v[8], u[8];
+        // A wave's 32 x 32 tiles go through LDS of its own, 64 columns at a time
+        // (GATE: 32 of gate and of up), so that eight lanes (four) hold eight
+        // columns each of a row and memory is written by whole lines.  Pieces of
+        // four values of row r lie at p ^ (r % 16): all banks, both ways.
+        const MlpProduct &p = c.p[done.which];
+        constexpr int WIDE = TO > 1 && !DUAL ? 2 : 1, CPR = 4 * WIDE, ITS = CPR / 2;  // chunks of a row; of a lane
+        constexpr int STEPS = TM * TO / WIDE;
+        constexpr bool READS = EPI == MLP_DGATE;
+        float *slab = reinterpret_cast<float *>(smem + (OWN_SLAB ? 2 * STAGE : 0)) + w * 2048;
+        const int r0 = lane / CPR, c0 = lane % CPR;
+        Kept<F32_> kg[2][READS ? ITS : 1], ku[2][READS ? ITS : 1];
+        const long long ld = EPI == MLP_STORE ? p.ldo : c.ld;
+        const int mw = done.m0 + wm * (BM / 2), nw = done.n0 + wn * (32 * TO);  // the wave's rows and columns
+        const size_t corner = (size_t)mw * ld + nw;
+        const unsigned mine = r0 * (unsigned)ld + 8 * c0;
+        const int rows = p.M - mw - r0, cols = p.N - nw - 8 * c0;  // inside, from the lane's first on
+        auto row_of = [](int step, int it) { return 32 * (step / (TO / WIDE)) + it * (64 / CPR); };
+        auto col_of = [](int step) { return 32 * WIDE * (step % (TO / WIDE)); };
+        auto place = [&](int step, int it) { return Place{corner + (size_t)row_of(step, it) * ld + col_of(step), mine}; };
+        auto fetch = [&](int step) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = from[e];
-            if (DUAL)
+            for (int it = 0; it < ITS; ++it)
+                if (row_of(step, it) < rows && col_of(step) < cols) {
+                    kg[step & 1][it].load(c.gate, place(step, it));
+                    ku[step & 1][it].load(c.up, place(step, it));
+                }
+        };
+        if constexpr (READS)
+            if (done.part < 0) fetch(0);
+        each<STEPS>([&](auto at) {
+            constexpr int step = decltype(at)::value, i = step / (TO / WIDE), jw = step % (TO / WIDE);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = from[BN / 2 + e];
-            if (c.part) {
-                const long long ldp = (p.N + 7) & ~7ll;
-                float *o = c.part + ((long long)blockIdx.y * p.M + row) * ldp * (DUAL ? 2 : 1) + col;
-                store8<true>(reinterpret_cast<char *>(o), 0, v);
-                if (DUAL) store8<true>(reinterpret_cast<char *>(o + ldp), 0, u);
-            } else {
-                finish<EPI, F32_>(c, p, row, col, v, u);
-            }
+            for (int h = 0; h < (DUAL ? 2 : WIDE); ++h)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const f32x16 &x = acc[i][DUAL ? jw + h * TO : jw * WIDE + h];
+                    *reinterpret_cast<f32x4 *>(slab + (lane & 31) * 64 +
+                                               4 * ((8 * h + 2 * v + (lane >> 5)) ^ (lane & 15))) =
+                        f32x4{x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]};
+                }
+            if constexpr (READS)
+                if (step + 1 < STEPS && done.part < 0) fetch(step + 1);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            each<ITS>([&](auto ati) {
+                constexpr int it = decltype(ati)::value;
+                const int r = r0 + it * (64 / CPR);
+                auto get = [&](int piece, float *v) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const f32x4 x = *reinterpret_cast<const f32x4 *>(slab + r * 64 + 4 * ((piece + h) ^ (r & 15)));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
+                    }
+                };
+                float v[8], u[8];
+                get(2 * c0, v);
+                if (DUAL) get(2 * c0 + 8, u);
+                if (done.part >= 0) {
+                    float *to = c.part + (size_t)done.part * (BM * BN) + (wm * (BM / 2) + row_of(step, it)) * BN +
+                                wn * (32 * TO) + col_of(step) + (r0 * BN + 8 * c0);
+                    store8f(to, v);
+                    if (DUAL) store8f(to + BN / 2, u);
+                } else if (row_of(step, it) < rows && col_of(step) < cols) {
+                    finish<EPI, F32_>(c, p, place(step, it), cols - col_of(step), v, u, kg[step & 1][READS ? it : 0],
+                                      ku[step & 1][READS ? it : 0]);
+                }
+                if constexpr (READS) __builtin_amdgcn_sched_barrier(0);
+            });
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        if (!again) break;
+        if (!OWN_SLAB) {
+            stage_barrier();
+            t = open(id);
+            begin(t);
         }
     }
 }
 
-// The sums of a split contraction, in their order.
-template <int EPI, bool F32_>
+// The sums of tiles whose contraction was split, in the parts' order.
+template <int BM, int BN, int EPI, bool F32_>
 __global__ __launch_bounds__(256) void k_mlp_join(MlpCall c) {
-    constexpr int D = EPI == MLP_GATE ? 2 : 1;
-    const MlpProduct &p = c.p[0];
-    const int ldp = (p.N + 7) & ~7, per = ldp / 8;
-    const long long n = (long long)p.M * per, slice = (long long)p.M * ldp * D;
-    for (long long t = blockIdx.x * 256ll + threadIdx.x; t < n; t += gridDim.x * 256ll) {
-        const int row = (int)(t / per), col = (int)(t % per) * 8;
-        const float *from = c.part + (long long)row * ldp * D + col;
-        float v[8], u[8];
+    constexpr bool DUAL = EPI == MLP_GATE;
+    constexpr int NCOLS = DUAL ? BN / 2 : BN, PER = BM * NCOLS / 8;
+    int tm, tn;
+    const MlpProduct &p = c.p[tile_of(c, c.whole + blockIdx.y, tm, tn)];
+    const int t = blockIdx.x * 256 + threadIdx.x, r = t / (NCOLS / 8), q = t % (NCOLS / 8) * 8;
+    const int row = tm * BM + r, col = tn * NCOLS + q;
+    if (t >= PER || row >= p.M || col >= p.N) return;
+    const float *from = c.part + (size_t)blockIdx.y * c.splits * (BM * BN) + r * BN + q;
+    float v[8], u[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = u[e] = 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = u[e] = 0.0f;
 #pragma unroll 4
-        for (int s = 0; s < c.splits; ++s) {
-            float x[8];
-            load8<true>(reinterpret_cast<const char *>(from + s * slice), 0, x);
+    for (int s = 0; s < c.splits; ++s, from += BM * BN) {
+        float x[8];
+        load8f(from, x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += x[e];
-            if (D == 2) {
-                load8<true>(reinterpret_cast<const char *>(from + s * slice + ldp), 0, x);
+        for (int e = 0; e < 8; ++e) v[e] += x[e];
+        if (DUAL) {
+            load8f(from + BN / 2, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] += x[e];
-            }
+            for (int e = 0; e < 8; ++e) u[e] += x[e];
         }
-        finish<EPI, F32_>(c, p, row, col, v, u);
     }
+    Kept<F32_> kg, ku;
+    const Place at{(size_t)row * (EPI == MLP_STORE ? p.ldo : c.ld) + col, 0};
+    if constexpr (EPI == MLP_DGATE) {
+        kg.load(c.gate, at);
+        ku.load(c.up, at);
+    }
+    finish<EPI, F32_>(c, p, at, p.N - col, v, u, kg, ku);
 }
 
 template <bool F32_>
@@ -502,11 +651,19 @@ __global__ __launch_bounds__(256) void k_mlp_planes(const char *src, long long l
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = DT::to_f(s[i]);
-        store_planes<F32_>(to, (size_t)(row * to.ld + col), v);
+        store_planes<F32_>(to, Place{(size_t)(row * to.ld + col), 0}, v);
     }
 }
 
-constexpr int kTiles[3][2] = {{256, 256}, {128, 128}, {64, 64}};
+// The tiles, how many workgroups of them a CU holds, and the microseconds of a
+// stage in each when all run, and of a unit besides.
+struct Tile {
+    int m, n, gate_n;  // gate_n: columns of a GATE tile (half of its operand's rows)
+    int held;
+    float stage, unit;
+};
+constexpr Tile kTiles[3] = {{256, 256, 128, 1, 2.0f, 8.0f}, {128, 128, 64, 2, 1.3f, 5.0f}, {64, 64, 64, 3, 0.9f, 4.0f}};
+constexpr int kCus = 256;
 
 unsigned blocks(long long n) {
     n = (n + 255) / 256;
@@ -514,39 +671,40 @@ unsigned blocks(long long n) {
 }
 
 template <int BM, int BN, int EPI, bool AC, bool BC, bool F32_>
-hipError_t run(const MlpCall &c, int tiles, hipStream_t s) {
-    constexpr int smem = 2 * (BM + BN) * KS * 2;
+hipError_t run(const MlpCall &c, const MlpPlan &plan, hipStream_t s) {
+    constexpr int smem = 2 * (BM + BN) * KS * 2 + (BM == 256 ? 32768 : 0);
+    static_assert(smem <= 163840 && smem >= 32768, "LDS");
     const void *fn = reinterpret_cast<const void *>(&k_mlp<BM, BN, EPI, AC, BC, F32_>);
     const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_mlp<BM, BN, EPI, AC, BC, F32_>), dim3(tiles, c.splits), dim3(256), smem, s, c);
-    if (c.part) {
-        const MlpProduct &p = c.p[0];
-        hipLaunchKernelGGL((k_mlp_join<EPI, F32_>), dim3(blocks((long long)p.M * ((p.N + 7) / 8))), dim3(256), 0, s,
+    const int slots = kCus * kTiles[plan.tile].held;
+    hipLaunchKernelGGL((k_mlp<BM, BN, EPI, AC, BC, F32_>), dim3(c.units < slots ? c.units : slots), dim3(256), smem, s,
+                       c);
+    if (plan.split_tiles) {
+        constexpr int per = BM * (EPI == MLP_GATE ? BN / 2 : BN) / 8;
+        hipLaunchKernelGGL((k_mlp_join<BM, BN, EPI, F32_>), dim3((per + 255) / 256, plan.split_tiles), dim3(256), 0, s,
                            c);
     }
     return hipGetLastError();
 }
 
+template <int EPI, bool AC, bool BC, bool F32_>
+hipError_t launch(const MlpCall &c, const MlpPlan &plan, hipStream_t s) {
+    if (plan.tile == 0) return run<256, 256, EPI, AC, BC, F32_>(c, plan, s);
+    if (plan.tile == 1) return run<128, 128, EPI, AC, BC, F32_>(c, plan, s);
+    return run<64, EPI == MLP_GATE ? 128 : 64, EPI, AC, BC, F32_>(c, plan, s);
+}
+
 template <int EPI, bool AC, bool BC>
-hipError_t launch(const MlpCall &c, int tile, int tiles, hipStream_t s) {
-    const bool f = c.dtype == LSTM_F32;
-    switch (tile) {
-        case 0: return f ? run<256, 256, EPI, AC, BC, true>(c, tiles, s) : run<256, 256, EPI, AC, BC, false>(c, tiles, s);
-        case 1: return f ? run<128, 128, EPI, AC, BC, true>(c, tiles, s) : run<128, 128, EPI, AC, BC, false>(c, tiles, s);
-        default: {
-            constexpr int BN = EPI == MLP_GATE ? 128 : 64;
-            return f ? run<64, BN, EPI, AC, BC, true>(c, tiles, s) : run<64, BN, EPI, AC, BC, false>(c, tiles, s);
-        }
-    }
+hipError_t launch(const MlpCall &c, const MlpPlan &plan, hipStream_t s) {
+    return c.dtype == LSTM_F32 ? launch<EPI, AC, BC, true>(c, plan, s) : launch<EPI, AC, BC, false>(c, plan, s);
 }
 
 long long tiles_of(const MlpCall &c, int tile, MlpCall *to) {
     long long n = 0;
-    // (gate and up side by side: half the columns; the smallest tile then is twice as wide)
-    const int bn = c.epilogue == MLP_GATE ? (tile == 2 ? 64 : kTiles[tile][1] / 2) : kTiles[tile][1];
+    const int bn = c.epilogue == MLP_GATE ? kTiles[tile].gate_n : kTiles[tile].n;
     for (int i = 0; i < c.count; ++i) {
-        const long long tm = (c.p[i].M + kTiles[tile][0] - 1) / kTiles[tile][0], tn = (c.p[i].N + bn - 1) / bn;
+        const long long tm = (c.p[i].M + kTiles[tile].m - 1) / kTiles[tile].m, tn = (c.p[i].N + bn - 1) / bn;
         if (to) to->p[i].tiles_m = (int)tm, to->p[i].tiles_n = (int)tn;
         n += tm * tn;
     }
@@ -555,38 +713,62 @@ long long tiles_of(const MlpCall &c, int tile, MlpCall *to) {
 
 }  // namespace
 
+// The tile and the split of the last round with the least estimated time:
+// rounds of units, and the partial sums' way to memory and back at 4 TB/s with
+// a launch to join them.
 MlpPlan mlp_plan(const MlpCall &c) {
-    MlpPlan r{0, 1, 0};
-    // the largest tile that still gives most CUs one
-    while (r.tile < 2 && tiles_of(c, r.tile, nullptr) < 200) ++r.tile;
-    if (c.count == 1) {
-        const MlpProduct &p = c.p[0];
-        const long long n = tiles_of(c, r.tile, nullptr);
-        const long long stages = (long long)((p.K + KS - 1) / KS) * p.lists * (c.dtype == LSTM_F32 ? 6 : 1);
-        // few tiles of a long contraction: split it, eight stages a part at least
-        long long k = n > 0 && n < 200 ? 512 / n : 1;
-        if (k > stages / 8) k = stages / 8;
-        if (k > 64) k = 64;
-        if (k > 1) {
-            r.splits = (int)k;
-            r.floats = (size_t)k * p.M * ((p.N + 7) & ~7) * (c.epilogue == MLP_GATE ? 2 : 1);
-        }
+    MlpPlan best{};
+    double least = 1e30;
+    double stages = 0;  // of a tile (the longest product's)
+    for (int i = 0; i < c.count; ++i) {
+        const double n = (double)((c.p[i].K + KS - 1) / KS) * c.p[i].lists * (c.dtype == LSTM_F32 ? 6 : 1);
+        if (n > stages) stages = n;
     }
-    return r;
+    for (int tile = 0; tile < 3; ++tile) {
+        const Tile &t = kTiles[tile];
+        const long long n = tiles_of(c, tile, nullptr), slots = kCus * t.held, rem = n % slots;
+        const double area = (double)t.m * (c.epilogue == MLP_GATE ? 2 * t.gate_n : t.n) * sizeof(float);
+        const double wide = c.epilogue == MLP_GATE && tile == 2 ? 1.5 : 1.0;
+        auto offer = [&](long long whole, long long splits) {
+            const long long split_tiles = splits > 1 ? n - whole : 0;
+            double us = 0;
+            const long long rounds = (whole + slots - 1) / slots;
+            us += rounds * (stages * t.stage * wide + t.unit);
+            if (split_tiles) {
+                us += ((split_tiles * splits + slots - 1) / slots) * (stages / splits * t.stage * wide + t.unit);
+                us += 4.0 + 2 * split_tiles * splits * area / 4e6;
+            }
+            if (us < least) {
+                least = us;
+                best.tile = tile;
+                best.whole = (int)whole;
+                best.splits = (int)splits;
+                best.split_tiles = (int)split_tiles;
+                best.units = (int)(whole + split_tiles * splits);
+                best.floats = (size_t)(split_tiles * splits) * (size_t)(area / sizeof(float));
+            }
+        };
+        offer(n, 1);
+        // split the tiles of the last round so that they fill it, in one or two rounds of parts
+        for (int k = 2; rem && k <= 64 && stages / k >= 4; ++k)
+            if (rem * k <= 2 * slots) offer(n - rem, k);
+    }
+    return best;
 }
 
 hipError_t launch_mlp(const MlpCall &call, hipStream_t s) {
     MlpCall c = call;
     const MlpPlan plan = mlp_plan(c);
+    c.whole = plan.whole;
     c.splits = plan.splits;
-    if (plan.splits == 1) c.part = nullptr;
-    const int tiles = (int)tiles_of(c, plan.tile, &c);
-    if (tiles == 0) return hipSuccess;
-    if (c.epilogue == MLP_GATE) return launch<MLP_GATE, false, false>(c, plan.tile, tiles, s);
-    if (c.epilogue == MLP_DGATE) return launch<MLP_DGATE, false, true>(c, plan.tile, tiles, s);
-    if (c.a_cols) return launch<MLP_STORE, true, true>(c, plan.tile, tiles, s);
-    if (c.b_cols) return launch<MLP_STORE, false, true>(c, plan.tile, tiles, s);
-    return launch<MLP_STORE, false, false>(c, plan.tile, tiles, s);
+    c.units = plan.units;
+    (void)tiles_of(c, plan.tile, &c);
+    if (c.units == 0) return hipSuccess;
+    if (c.epilogue == MLP_GATE) return launch<MLP_GATE, false, false>(c, plan, s);
+    if (c.epilogue == MLP_DGATE) return launch<MLP_DGATE, false, true>(c, plan, s);
+    if (c.a_cols) return launch<MLP_STORE, true, true>(c, plan, s);
+    if (c.b_cols) return launch<MLP_STORE, false, true>(c, plan, s);
+    return launch<MLP_STORE, false, false>(c, plan, s);
 }
 
 hipError_t launch_mlp_planes(int dtype, const void *src, long long ld, long long rows, int cols, const MlpOperand &to,
