@@ -115,6 +115,20 @@ struct MlpPlan {
 };
 MlpPlan mlp_plan(const MlpCall &c);
 hipError_t launch_mlp(const MlpCall &c, hipStream_t s);
+// The products of the forward call for up to MLP_FEW rows, from the matrices as
+// they are: w[0] and w[1] gate and up, out receives h [rows][ld] of the call's
+// dtype, zeros past N; or w[0] alone, out receives [rows][N].
+constexpr int MLP_FEW = 64;
+struct MlpFew {
+    const char *x, *w[2];  // w [N][K]
+    long long xs;          // elements from row to row of x
+    int rows, N, K, dtype, act;
+    char *out;
+    long long ld;
+    MlpKept gate, up;      // kept for the backward call where keep.p is set
+    MlpOperand keep;       // h as an operand
+};
+hipError_t launch_mlp_few(const MlpFew &c, hipStream_t s);
 // src [rows][cols] of dtype (ld elements from row to row) as bf16 planes (one, or three for fp32) of rows `to.ld`
 // long, the columns past cols 0.
 hipError_t launch_mlp_planes(int dtype, const void *src, long long ld, long long rows, int cols, const MlpOperand &to,

@@ -241,6 +241,8 @@ size_t most(size_t a, size_t b) { return a > b ? a : b; }
 
 // The launches of a forward call and its workspace.
 struct Forward {
+    bool few;
+    MlpFew few_gate, few_down;
     Operands ops;
     MlpCall gate, down;
     size_t bytes;
@@ -250,18 +252,34 @@ Forward forward_of(const lstm_gated_mlp_shape *s, const void *x, long long xs, c
                    const void *wd, void *y, void *reserve, void *workspace) {
     Carver k{static_cast<char *>(workspace)};
     Forward f{};
+    f.few = s->rows <= MLP_FEW;
+    const Reserve r = reserve_of(s, reserve);
+    if (f.few) {
+        const long long ld = padded(s->hidden);
+        char *h = k.take((size_t)s->rows, (size_t)ld, elem(s->dtype));
+        f.few_gate = MlpFew{static_cast<const char *>(x), {static_cast<const char *>(wg), static_cast<const char *>(wu)},
+                            xs, s->rows, s->hidden, s->in, s->dtype, s->activation, h, ld, {}, {}, {}};
+        if (reserve) {
+            f.few_gate.gate = r.gate;
+            f.few_gate.up = r.up;
+            f.few_gate.keep = r.product;
+        }
+        f.few_down = MlpFew{h, {static_cast<const char *>(wd), nullptr}, ld, s->rows, s->out, s->hidden, s->dtype,
+                            s->activation, static_cast<char *>(y), s->out, {}, {}, {}};
+        f.bytes = k.used;
+        f.ok = k.ok;
+        return f;
+    }
     f.ops.s = s;
     f.ops.k = &k;
     const MlpOperand ox = f.ops.add(x, xs, s->rows, s->in, false);
     const MlpOperand og = f.ops.add(wg, s->in, s->hidden, s->in, true), ou = f.ops.add(wu, s->in, s->hidden, s->in, true);
     const MlpOperand od = f.ops.add(wd, s->hidden, s->out, s->hidden, true);
-    const MlpOperand mine = k.operand(s, (size_t)s->rows, s->hidden);
     f.gate = mlp_call(s, MLP_GATE, 0, 0);
     f.gate.p[0] = product(ox, og, s->rows, s->hidden, s->in);
     f.gate.p[0].b[1] = ou;
-    f.gate.product = mine;
+    f.gate.product = k.operand(s, (size_t)s->rows, s->hidden);
     if (reserve) {
-        const Reserve r = reserve_of(s, reserve);
         f.gate.gate = r.gate;
         f.gate.up = r.up;
         f.gate.product = r.product;
@@ -551,6 +569,10 @@ lstm_status lstm_gated_mlp_forward(const lstm_gated_mlp_shape *s, const void *x,
     if (!all_on_device(ptrs, 7, dev)) return LSTM_ERR_DEVICE;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const Forward f = forward_of(s, x, x_stride, w_gate, w_up, w_down, y, reserve, workspace);
+    if (f.few) {
+        if ((rc = launched(launch_mlp_few(f.few_gate, st))) != LSTM_OK) return rc;
+        return launched(launch_mlp_few(f.few_down, st));
+    }
     if ((rc = launched(f.ops.launch(st))) != LSTM_OK) return rc;
     if ((rc = launched(launch_mlp(f.gate, st))) != LSTM_OK) return rc;
     return launched(launch_mlp(f.down, st));

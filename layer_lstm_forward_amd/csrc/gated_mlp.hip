@@ -16,8 +16,6 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int KS = 64;  // of the contraction, a stage
-
 // The pairs of planes whose products make one product of fp32 matrices, the
 // smallest first: what they leave out is below 2^-24 of each operand.
 __device__ constexpr int kPairA[6] = {2, 1, 0, 1, 0, 0}, kPairB[6] = {0, 1, 2, 0, 1, 0};
@@ -208,18 +206,26 @@ __device__ inline void finish(const MlpCall &c, const MlpProduct &p, Place at, i
 }
 
 // ------------------------------------------------------------------ operands
-// One stage of an operand lies in LDS as ROWS rows of 64 values (k along the
-// rows) or as 64 rows of ROWS values (k along the columns), filled by loads
+// One stage, KS of the contraction, of an operand lies in LDS as ROWS rows of KS
+// values (k along the rows) or as KS rows of ROWS values (k along the columns),
+// filled by loads
 // that write 64 16-byte pieces to consecutive places, so the place decides
 // which piece a lane fetches.  Pieces are permuted inside a row such that the
 // lanes of a fragment read fall on all banks:
-//   rows of 64 values (128 bytes): piece p of row r lies at p ^ (r / 2 % 8);
+//   rows of 64 values (128 bytes): piece p of row r lies at p ^ (r / 2 % 8), of
+//   32 values at p ^ (r / 4 % 4);
 //   columns: 64-byte groups g of row k lie at g ^ (k % 4), with 128-byte rows
 //   (ROWS = 64) at g ^ (k / 2 % 2).
-template <int ROWS, bool COLS, bool DUAL>
+template <int ROWS, int KS, bool COLS, bool DUAL>
 struct Side {
-    static constexpr int PER = ROWS / 32;       // loads of a wave for a stage
-    static constexpr int RB = COLS ? ROWS * 2 : 128;  // bytes of a row in LDS
+    static constexpr int PER = ROWS * KS / 2048;         // loads of a wave for a stage
+    static constexpr int RB = COLS ? ROWS * 2 : KS * 2;  // bytes of a row in LDS
+    static constexpr int PP = RB / 16;                   // pieces of a row
+    static_assert(PER > 0 && (KS == 64 || KS == 32), "stage");
+    static __device__ int key_of(int row) {
+        if (COLS) return ROWS == 64 ? (row >> 1) & 1 : row & 3;  // of 64-byte groups
+        return KS == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
+    }
     const char *seg[2];  // of this tile: first row (or column), k = 0
     long long ld2;       // bytes from row to row
     long long bytes[2];  // of the tile's part from seg on
@@ -234,14 +240,12 @@ struct Side {
         for (int i = 0; i < PER; ++i) {
             const int blk = w + 4 * i;
             if constexpr (COLS) {
-                constexpr int PP = ROWS / 8;  // pieces a row
                 const int k = blk * (64 / PP) + lane / PP, p = lane % PP;
-                const int g = ROWS == 64 ? (p >> 2) ^ ((k >> 1) & 1) : (p >> 2) ^ (k & 3);
-                off[i] = (unsigned)(k * ld2) + (g * 4 + (p & 3)) * 16;
+                off[i] = (unsigned)(k * ld2) + (((p >> 2) ^ key_of(k)) * 4 + (p & 3)) * 16;
             } else {
                 // (two matrices side by side: the second's rows count anew)
-                const int row = (DUAL ? blk % (ROWS / 16) : blk) * 8 + lane / 8;
-                const int p = (lane & 7) ^ ((blk * 8 + lane / 8) >> 1 & 7);
+                const int in = lane / PP, row = (DUAL ? blk % (ROWS * PP / 128) : blk) * (64 / PP) + in;
+                const int p = (lane % PP) ^ key_of(blk * (64 / PP) + in);
                 off[i] = (unsigned)(row * ld2) + p * 16;
                 kpiece = p * 8;
             }
@@ -292,10 +296,10 @@ struct Side {
         if constexpr (COLS) {
             const int m = lane % 16;
             r.a = (8 * (lane >> 5) + (m >> 2)) * RB + ((lane >> 4) & 1) * 32 + (m & 3) * 8;
-            r.key = ROWS == 64 ? m >> 3 : m >> 2;  // of k = ... + m / 4
+            r.key = key_of(m >> 2);  // of k = 4 ... + m / 4
         } else {
             r.a = (lane & 31) * RB;
-            r.key = ((lane & 31) >> 1) & 7;
+            r.key = key_of(lane & 31);
         }
         return r;
     }
@@ -319,10 +323,12 @@ struct Side {
     }
 };
 
-// Every load of this wave is in LDS and none of its LDS reads is under way;
-// then the other waves'.
+// All but LEFT of this wave's loads are in LDS and none of its LDS reads is under
+// way; then the other waves'.
+template <int LEFT = 0>
 __device__ inline void stage_barrier() {
-    __builtin_amdgcn_s_waitcnt(7 << 4);
+    static_assert(LEFT < 64, "vmcnt field");
+    __builtin_amdgcn_s_waitcnt(7 << 4 | (LEFT & 15) | (LEFT >> 4) << 14);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -359,20 +365,21 @@ __device__ inline int tile_of(const MlpCall &c, int id, int &tm, int &tn) {
 // A workgroup takes one unit after the other: the first `whole` are tiles, the
 // others the parts, in k, of the tiles that would not fill a last round.  The
 // first loads of a unit go out before the one before it is finished off.
-template <int BM, int BN, int EPI, bool ACOLS, bool BCOLS, bool F32_>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
+template <class TL, int EPI, bool ACOLS, bool BCOLS, bool F32_>
+__global__ __launch_bounds__(256, TL::HELD > 1 ? 2 : 1) void k_mlp(MlpCall c) {
+    constexpr int BM = TL::BM, BN = TL::BN, KS = TL::KS, KC = KS / 16, NBUF = TL::NBUF;
     constexpr bool DUAL = EPI == MLP_GATE;
     constexpr int TM = BM / 64, TN = BN / 64, TO = DUAL ? TN / 2 : TN;  // 32 x 32 tiles of a wave; of its results
     constexpr unsigned ABYTES = BM * KS * 2, STAGE = (BM + BN) * KS * 2;
     constexpr int PAIRS = F32_ ? 6 : 1, NCOLS = DUAL ? BN / 2 : BN;
-    constexpr bool OWN_SLAB = BM == 256;  // LDS for the results besides the stages
+    constexpr bool OWN_SLAB = TL::HELD == 1;  // LDS for the results besides the stages
     extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = w >> 1, wn = w & 1;
     const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
 
-    Side<BM, ACOLS, false> sa;
-    Side<BN, BCOLS, DUAL> sb;
+    Side<BM, KS, ACOLS, false> sa;
+    Side<BN, KS, BCOLS, DUAL> sb;
     const auto la = sa.lane_of(lane);
     const auto lb = sb.lane_of(lane);
     constexpr int LOADS = sa.PER + sb.PER;
@@ -427,14 +434,14 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
         else
             sb.load(i - sa.PER, kt * KS, buf + ABYTES, w);
     };
-    // the first stage's loads and half of the second's
+    // the loads of the first NBUF - 1 stages and half of the next one's
     auto begin = [&](const Unit &t) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(i, lds0);
-        if (t.stages > 1) {
-            next(t);
+        for (int s = 0; s < NBUF; ++s) {
+            if (s >= t.stages) break;
+            if (s > 0) next(t);
 #pragma unroll
-            for (int i = 0; i < LOADS / 2; ++i) load(i, lds0 + STAGE);
+            for (int i = 0; i < (s == NBUF - 1 ? LOADS / 2 : LOADS); ++i) load(i, lds0 + s * STAGE);
         }
     };
 
@@ -466,21 +473,25 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-        // Loads run two stages ahead: those of a stage go out behind the products
-        // of the last quarter of the stage two before it, as soon as its buffer
-        // is free, and of the first quarter of the next.
-        constexpr int EACH = (LOADS + 2 * TM - 1) / (2 * TM);
+        // Loads run NBUF stages ahead: those of a stage go out as soon as its
+        // buffer is free, behind the products of the last part of the stage that
+        // had it and of the first part of the one after that.
+        constexpr int HALF = LOADS - LOADS / 2, EACH = (HALF + TM - 1) / TM;
         stage_barrier();
         frags(smem, 0, 0);
+        unsigned here = 0, last = (NBUF - 1) * STAGE;  // the buffers of stages s and s - 1
         for (int s = 0; s < t.stages; ++s) {
-            const unsigned here = (s & 1) * STAGE, there = STAGE - here;
-            const bool more = s + 1 < t.stages, more2 = s + 2 < t.stages;
+            const unsigned there = here == (NBUF - 1) * STAGE ? 0 : here + STAGE;
+            const bool more = s + 1 < t.stages, late = s + NBUF - 1 < t.stages, early = s + NBUF < t.stages;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k < 3) {
+            for (int k = 0; k < KC; ++k) {
+                if (k < KC - 1) {
                     frags(smem + here, k + 1, (k + 1) & 1);
                 } else if (more) {
-                    stage_barrier();
+                    if (NBUF > 2 && late)
+                        stage_barrier<(NBUF - 2) * LOADS>();
+                    else
+                        stage_barrier();
                     frags(smem + there, 0, 0);
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -490,20 +501,22 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
 #pragma unroll
                     for (int j = 0; j < TN; ++j)
                         acc[i][j] = mma32_chunk(BF16{}, acc[i][j], fb[k & 1][j], fa[k & 1][i]);
-                    if (k == 0 && more) {
+                    if (k == 0 && late) {
 #pragma unroll
                         for (int x = 0; x < EACH; ++x)
-                            if (LOADS / 2 + i * EACH + x < LOADS) load(LOADS / 2 + i * EACH + x, lds0 + there);
+                            if (LOADS / 2 + i * EACH + x < LOADS) load(LOADS / 2 + i * EACH + x, lds0 + last);
                     }
-                    if (k == 3 && more2) {
+                    if (k == KC - 1 && early) {
 #pragma unroll
                         for (int x = 0; x < EACH; ++x)
                             if (i * EACH + x < LOADS / 2) load(i * EACH + x, lds0 + here);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (k == 0 && more2) next(t);
+                if (k == 0 && early) next(t);
             }
+            last = here;
+            here = there;
         }
 
         // The next unit's first loads, then this one's results (with the small
@@ -524,9 +537,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
         constexpr int WIDE = TO > 1 && !DUAL ? 2 : 1, CPR = 4 * WIDE, ITS = CPR / 2;  // chunks of a row; of a lane
         constexpr int STEPS = TM * TO / WIDE;
         constexpr bool READS = EPI == MLP_DGATE;
-        float *slab = reinterpret_cast<float *>(smem + (OWN_SLAB ? 2 * STAGE : 0)) + w * 2048;
+        float *slab = reinterpret_cast<float *>(smem + (OWN_SLAB ? NBUF * STAGE : 0)) + w * 2048;
         const int r0 = lane / CPR, c0 = lane % CPR;
-        Kept<F32_> kg[2][READS ? ITS : 1], ku[2][READS ? ITS : 1];
+        // g and u of a step, of the next one, too, where registers allow
+        constexpr int AHEAD = OWN_SLAB && !F32_ ? 1 : 0;
+        Kept<F32_> kg[AHEAD + 1][READS ? ITS : 1], ku[AHEAD + 1][READS ? ITS : 1];
         const long long ld = EPI == MLP_STORE ? p.ldo : c.ld;
         const int mw = done.m0 + wm * (BM / 2), nw = done.n0 + wn * (32 * TO);  // the wave's rows and columns
         const size_t corner = (size_t)mw * ld + nw;
@@ -539,12 +554,12 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
 #pragma unroll
             for (int it = 0; it < ITS; ++it)
                 if (row_of(step, it) < rows && col_of(step) < cols) {
-                    kg[step & 1][it].load(c.gate, place(step, it));
-                    ku[step & 1][it].load(c.up, place(step, it));
+                    kg[step & AHEAD][it].load(c.gate, place(step, it));
+                    ku[step & AHEAD][it].load(c.up, place(step, it));
                 }
         };
         if constexpr (READS)
-            if (done.part < 0) fetch(0);
+            if (AHEAD && done.part < 0) fetch(0);
         each<STEPS>([&](auto at) {
             constexpr int step = decltype(at)::value, i = step / (TO / WIDE), jw = step % (TO / WIDE);
 #pragma unroll
@@ -557,7 +572,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
                         f32x4{x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]};
                 }
             if constexpr (READS)
-                if (step + 1 < STEPS && done.part < 0) fetch(step + 1);
+                if (step + AHEAD < STEPS && done.part < 0) fetch(step + AHEAD);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             each<ITS>([&](auto ati) {
                 constexpr int it = decltype(ati)::value;
@@ -579,8 +594,8 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
                     store8f(to, v);
                     if (DUAL) store8f(to + BN / 2, u);
                 } else if (row_of(step, it) < rows && col_of(step) < cols) {
-                    finish<EPI, F32_>(c, p, place(step, it), cols - col_of(step), v, u, kg[step & 1][READS ? it : 0],
-                                      ku[step & 1][READS ? it : 0]);
+                    finish<EPI, F32_>(c, p, place(step, it), cols - col_of(step), v, u, kg[step & AHEAD][READS ? it : 0],
+                                      ku[step & AHEAD][READS ? it : 0]);
                 }
                 if constexpr (READS) __builtin_amdgcn_sched_barrier(0);
             });
@@ -597,8 +612,9 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_mlp(MlpCall c) {
 }
 
 // The sums of tiles whose contraction was split, in the parts' order.
-template <int BM, int BN, int EPI, bool F32_>
+template <class TL, int EPI, bool F32_>
 __global__ __launch_bounds__(256) void k_mlp_join(MlpCall c) {
+    constexpr int BM = TL::BM, BN = TL::BN;
     constexpr bool DUAL = EPI == MLP_GATE;
     constexpr int NCOLS = DUAL ? BN / 2 : BN, PER = BM * NCOLS / 8;
     int tm, tn;
@@ -631,6 +647,143 @@ __global__ __launch_bounds__(256) void k_mlp_join(MlpCall c) {
     finish<EPI, F32_>(c, p, at, p.N - col, v, u, kg, ku);
 }
 
+// ------------------------------------------------------------------ few rows
+// Up to 16 NT rows x: the weights' traffic is all that counts.  A workgroup
+// takes 16 rows of a weight (GATE: of gate and of up), its NW waves every NW-th
+// 128 bytes of k.  Weights go from memory to registers as fragments (lane (m, g):
+// row m, 16 bytes at 16 g of each 64), several on their way at a time, and meet
+// the rows of x, which stay in the caches, on 16 x 16 tiles.  fp32 runs on fp32
+// matrix instructions: memory is slower than they are.
+template <class DT>
+__device__ inline u32x4 few_load(const char *row, int k, int K) {
+    using S = typename DT::S;
+    const S *q = reinterpret_cast<const S *>(row);
+    S t[DT::PER16];
+    if (k + DT::PER16 <= K) {
+        __builtin_memcpy(t, q + k, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < DT::PER16; ++e) t[e] = k + e < K ? q[k + e] : (S)0;
+    }
+    return __builtin_bit_cast(u32x4, t);
+}
+
+template <class DT, int NT, bool GATE>
+__global__ __launch_bounds__(GATE ? 512 : 1024) void k_mlp_few(MlpFew c) {
+    constexpr bool F32_ = sizeof(typename DT::S) == 4;
+    constexpr int NW = GATE ? 8 : 16, D = GATE ? 2 : 1, U = NT > 2 ? 2 : 4;  // U: fragments of each on their way
+    __shared__ f32x4 sums[NW][D][NT][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    constexpr long long ES = sizeof(typename DT::S);
+    const long long row = (long long)min(n0 + m, c.N - 1) * c.K * ES;  // past the last: it again, its sums are dropped
+    const char *wa = c.w[0] + row, *wb = GATE ? c.w[1] + row : nullptr;
+    const char *x[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) x[t] = c.x + min(16 * t + m, c.rows - 1) * c.xs * ES;
+    f32x4 acc[D][NT];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[d][t] = f32x4{0, 0, 0, 0};
+    constexpr int LINE = 2 * DT::KC;  // k of a 128-byte line: two fragments
+    for (int k0 = w * LINE; k0 < c.K; k0 += NW * LINE * (U / 2)) {
+        u32x4 a[D][U], b[NT][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + (u / 2) * NW * LINE + (u % 2) * DT::KC + g * DT::PER16;
+            a[0][u] = few_load<DT>(wa, k, c.K);
+            if (GATE) a[D - 1][u] = few_load<DT>(wb, k, c.K);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) b[t][u] = few_load<DT>(x[t], k, c.K);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int d = 0; d < D; ++d) acc[d][t] = mma_chunk(DT{}, acc[d][t], a[d][u], b[t][u]);
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sums[w][d][t][lane] = acc[d][t];
+    __syncthreads();
+    // thread (t, lane): the waves' sums in their order, of row 16 t + m and four columns
+    if (threadIdx.x >= NT * 64) return;
+    const int t = threadIdx.x >> 6, r = 16 * t + m, col = n0 + 4 * g;
+    f32x4 v[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        for (int i = 0; i < NW; ++i) v[d] += sums[i][d][t][lane];
+    if (r >= c.rows) return;
+    if constexpr (!GATE) {
+        auto *o = reinterpret_cast<typename DT::S *>(c.out) + (long long)r * c.N + col;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < c.N) o[e] = round_to<DT>(v[0][e]);
+    } else {
+        if (col >= c.ld) return;
+        float h[4], gv[8], av[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gv[e] = v[0][e % 4];
+        activate<false>(c.act, gv, av, nullptr);
+        const size_t at = (size_t)r * c.ld + col;
+        uint32_t bits[2][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = col + e < c.N;  // up to ld zeros
+            h[e] = in ? av[e] * v[1][e] : 0.0f;
+            bits[0][e] = in ? __float_as_uint(v[0][e]) : 0u;
+            bits[1][e] = in ? __float_as_uint(v[1][e]) : 0u;
+        }
+        typename DT::S s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = round_to<DT>(h[e]);
+        __builtin_memcpy(c.out + at * ES, s, sizeof(s));
+        if (!c.keep.p) return;
+        // as Kept and store_planes write them
+        const MlpKept *kept[2] = {&c.gate, &c.up};
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            if constexpr (F32_) {
+                __builtin_memcpy(kept[d]->p + at * 4, bits[d], 16);
+            } else {
+                uint16_t high[4];
+                unsigned char low[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) high[e] = bits[d][e] >> 16, low[e] = bits[d][e] >> 8 & 0xFF;
+                __builtin_memcpy(kept[d]->p + at * 2, high, 8);
+                __builtin_memcpy(kept[d]->p + kept[d]->low + at, low, 4);
+            }
+        }
+        char *planes = const_cast<char *>(c.keep.p) + at * 2;
+#pragma unroll
+        for (int k = 0; k < (F32_ ? 3 : 1); ++k) {
+            uint16_t q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float f = F32_ && k < 2 ? first_term(h[e]) : h[e];
+                q[e] = round_to<BF16>(f);
+                h[e] -= f;
+            }
+            __builtin_memcpy(planes + k * c.keep.plane, q, 8);
+        }
+    }
+}
+
+template <class DT, bool GATE>
+hipError_t run_few(const MlpFew &c, hipStream_t s) {
+    const dim3 grid(GATE ? (unsigned)((c.ld + 15) / 16) : (c.N + 15) / 16), block(GATE ? 512 : 1024);
+    if (c.rows <= 16)
+        hipLaunchKernelGGL((k_mlp_few<DT, 1, GATE>), grid, block, 0, s, c);
+    else if (c.rows <= 32)
+        hipLaunchKernelGGL((k_mlp_few<DT, 2, GATE>), grid, block, 0, s, c);
+    else
+        hipLaunchKernelGGL((k_mlp_few<DT, 4, GATE>), grid, block, 0, s, c);
+    return hipGetLastError();
+}
+
 template <bool F32_>
 __global__ __launch_bounds__(256) void k_mlp_planes(const char *src, long long ld, long long rows, int cols,
                                                     MlpOperand to) {
@@ -655,14 +808,31 @@ __global__ __launch_bounds__(256) void k_mlp_planes(const char *src, long long l
     }
 }
 
-// The tiles, how many workgroups of them a CU holds, and the microseconds of a
-// stage in each when all run, and of a unit besides.
+// Tiles of BM x BN, stages of KS, NBUF of them in LDS, and HELD workgroups on a
+// CU; a GATE tile has BN / 2 columns.
+template <int BM_, int BN_, int KS_, int NBUF_, int HELD_>
+struct MlpTile {
+    static constexpr int BM = BM_, BN = BN_, KS = KS_, NBUF = NBUF_, HELD = HELD_;
+    static constexpr int SLAB = HELD == 1 ? 32768 : 0, LDS = NBUF * (BM + BN) * KS * 2 + SLAB;
+    static_assert(LDS * HELD <= 163840 && LDS >= 32768, "LDS");
+};
+using Tile0 = MlpTile<256, 256, 64, 2, 1>;
+using Tile1 = MlpTile<128, 128, 64, 2, 2>;
+using Tile2 = MlpTile<64, 128, 64, 3, 2>;
+
+// Of each tile: the microseconds of 64 of the contraction in each workgroup when
+// all run, and of a unit besides.
 struct Tile {
-    int m, n, gate_n;  // gate_n: columns of a GATE tile (half of its operand's rows)
-    int held;
+    int m, n, held;
     float stage, unit;
 };
-constexpr Tile kTiles[3] = {{256, 256, 128, 1, 2.0f, 8.0f}, {128, 128, 64, 2, 1.3f, 5.0f}, {64, 64, 64, 3, 0.9f, 4.0f}};
+template <class TL>
+constexpr Tile tile_of_type(float stage, float unit) {
+    return {TL::BM, TL::BN, TL::HELD, stage, unit};
+}
+constexpr int kTileCount = 3;
+constexpr Tile kTiles[kTileCount] = {tile_of_type<Tile0>(1.9f, 7.0f), tile_of_type<Tile1>(1.1f, 5.0f),
+                                     tile_of_type<Tile2>(0.8f, 4.0f)};
 constexpr int kCus = 256;
 
 unsigned blocks(long long n) {
@@ -670,29 +840,25 @@ unsigned blocks(long long n) {
     return (unsigned)(n < 1 ? 1 : n > 8192 ? 8192 : n);
 }
 
-template <int BM, int BN, int EPI, bool AC, bool BC, bool F32_>
+template <class TL, int EPI, bool AC, bool BC, bool F32_>
 hipError_t run(const MlpCall &c, const MlpPlan &plan, hipStream_t s) {
-    constexpr int smem = 2 * (BM + BN) * KS * 2 + (BM == 256 ? 32768 : 0);
-    static_assert(smem <= 163840 && smem >= 32768, "LDS");
-    const void *fn = reinterpret_cast<const void *>(&k_mlp<BM, BN, EPI, AC, BC, F32_>);
-    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const void *fn = reinterpret_cast<const void *>(&k_mlp<TL, EPI, AC, BC, F32_>);
+    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, TL::LDS);
     if (e != hipSuccess) return e;
-    const int slots = kCus * kTiles[plan.tile].held;
-    hipLaunchKernelGGL((k_mlp<BM, BN, EPI, AC, BC, F32_>), dim3(c.units < slots ? c.units : slots), dim3(256), smem, s,
-                       c);
+    const int slots = kCus * TL::HELD;
+    hipLaunchKernelGGL((k_mlp<TL, EPI, AC, BC, F32_>), dim3(c.units < slots ? c.units : slots), dim3(256), TL::LDS, s, c);
     if (plan.split_tiles) {
-        constexpr int per = BM * (EPI == MLP_GATE ? BN / 2 : BN) / 8;
-        hipLaunchKernelGGL((k_mlp_join<BM, BN, EPI, F32_>), dim3((per + 255) / 256, plan.split_tiles), dim3(256), 0, s,
-                           c);
+        constexpr int per = TL::BM * (EPI == MLP_GATE ? TL::BN / 2 : TL::BN) / 8;
+        hipLaunchKernelGGL((k_mlp_join<TL, EPI, F32_>), dim3((per + 255) / 256, plan.split_tiles), dim3(256), 0, s, c);
     }
     return hipGetLastError();
 }
 
 template <int EPI, bool AC, bool BC, bool F32_>
 hipError_t launch(const MlpCall &c, const MlpPlan &plan, hipStream_t s) {
-    if (plan.tile == 0) return run<256, 256, EPI, AC, BC, F32_>(c, plan, s);
-    if (plan.tile == 1) return run<128, 128, EPI, AC, BC, F32_>(c, plan, s);
-    return run<64, EPI == MLP_GATE ? 128 : 64, EPI, AC, BC, F32_>(c, plan, s);
+    if (plan.tile == 0) return run<Tile0, EPI, AC, BC, F32_>(c, plan, s);
+    if (plan.tile == 1) return run<Tile1, EPI, AC, BC, F32_>(c, plan, s);
+    return run<Tile2, EPI, AC, BC, F32_>(c, plan, s);
 }
 
 template <int EPI, bool AC, bool BC>
@@ -702,7 +868,7 @@ hipError_t launch(const MlpCall &c, const MlpPlan &plan, hipStream_t s) {
 
 long long tiles_of(const MlpCall &c, int tile, MlpCall *to) {
     long long n = 0;
-    const int bn = c.epilogue == MLP_GATE ? kTiles[tile].gate_n : kTiles[tile].n;
+    const int bn = c.epilogue == MLP_GATE ? kTiles[tile].n / 2 : kTiles[tile].n;
     for (int i = 0; i < c.count; ++i) {
         const long long tm = (c.p[i].M + kTiles[tile].m - 1) / kTiles[tile].m, tn = (c.p[i].N + bn - 1) / bn;
         if (to) to->p[i].tiles_m = (int)tm, to->p[i].tiles_n = (int)tn;
@@ -719,25 +885,26 @@ long long tiles_of(const MlpCall &c, int tile, MlpCall *to) {
 MlpPlan mlp_plan(const MlpCall &c) {
     MlpPlan best{};
     double least = 1e30;
-    double stages = 0;  // of a tile (the longest product's)
+    double stages = 0;  // of 64, of a tile (the longest product's)
     for (int i = 0; i < c.count; ++i) {
-        const double n = (double)((c.p[i].K + KS - 1) / KS) * c.p[i].lists * (c.dtype == LSTM_F32 ? 6 : 1);
+        const double n = (double)((c.p[i].K + 63) / 64) * c.p[i].lists * (c.dtype == LSTM_F32 ? 6 : 1);
         if (n > stages) stages = n;
     }
-    for (int tile = 0; tile < 3; ++tile) {
+    for (int tile = 0; tile < kTileCount; ++tile) {
         const Tile &t = kTiles[tile];
         const long long n = tiles_of(c, tile, nullptr), slots = kCus * t.held, rem = n % slots;
-        const double area = (double)t.m * (c.epilogue == MLP_GATE ? 2 * t.gate_n : t.n) * sizeof(float);
-        const double wide = c.epilogue == MLP_GATE && tile == 2 ? 1.5 : 1.0;
+        const double area = (double)t.m * t.n * sizeof(float);
         auto offer = [&](long long whole, long long splits) {
             const long long split_tiles = splits > 1 ? n - whole : 0;
             double us = 0;
-            const long long rounds = (whole + slots - 1) / slots;
-            us += rounds * (stages * t.stage * wide + t.unit);
-            if (split_tiles) {
-                us += ((split_tiles * splits + slots - 1) / slots) * (stages / splits * t.stage * wide + t.unit);
-                us += 4.0 + 2 * split_tiles * splits * area / 4e6;
-            }
+            // (alone on its CU a workgroup of a small tile takes two thirds of that)
+            auto units = [&](long long n, double stages) {
+                const long long last = n % slots;
+                const double one = stages * t.stage + t.unit;
+                return n / slots * one + (last == 0 ? 0.0 : last <= kCus && t.held > 1 ? one * 0.67 : one);
+            };
+            us += units(whole, stages);
+            if (split_tiles) us += units(split_tiles * splits, stages / splits) + 4.0 + 2 * split_tiles * splits * area / 4e6;
             if (us < least) {
                 least = us;
                 best.tile = tile;
@@ -769,6 +936,11 @@ hipError_t launch_mlp(const MlpCall &call, hipStream_t s) {
     if (c.a_cols) return launch<MLP_STORE, true, true>(c, plan, s);
     if (c.b_cols) return launch<MLP_STORE, false, true>(c, plan, s);
     return launch<MLP_STORE, false, false>(c, plan, s);
+}
+
+hipError_t launch_mlp_few(const MlpFew &c, hipStream_t s) {
+    if (c.w[1]) return c.dtype == LSTM_F32 ? run_few<F32, true>(c, s) : run_few<BF16, true>(c, s);
+    return c.dtype == LSTM_F32 ? run_few<F32, false>(c, s) : run_few<BF16, false>(c, s);
 }
 
 hipError_t launch_mlp_planes(int dtype, const void *src, long long ld, long long rows, int cols, const MlpOperand &to,
