@@ -27,8 +27,8 @@ struct GrCall {
     int T, B, width, dtype;
     int nseg, seg_tokens;
 };
-// Segments a sequence is cut into, and their tokens.
-void gr_segments(int T, int B, int width, int dtype, bool backward, int *nseg, int *seg_tokens);
+// Segments a sequence is cut into, and their tokens; 0: one, in tiles.
+void gr_plan(int T, int B, int width, int dtype, bool backward, int *nseg, int *seg_tokens);
 hipError_t launch_gr_forward(const GrCall &c, hipStream_t s);
 hipError_t launch_gr_backward(const GrCall &c, hipStream_t s);
 

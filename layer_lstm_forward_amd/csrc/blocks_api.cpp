@@ -37,7 +37,7 @@ lstm_status gr_size(const lstm_gated_recurrence_shape *s, bool backward, GrCall 
     const lstm_status rc = gr_check(s);
     if (rc != LSTM_OK) return rc;
     if (!bytes) return LSTM_ERR_ARG;
-    gr_segments(s->T, s->B, s->width, s->dtype, backward, &c->nseg, &c->seg_tokens);
+    gr_plan(s->T, s->B, s->width, s->dtype, backward, &c->nseg, &c->seg_tokens);
     *bytes = 0;
     if (c->nseg > 1 && !add_bytes(bytes, 2 * (size_t)c->nseg, (size_t)s->B, (size_t)s->width, sizeof(float)))
         return LSTM_ERR_SHAPE;

@@ -832,7 +832,7 @@ constexpr Tile tile_of_type(float stage, float unit) {
 }
 constexpr int kTileCount = 3;
 constexpr Tile kTiles[kTileCount] = {tile_of_type<Tile0>(1.9f, 7.0f), tile_of_type<Tile1>(1.1f, 5.0f),
-                                     tile_of_type<Tile2>(0.8f, 4.0f)};
+                                     tile_of_type<Tile2>(0.7f, 4.0f)};
 constexpr int kCus = 256;
 
 unsigned blocks(long long n) {

@@ -2,12 +2,16 @@
 // and backward, and single tokens.
 //     z = s(-f) (= 1 - a),  w = s(i) or z,  h_t = h_{t-1} - z h_{t-1} + w x_t
 //     D_t = dy_t + E_{t+1},  E_t = D_t - z D_t  (E: what reaches h_{t-1})
-//     dx = w D,  df = D (h_{t-1} - [w = z] x) z (1 - z),  di = D x w (1 - w)
-// A thread walks the tokens of V neighbouring channels of a batch row, 16 bytes
-// of each tensor at a time.  Where the channels do not fill the card the
-// sequence is cut into segments: one launch takes each segment's own map
-// (carry -> A carry + B, A the product of its 1 - z), one joins them, and one
-// walks the segments from the states that they begin with.
+//     dx = w D,  df = D (h_{t-1} - [w = z] x) z a,  di = D x w (1 - w)
+// Two ways, chosen by an estimate of their times (gr_plan):
+// k_gr_lanes: a thread walks the tokens of V neighbouring channels of a batch
+// row, the next tokens' values under way meanwhile.  Where the channels do not
+// fill the card the sequence is cut into segments: one launch takes each
+// segment's own map (carry -> A carry + B, A the product of its 1 - z), one
+// joins them, and one walks the segments from the carries that they begin with.
+// k_gr_tile, for little work: a workgroup spreads the tokens of 128 bytes of
+// channels over its threads and scans their maps: one launch, and memory is
+// read once, but each tile waits for its loads.
 #include <type_traits>
 
 #include "blocks.h"
@@ -17,7 +21,7 @@
 namespace lstm_amd {
 namespace {
 
-constexpr int U = 8;  // tokens on their way at a time
+constexpr int LN = 8;  // lanes of a token's channels: 128 bytes
 
 template <class DT, int V>
 __device__ inline void gr_load(const char *p, float *v) {
@@ -48,6 +52,23 @@ struct Raw {
     __device__ float at(int e) const { return DT::to_f(s[e]); }
 };
 
+template <class DT>
+__device__ inline const char *gr_at(const GrView &v, int b, int ch, int t) {
+    return v.p + (v.t * t + v.b * b + ch) * (long long)sizeof(typename DT::S);
+}
+
+__device__ inline int gr_length(const GrCall &c, int b) {
+    return c.lengths ? min(max(c.lengths[b], 0), c.T) : c.T;
+}
+
+// s(-f) and s(f), each with all its digits.
+__device__ inline void gates(float f, float &z, float &a) {
+    const float e = __builtin_amdgcn_exp2f(fabsf(f) * -1.4426950408889634f), big = __builtin_amdgcn_rcpf(1.0f + e);
+    const float small = e * big;
+    z = f < 0.0f ? big : small;
+    a = f < 0.0f ? small : big;
+}
+
 // The thread's batch row and first channel.  Where the width is no multiple of
 // V the last piece ends with the row, and its first `own` values are read but
 // are the thread before's to write (state and state_out may be one memory).
@@ -63,171 +84,315 @@ __device__ inline bool gr_place(const GrCall &c, int *b, int *ch, int *own) {
     return true;
 }
 
-template <class DT>
-__device__ inline const char *gr_at(const GrView &v, int b, int ch, int t) {
-    return v.p + (v.t * t + v.b * b + ch) * (long long)sizeof(typename DT::S);
-}
-
-__device__ inline int gr_length(const GrCall &c, int b) {
-    return c.lengths ? min(max(c.lengths[b], 0), c.T) : c.T;
-}
-
-// APPLY: the outputs; else the segment's map, to the workspace.
-template <class DT, int V, bool INPUT, bool APPLY>
-__global__ __launch_bounds__(256) void k_gr_forward(GrCall c) {
+// SUM: the segment's map, to the workspace; else the outputs.  Backward the
+// tokens count from the segment's end.
+template <class DT, int V, bool INPUT, bool BACK, bool SUM>
+__global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
+    // tokens loaded at a time, and as many under way: with more tensors fewer
+    constexpr int U = BACK && !SUM ? 4 : 8;
     int b, ch, own;
     if (!gr_place<V>(c, &b, &ch, &own)) return;
     const int sg = blockIdx.y, n = gr_length(c, b), t0 = sg * c.seg_tokens, t1 = min(t0 + c.seg_tokens, c.T);
-    const int end = min(t1, n);  // of the tokens that count
+    const int end = min(t1, n), count = end - t0;  // of the tokens that count
     const size_t slab = (size_t)c.B * c.width, at = (size_t)b * c.width + ch;
     float h[V], A[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) h[e] = 0.0f, A[e] = 1.0f;
-    if (APPLY) {
-        const float *s = c.nseg > 1 ? c.seg + sg * slab : c.s0;
+    if (!SUM) {
+        const float *s = c.nseg > 1 ? c.seg + sg * slab : BACK ? c.ds1 : c.s0;
         if (s) __builtin_memcpy(h, s + at, sizeof(h));
     }
-    const long long sx = c.x.t * (long long)sizeof(typename DT::S), sf = c.f.t * (long long)sizeof(typename DT::S);
-    const long long si = c.i.t * (long long)sizeof(typename DT::S), sy = c.y.t * (long long)sizeof(typename DT::S);
-    const char *px = gr_at<DT>(c.x, b, ch, t0), *pf = gr_at<DT>(c.f, b, ch, t0);
-    const char *pi = INPUT ? gr_at<DT>(c.i, b, ch, t0) : nullptr;
-    char *py = APPLY ? const_cast<char *>(gr_at<DT>(c.y, b, ch, t0)) : nullptr;
-    Raw<DT, V> x[U], f[U], g[U];
-    auto fetch = [&](int t) {
+    struct Tokens {
+        Raw<DT, V> x[U], f[U], g[U], d[U], p[U];
+    } q[2];
+    auto token = [&](int o) { return BACK ? end - 1 - o : t0 + o; };
+    auto fetch = [&](Tokens &k, int o) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = min(t + u, end - 1) - t0;  // past the end: the last token again
-            x[u].load(px + k * sx);
-            f[u].load(pf + k * sf);
-            if (INPUT) g[u].load(pi + k * si);
+            const int t = token(min(o + u, count - 1));  // past the end: the last token again
+            k.f[u].load(gr_at<DT>(c.f, b, ch, t));
+            if (BACK) k.d[u].load(gr_at<DT>(c.dy, b, ch, t));
+            if (!BACK || !SUM) {
+                k.x[u].load(gr_at<DT>(c.x, b, ch, t));
+                if (INPUT) k.g[u].load(gr_at<DT>(c.i, b, ch, t));
+            }
+            if (BACK && !SUM) k.p[u].load(gr_at<DT>(c.y, b, ch, max(t - 1, 0)));
         }
     };
-    for (int t = t0; t < end; t += U) {
-        fetch(t);
+    auto walk = [&](Tokens &k, int o) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (t + u >= end) break;
-            float y[V];
+            if (o + u >= count) break;
+            const int t = token(o + u);
+            float r[3][V], was[V];
+            if (BACK && !SUM) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) was[e] = k.p[u].at(e);
+                if (t == 0) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) was[e] = 0.0f;
+                    if (c.s0) __builtin_memcpy(was, c.s0 + at, sizeof(was));
+                }
+            }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float z = sigmoid_f(-f[u].at(e)), w = INPUT ? sigmoid_f(g[u].at(e)) : z;
-                h[e] = fmaf(w, x[u].at(e), fmaf(-z, h[e], h[e]));
-                if (!APPLY) A[e] = fmaf(-z, A[e], A[e]);
-                y[e] = h[e];
+                float z, a;
+                if (BACK && !SUM)
+                    gates(k.f[u].at(e), z, a);
+                else
+                    z = sigmoid_f(-k.f[u].at(e));
+                if (!BACK) {
+                    const float w = INPUT ? sigmoid_f(k.g[u].at(e)) : z;
+                    h[e] = fmaf(w, k.x[u].at(e), fmaf(-z, h[e], h[e]));
+                    r[0][e] = h[e];
+                } else {
+                    const float D = k.d[u].at(e) + h[e];
+                    if (!SUM) {
+                        const float x = k.x[u].at(e);
+                        if (INPUT) {
+                            float v, w;
+                            gates(k.g[u].at(e), v, w);
+                            r[0][e] = w * D;
+                            r[1][e] = D * was[e] * (z * a);
+                            r[2][e] = D * x * (w * v);
+                        } else {
+                            r[0][e] = z * D;
+                            r[1][e] = D * (was[e] - x) * (z * a);
+                        }
+                    }
+                    h[e] = fmaf(-z, D, D);
+                }
+                if (SUM) A[e] = fmaf(-z, A[e], A[e]);
             }
-            if (APPLY) gr_store<DT, V>(py + (t + u - t0) * sy, y, own);
+            if (!SUM && !BACK) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), r[0], own);
+            if (!SUM && BACK) {
+                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.dx, b, ch, t)), r[0], own);
+                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.df, b, ch, t)), r[1], own);
+                if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, t)), r[2], own);
+            }
         }
+    };
+    if (count > 0) fetch(q[0], 0);
+    for (int o = 0; o < count; o += 2 * U) {
+        if (o + U < count) fetch(q[1], o + U);
+        walk(q[0], o);
+        if (o + 2 * U < count) fetch(q[0], o + 2 * U);
+        walk(q[1], o + U);
     }
-    if (!APPLY) {
+    if (SUM) {
         float *s = c.seg + sg * slab + at;
         gr_store<F32, V>(reinterpret_cast<char *>(s), h, own);
         gr_store<F32, V>(reinterpret_cast<char *>(s + c.nseg * slab), A, own);
         return;
     }
     const float zero[V] = {};
-    for (int t = max(end, t0); t < t1; ++t) gr_store<DT, V>(py + (t - t0) * sy, zero, own);
-    if (sg == c.nseg - 1 && c.s1) gr_store<F32, V>(reinterpret_cast<char *>(c.s1 + at), h, own);
-}
-
-template <class DT, int V, bool INPUT, bool APPLY>
-__global__ __launch_bounds__(256) void k_gr_backward(GrCall c) {
-    int b, ch, own;
-    if (!gr_place<V>(c, &b, &ch, &own)) return;
-    const int sg = blockIdx.y, n = gr_length(c, b), t0 = sg * c.seg_tokens, t1 = min(t0 + c.seg_tokens, c.T);
-    const int end = min(t1, n);
-    const size_t slab = (size_t)c.B * c.width, at = (size_t)b * c.width + ch;
-    float E[V], A[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) E[e] = 0.0f, A[e] = 1.0f;
-    if (APPLY) {
-        const float *s = c.nseg > 1 ? c.seg + sg * slab : c.ds1;
-        if (s) __builtin_memcpy(E, s + at, sizeof(E));
-    }
-    Raw<DT, V> x[U], f[U], g[U], d[U], h[U];
-    if (APPLY) {
-        const float zero[V] = {};
-        for (int t = max(end, t0); t < t1; ++t) {
+    for (int t = max(end, t0); t < t1; ++t) {
+        if (!BACK) {
+            gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), zero, own);
+        } else {
             gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.dx, b, ch, t)), zero, own);
             gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.df, b, ch, t)), zero, own);
             if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, t)), zero, own);
         }
     }
-    for (int t = end - 1; t >= t0; t -= U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = max(t - u, t0);
-            f[u].load(gr_at<DT>(c.f, b, ch, k));
-            d[u].load(gr_at<DT>(c.dy, b, ch, k));
-            if (APPLY) {
-                x[u].load(gr_at<DT>(c.x, b, ch, k));
-                if (INPUT) g[u].load(gr_at<DT>(c.i, b, ch, k));
-                h[u].load(gr_at<DT>(c.y, b, ch, max(k - 1, 0)));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = t - u;
-            if (k < t0) break;
-            float dx[V], df[V], di[V];
-            float before[V];
-            if (APPLY) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) before[e] = h[u].at(e);
-                if (k == 0) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) before[e] = 0.0f;
-                    if (c.s0) __builtin_memcpy(before, c.s0 + at, sizeof(before));
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float z = sigmoid_f(-f[u].at(e)), D = d[u].at(e) + E[e];
-                if (APPLY) {
-                    const float a = sigmoid_f(f[u].at(e)), xv = x[u].at(e);
-                    if (INPUT) {
-                        const float w = sigmoid_f(g[u].at(e)), v = sigmoid_f(-g[u].at(e));
-                        dx[e] = w * D;
-                        df[e] = D * before[e] * (z * a);
-                        di[e] = D * xv * (w * v);
-                    } else {
-                        dx[e] = z * D;
-                        df[e] = D * (before[e] - xv) * (z * a);
-                    }
-                } else {
-                    A[e] = fmaf(-z, A[e], A[e]);
-                }
-                E[e] = fmaf(-z, D, D);
-            }
-            if (APPLY) {
-                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.dx, b, ch, k)), dx, own);
-                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.df, b, ch, k)), df, own);
-                if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, k)), di, own);
-            }
-        }
-    }
-    if (!APPLY) {
-        float *s = c.seg + sg * slab + at;
-        gr_store<F32, V>(reinterpret_cast<char *>(s), E, own);
-        gr_store<F32, V>(reinterpret_cast<char *>(s + c.nseg * slab), A, own);
-    } else if (sg == 0 && c.ds0) {
-        gr_store<F32, V>(reinterpret_cast<char *>(c.ds0 + at), E, own);
-    }
+    // the state is what the row's last token leaves (or a row of none has)
+    float *const last = BACK ? (sg == 0 ? c.ds0 : nullptr) : (n > t0 || sg == 0) && n <= t1 ? c.s1 : nullptr;
+    if (last) gr_store<F32, V>(reinterpret_cast<char *>(last + at), h, own);
 }
 
-// Each segment's B becomes the carry that it begins with.
+// Each segment's B becomes the carry that it begins with: 16 threads a channel
+// compose a sixteenth of the segments' maps each, then walk them from the
+// carries that these give.
 template <bool BACK>
 __global__ __launch_bounds__(256) void k_gr_join(GrCall c) {
-    const size_t slab = (size_t)c.B * c.width, at = blockIdx.x * 256ull + threadIdx.x;
+    __shared__ float maps[2][16][16];
+    const size_t slab = (size_t)c.B * c.width;
+    const int x = threadIdx.x % 16, y = threadIdx.x / 16;
+    const size_t at = blockIdx.x * 16ull + x;
+    const int per = (c.nseg + 15) / 16, k0 = min(y * per, c.nseg), k1 = min(k0 + per, c.nseg);
+    auto segment = [&](int k) { return c.seg + (BACK ? c.nseg - 1 - k : k) * slab + at; };
+    float A = 1.0f, B = 0.0f;
+    if (at < slab)
+#pragma unroll 8
+        for (int k = k0; k < k1; ++k) {
+            const float *s = segment(k);
+            const float b = *s, a = s[c.nseg * slab];
+            B = fmaf(a, B, b);
+            A *= a;
+        }
+    maps[0][y][x] = A;
+    maps[1][y][x] = B;
+    __syncthreads();
     if (at >= slab) return;
     const float *first = BACK ? c.ds1 : c.s0;
     float carry = first ? first[at] : 0.0f;
+    for (int i = 0; i < y; ++i) carry = fmaf(maps[0][i][x], carry, maps[1][i][x]);
 #pragma unroll 8
-    for (int i = 0; i < c.nseg; ++i) {
-        float *s = c.seg + (BACK ? c.nseg - 1 - i : i) * slab + at;
+    for (int k = k0; k < k1; ++k) {
+        float *s = segment(k);
         const float b = *s, a = s[c.nseg * slab];
         *s = carry;
         carry = fmaf(a, carry, b);
     }
+}
+
+// A tile's threads: LN lanes x TC runs of U tokens.
+template <int TC_, int U_>
+struct GrTile {
+    static constexpr int TC = TC_, U = U_, THREADS = LN * TC, WAVES = THREADS / 64;
+};
+
+// Each thread composes the maps of its U tokens, the workgroup scans the
+// threads' maps, and each thread walks its tokens again from the carry that it
+// begins with.  Backward the tokens count from the row's end.
+template <class DT, int V, bool INPUT, bool BACK, class TL>
+__global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
+    constexpr int U = TL::U, TC = TL::TC, WAVES = TL::WAVES;
+    constexpr long long ES = sizeof(typename DT::S);
+    __shared__ float maps[2][WAVES][LN][2 * V];  // the waves' maps of a tile, in turn
+    const int l = threadIdx.x % LN, run = threadIdx.x / LN, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int slabs = (c.width + LN * V - 1) / (LN * V), b = blockIdx.x / slabs;
+    const int from = (blockIdx.x % slabs * LN + l) * V, ch = min(from, c.width - V), own = from - ch;
+    const int count = gr_length(c, b);  // tokens that count
+    const size_t at = (size_t)b * c.width + ch;
+    const float *first = BACK ? c.ds1 : c.s0;
+    float *const last = BACK ? c.ds0 : c.s1;
+    float carry[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) carry[e] = 0.0f;
+    if (first) __builtin_memcpy(carry, first + at, sizeof(carry));
+    auto tokens = [&](int o) { return BACK ? count - 1 - o : o; };
+    struct Tokens {
+        Raw<DT, V> x[U], f[U], g[U], d[U], h[U];
+    };
+    auto fetch = [&](Tokens &q, int o0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = tokens(min(o0 + u, count - 1));  // past the end: the last token again
+            q.f[u].load(gr_at<DT>(c.f, b, ch, t));
+            if (BACK) q.d[u].load(gr_at<DT>(c.dy, b, ch, t));
+            q.x[u].load(gr_at<DT>(c.x, b, ch, t));
+            if (INPUT) q.g[u].load(gr_at<DT>(c.i, b, ch, t));
+            if (BACK) q.h[u].load(gr_at<DT>(c.y, b, ch, max(t - 1, 0)));
+        }
+    };
+    int turn = 0;
+    for (int o0 = 0; o0 < count; o0 += TC * U, turn ^= 1) {
+        const int mine = o0 + run * U;
+        Tokens q;
+        fetch(q, mine);
+        // the thread's own map
+        float A[V], B[V], z[U][V], w[INPUT && !BACK ? U : 1][V];
+        auto in = [&](int u, int e) {  // x or dy, 0 past the end
+            return mine + u < count ? BACK ? q.d[u].at(e) : q.x[u].at(e) : 0.0f;
+        };
+        auto gate = [&](int u, int e) { return INPUT ? w[INPUT && !BACK ? u : 0][e] : z[u][e]; };
+#pragma unroll
+        for (int e = 0; e < V; ++e) A[e] = 1.0f, B[e] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool on = mine + u < count;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                z[u][e] = on ? sigmoid_f(-q.f[u].at(e)) : 0.0f;
+                if (BACK) {
+                    const float D = in(u, e) + B[e];
+                    B[e] = fmaf(-z[u][e], D, D);
+                } else {
+                    if (INPUT) w[INPUT && !BACK ? u : 0][e] = on ? sigmoid_f(q.g[u].at(e)) : 0.0f;
+                    B[e] = fmaf(gate(u, e), in(u, e), fmaf(-z[u][e], B[e], B[e]));
+                }
+                A[e] = fmaf(-z[u][e], A[e], A[e]);
+            }
+        }
+        // Scan: the threads of a wave with the same channels (LN lanes apart),
+        // then the waves.  (A, B) after (A', B') is (A A', A B' + B).
+#pragma unroll
+        for (int s = LN; s < 64; s *= 2) {
+            const bool on = lane >= s;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float a = __shfl_up(A[e], s), p = __shfl_up(B[e], s);
+                B[e] = on ? fmaf(A[e], p, B[e]) : B[e];
+                A[e] = on ? A[e] * a : A[e];
+            }
+        }
+        if (lane >= 64 - LN)
+#pragma unroll
+            for (int e = 0; e < V; ++e) maps[turn][wave][l][e] = A[e], maps[turn][wave][l][V + e] = B[e];
+        // what a thread begins with: the thread's before it in the wave
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            A[e] = __shfl_up(A[e], LN);
+            B[e] = __shfl_up(B[e], LN);
+            if (lane < LN) A[e] = 1.0f, B[e] = 0.0f;
+        }
+        __syncthreads();  // (the other buffer's readers are past this barrier's predecessor)
+        float h[V];
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (w == wave) h[e] = carry[e];
+                const float a = maps[turn][w][l][e];
+                carry[e] = fmaf(a, carry[e], maps[turn][w][l][V + e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[e] = fmaf(A[e], h[e], B[e]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (mine + u >= count) break;
+            const int t = tokens(mine + u);
+            if (!BACK) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) h[e] = fmaf(gate(u, e), in(u, e), fmaf(-z[u][e], h[e], h[e]));
+                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), h, own);
+            } else {
+                float was[V], dx[V], df[V], di[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) was[e] = q.h[u].at(e);
+                if (t == 0) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) was[e] = 0.0f;
+                    if (c.s0) __builtin_memcpy(was, c.s0 + at, sizeof(was));
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float D = in(u, e) + h[e], x = q.x[u].at(e);
+                    float zz, a;
+                    gates(q.f[u].at(e), zz, a);
+                    if (INPUT) {
+                        float v, w;
+                        gates(q.g[u].at(e), v, w);
+                        dx[e] = w * D;
+                        df[e] = D * was[e] * (zz * a);
+                        di[e] = D * x * (w * v);
+                    } else {
+                        dx[e] = zz * D;
+                        df[e] = D * (was[e] - x) * (zz * a);
+                    }
+                    h[e] = fmaf(-z[u][e], D, D);
+                }
+                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.dx, b, ch, t)), dx, own);
+                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.df, b, ch, t)), df, own);
+                if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, t)), di, own);
+            }
+        }
+        // the state after the last token
+        if (last && mine < count && mine + U >= count) gr_store<F32, V>(reinterpret_cast<char *>(last + at), h, own);
+    }
+    const float zero[V] = {};
+    for (int t = count + run; t < c.T; t += TC) {
+        if (!BACK) {
+            gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), zero, own);
+        } else {
+            gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.dx, b, ch, t)), zero, own);
+            gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.df, b, ch, t)), zero, own);
+            if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, t)), zero, own);
+        }
+    }
+    if (last && count == 0 && run == 0) gr_store<F32, V>(reinterpret_cast<char *>(last + at), carry, own);
 }
 
 template <class DT, int V, bool INPUT>
@@ -258,34 +423,45 @@ __global__ __launch_bounds__(64) void k_gr_step(GrStep c) {
     gr_store<DT, V>(y, h);
 }
 
-// f(integral_constant V) for the widest piece that a row holds.
-template <class DT, class F>
-void with_piece(int width, F f) {
-    if (width >= DT::PER16)
-        f(std::integral_constant<int, DT::PER16>{});
-    else
-        f(std::integral_constant<int, 1>{});
+// A piece of a row is 16 bytes, or one value where the row is shorter.
+int piece(int width, int dtype) {
+    const int per = dtype == LSTM_BF16 ? 8 : 4;
+    return width >= per ? per : 1;
+}
+
+constexpr int kU = 4;  // tokens of a tile's thread
+
+template <class DT, int V, bool INPUT, bool BACK>
+void run_piece(const GrCall &c, hipStream_t s) {
+    if (c.nseg == 0) {
+        const dim3 grid((unsigned)(c.B * (long long)((c.width + LN * V - 1) / (LN * V))));
+        auto go = [&](auto tile) {
+            using TL = decltype(tile);
+            hipLaunchKernelGGL((k_gr_tile<DT, V, INPUT, BACK, TL>), grid, dim3(TL::THREADS), 0, s, c);
+        };
+        if (c.T <= 8 * kU)
+            go(GrTile<8, kU>{});
+        else if (c.T <= 32 * kU)
+            go(GrTile<32, kU>{});
+        else
+            go(GrTile<64, kU>{});
+        return;
+    }
+    const long long threads = (long long)c.B * ((c.width + V - 1) / V);
+    const dim3 grid((unsigned)((threads + 255) / 256), c.nseg);
+    if (c.nseg > 1) {
+        hipLaunchKernelGGL((k_gr_lanes<DT, V, INPUT, BACK, true>), grid, dim3(256), 0, s, c);
+        hipLaunchKernelGGL(k_gr_join<BACK>, dim3((unsigned)(((long long)c.B * c.width + 15) / 16)), dim3(256), 0, s, c);
+    }
+    hipLaunchKernelGGL((k_gr_lanes<DT, V, INPUT, BACK, false>), grid, dim3(256), 0, s, c);
 }
 
 template <class DT, bool INPUT, bool BACK>
 hipError_t run(const GrCall &c, hipStream_t s) {
-    with_piece<DT>(c.width, [&](auto v) {
-        constexpr int V = decltype(v)::value;
-        const long long threads = (long long)c.B * ((c.width + V - 1) / V);
-        const dim3 grid((unsigned)((threads + 255) / 256), c.nseg);
-        if (c.nseg > 1) {
-            if (BACK)
-                hipLaunchKernelGGL((k_gr_backward<DT, V, INPUT, false>), grid, dim3(256), 0, s, c);
-            else
-                hipLaunchKernelGGL((k_gr_forward<DT, V, INPUT, false>), grid, dim3(256), 0, s, c);
-            hipLaunchKernelGGL(k_gr_join<BACK>, dim3((unsigned)(((long long)c.B * c.width + 255) / 256)), dim3(256), 0,
-                               s, c);
-        }
-        if (BACK)
-            hipLaunchKernelGGL((k_gr_backward<DT, V, INPUT, true>), grid, dim3(256), 0, s, c);
-        else
-            hipLaunchKernelGGL((k_gr_forward<DT, V, INPUT, true>), grid, dim3(256), 0, s, c);
-    });
+    if (piece(c.width, c.dtype) > 1)
+        run_piece<DT, DT::PER16, INPUT, BACK>(c, s);
+    else
+        run_piece<DT, 1, INPUT, BACK>(c, s);
     return hipGetLastError();
 }
 
@@ -312,18 +488,33 @@ hipError_t run_step(const GrStep &c, hipStream_t s) {
 
 }  // namespace
 
-void gr_segments(int T, int B, int width, int dtype, bool backward, int *nseg, int *seg_tokens) {
-    const int V = dtype == LSTM_BF16 ? 8 : 4;
-    const long long rows = (long long)B * ((width + V - 1) / V);  // threads of one segment
-    // Two waves a SIMD, in segments of 32 tokens at least.
-    long long n = (1 << 17) / rows;
-    const long long most = (T + 31) / 32;
-    if (n > most) n = most;
-    if (n > 512) n = 512;
-    if (n < 2) n = 1;
-    const int per = (int)((T + n - 1) / n);
-    *seg_tokens = per;
-    *nseg = (T + per - 1) / per;
+// The way with the least estimated time.  nseg 0: tiles.
+void gr_plan(int T, int B, int width, int dtype, bool backward, int *nseg, int *seg_tokens) {
+    const int V = piece(width, dtype);
+    const double lanes = (double)B * ((width + V - 1) / V);
+    const double groups = (double)B * ((width + LN * V - 1) / (LN * V));
+    const double bytes = (double)T * B * width * (dtype == LSTM_BF16 ? 2 : 4) * (backward ? 6 : 3);
+    // Tiles of 256 tokens take 4 us alone and 9 where a CU has always one (6 and 15 backward).
+    const double tiles = (T + 255) / 256;
+    const double turns = groups * tiles / 256;
+    double least = 3.0 + (backward ? 6.0 : 4.0) * tiles;
+    if (turns > 1 && 3.0 + (backward ? 15.0 : 9.0) * turns > least) least = 3.0 + (backward ? 15.0 : 9.0) * turns;
+    *nseg = 0;
+    *seg_tokens = T;
+    // Lanes: 2.5 us for eight tokens that a thread waits for, 5 TB/s, and with
+    // segments two launches more and two thirds of the reads again.
+    for (int n = 1; n <= 512 && (n == 1 || T / n >= 16); n *= 2) {
+        const int per = (T + n - 1) / n;
+        double wait = (per + 7) / 8 * (backward ? 4.0 : 2.5), stream = bytes / 5e6;
+        if (lanes * n < 32768) stream *= 32768 / (lanes * n);
+        double us = 3.0 + (wait > stream ? wait : stream);
+        if (n > 1) us += 10.0 + ((per + 7) / 8 * 2.5 > stream * 0.6 ? (per + 7) / 8 * 2.5 : stream * 0.6);
+        if (us < least) {
+            least = us;
+            *seg_tokens = per;
+            *nseg = (T + per - 1) / per;
+        }
+    }
 }
 
 hipError_t launch_gr_forward(const GrCall &c, hipStream_t s) { return launch<false>(c, s); }

@@ -141,6 +141,19 @@ def test_recurrence_lengths(T):
     Rec(T, 3, 20, "bf16", 1, lengths=[0, 0, 0]).check()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,W,gates", [(11, 300, 1000, 1), (11, 290, 1003, 2), (40, 150, 515, 1)])
+def test_recurrence_many_channels(T, B, W, gates, dtype):
+    """Enough channels for the card without cutting the sequence; rows of every length."""
+    Rec(T, B, W, dtype, gates, lengths=[b % (T + 1) for b in range(B)], packed=gates == 2).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,W,gates", [(1500, 2, 9, 1), (3000, 1, 130, 2), (4097, 1, 3, 1)])
+def test_recurrence_in_segments(T, B, W, gates, dtype):
+    Rec(T, B, W, dtype, gates, lengths=[T] if B == 1 else [T - 700, T]).check()
+
+
 def test_recurrence_long_memory():
     """Gates so near 1 that 1 - a has no digits left in a itself (logits up to 20)."""
     Rec(512, 2, 64, "f32", 1, keep=20.0).check()
