@@ -9,8 +9,8 @@
 // fill the card the sequence is cut into segments: one launch takes each
 // segment's own map (carry -> A carry + B, A the product of its 1 - z), one
 // joins them, and one walks the segments from the carries that they begin with.
-// k_gr_tile, for little work: a workgroup spreads the tokens of 128 bytes of
-// channels over its threads and scans their maps: one launch, and memory is
+// k_gr_tile, for little work: a workgroup spreads the tokens of 32 channels over
+// its threads and scans their maps: one launch, and memory is
 // read once, but each tile waits for its loads.
 #include <type_traits>
 
@@ -21,7 +21,7 @@
 namespace lstm_amd {
 namespace {
 
-constexpr int LN = 8;  // lanes of a token's channels: 128 bytes
+constexpr int LN = 8;  // lanes of a token's channels in a tile: 32 channels
 
 template <class DT, int V>
 __device__ inline void gr_load(const char *p, float *v) {
@@ -248,7 +248,6 @@ struct GrTile {
 template <class DT, int V, bool INPUT, bool BACK, class TL>
 __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
     constexpr int U = TL::U, TC = TL::TC, WAVES = TL::WAVES;
-    constexpr long long ES = sizeof(typename DT::S);
     __shared__ float maps[2][WAVES][LN][2 * V];  // the waves' maps of a tile, in turn
     const int l = threadIdx.x % LN, run = threadIdx.x / LN, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const int slabs = (c.width + LN * V - 1) / (LN * V), b = blockIdx.x / slabs;
@@ -423,11 +422,9 @@ __global__ __launch_bounds__(64) void k_gr_step(GrStep c) {
     gr_store<DT, V>(y, h);
 }
 
-// A piece of a row is 16 bytes, or one value where the row is shorter.
-int piece(int width, int dtype) {
-    const int per = dtype == LSTM_BF16 ? 8 : 4;
-    return width >= per ? per : 1;
-}
+// Channels of a thread: four, or one where the row is shorter.  (Of bf16 eight,
+// 16 bytes, give half as many waves: 512 x 256 x 2048 backward 745 us against 598.)
+int piece(int width) { return width >= 4 ? 4 : 1; }
 
 constexpr int kU = 4;  // tokens of a tile's thread
 
@@ -458,8 +455,8 @@ void run_piece(const GrCall &c, hipStream_t s) {
 
 template <class DT, bool INPUT, bool BACK>
 hipError_t run(const GrCall &c, hipStream_t s) {
-    if (piece(c.width, c.dtype) > 1)
-        run_piece<DT, DT::PER16, INPUT, BACK>(c, s);
+    if (piece(c.width) == 4)
+        run_piece<DT, 4, INPUT, BACK>(c, s);
     else
         run_piece<DT, 1, INPUT, BACK>(c, s);
     return hipGetLastError();
@@ -490,7 +487,7 @@ hipError_t run_step(const GrStep &c, hipStream_t s) {
 
 // The way with the least estimated time.  nseg 0: tiles.
 void gr_plan(int T, int B, int width, int dtype, bool backward, int *nseg, int *seg_tokens) {
-    const int V = piece(width, dtype);
+    const int V = piece(width);
     const double lanes = (double)B * ((width + V - 1) / V);
     const double groups = (double)B * ((width + LN * V - 1) / (LN * V));
     const double bytes = (double)T * B * width * (dtype == LSTM_BF16 ? 2 : 4) * (backward ? 6 : 3);

@@ -13,8 +13,8 @@
 namespace lstm_amd {
 namespace {
 
-constexpr int HEADS = 8;  // of a token, one after the other
-constexpr int AHEAD = 4;  // of them on their way at a time
+constexpr int HEADS = 8;  // of a token, a lane's
+constexpr int AHEAD = 4;  // of them, loaded at a time
 
 // What lane `j` of a row holds: values lo..lo+P-1 and hi..hi+P-1, turned pair
 // by pair (half layout: lo[e] with hi[e]; neighbours: the 2P values from lo on).
@@ -39,19 +39,23 @@ struct Block {
     }
 };
 
+// The block's values of a row as they are in memory.
 template <class DT, int P>
-__device__ inline void rot_load(const char *row, const Block<P> &b, float *v) {
-    using S = typename DT::S;
-    const S *q = reinterpret_cast<const S *>(row);
-    S s[2 * P];
-    __builtin_memcpy(s, q + b.lo, sizeof(s) / 2);
-    if (!(P == 1 && b.odd))
-        __builtin_memcpy(s + P, q + b.hi, sizeof(s) / 2);
-    else
-        s[P] = (S)0;
+struct Row {
+    typename DT::S s[2 * P];
+    __device__ void load(const char *row, const Block<P> &b) {
+        const typename DT::S *q = reinterpret_cast<const typename DT::S *>(row);
+        __builtin_memcpy(s, q + b.lo, sizeof(s) / 2);
+        if (!(P == 1 && b.odd))
+            __builtin_memcpy(s + P, q + b.hi, sizeof(s) / 2);
+        else
+            s[P] = (typename DT::S)0;
+    }
+    __device__ void values(bool on, float *v) const {
 #pragma unroll
-    for (int e = 0; e < 2 * P; ++e) v[e] = DT::to_f(s[e]);
-}
+        for (int e = 0; e < 2 * P; ++e) v[e] = on ? DT::to_f(s[e]) : 0.0f;
+    }
+};
 
 template <class DT, int P>
 __device__ inline void rot_store(char *row, const Block<P> &b, const float *v) {
@@ -76,8 +80,10 @@ __device__ inline void turn(float *v, const float *co, const float *si) {
     }
 }
 
-// Angles p f_j in 64 bits, as parts of a turn.
-template <int P>
+// Angles p f_j in 64 bits, as parts of a turn.  bf16 takes the hardware's sine and
+// cosine of parts of a turn, whose error (below 2^-18) is lost in the results'
+// rounding; fp32 the library's.
+template <class DT, int P>
 __device__ inline void angles(const RotCall &c, const Block<P> &b, int p, float *co, float *si) {
 #pragma unroll
     for (int e = 0; e < P; ++e) {
@@ -86,7 +92,12 @@ __device__ inline void angles(const RotCall &c, const Block<P> &b, int p, float 
         if (b.pair >= 0) {
             const double turns = (double)p * c.freq[b.pair + e] * 0.15915494309189535;
             const float part = (float)(turns - __builtin_rint(turns));
-            sincospif(2.0f * part, &si[e], &co[e]);
+            if (sizeof(typename DT::S) == 2) {
+                si[e] = __builtin_amdgcn_sinf(part);
+                co[e] = __builtin_amdgcn_cosf(part);
+            } else {
+                sincospif(2.0f * part, &si[e], &co[e]);
+            }
             si[e] *= c.scale;
             co[e] *= c.scale;
         }
@@ -120,46 +131,52 @@ __global__ __launch_bounds__(256) void k_rot(RotCall c) {
         b[k].place(c, lane + k * L);
 #pragma unroll
         for (int e = 0; e < 2 * P; ++e) w[k][e] = 1.0f, dw[k][e] = 0.0f;
-        if (s.w && b[k].on) rot_load<DT, P>(s.w, b[k], w[k]);
+        if (s.w && b[k].on) {
+            Row<DT, P> row;
+            row.load(s.w, b[k]);
+            row.values(true, w[k]);
+        }
     }
     const int tokens = c.T * c.B;
     for (long long tok = (long long)blockIdx.x * GROUPS + group; tok < tokens; tok += (long long)gridDim.x * GROUPS) {
         const int t = (int)(tok / c.B), bt = (int)(tok % c.B);
         const int p = c.pos ? c.pos[c.pos_t * t + c.pos_b * bt] : t;
-        float co[NB][P], si[NB][P];
-#pragma unroll
-        for (int k = 0; k < NB; ++k) angles<P>(c, b[k], p, co[k], si[k]);
         const char *x = s.x.p + (s.x.t * t + s.x.b * bt) * ES;
         const char *yi = s.y.p + (s.y.t * t + s.y.b * bt) * ES;
         char *out = BACK ? s.dx.p + (s.dx.t * t + s.dx.b * bt) * ES : const_cast<char *>(yi);
         const long long oh = (BACK ? s.dx.h : s.y.h) * ES;
-        for (int h = h0; h < h1; h += AHEAD) {
-            float v[AHEAD][NB][2 * P], g[BACK ? AHEAD : 1][NB][2 * P];
+        Row<DT, P> rx[AHEAD][NB], ry[BACK ? AHEAD : 1][NB];
+        auto fetch = [&](int h) {
 #pragma unroll
             for (int a = 0; a < AHEAD; ++a) {
                 const long long q = min(h + a, h1 - 1);  // past the last head: it again
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
-#pragma unroll
-                    for (int e = 0; e < 2 * P; ++e) {
-                        v[a][k][e] = 0.0f;
-                        if (BACK) g[a][k][e] = 0.0f;
-                    }
                     if (!b[k].on) continue;
-                    if (!BACK || c.norm) rot_load<DT, P>(x + q * s.x.h * ES, b[k], v[a][k]);
-                    if (BACK) rot_load<DT, P>(yi + q * s.y.h * ES, b[k], g[a][k]);
+                    if (!BACK || c.norm) rx[a][k].load(x + q * s.x.h * ES, b[k]);
+                    if (BACK) ry[BACK ? a : 0][k].load(yi + q * s.y.h * ES, b[k]);
                 }
             }
+        };
+        fetch(h0);
+        float co[NB][P], si[NB][P];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) angles<DT, P>(c, b[k], p, co[k], si[k]);
+#pragma unroll 1
+        for (int h = h0; h < h1; h += AHEAD) {
 #pragma unroll
             for (int a = 0; a < AHEAD; ++a) {
                 if (h + a >= h1) break;
-                float r = 1.0f;
+                __builtin_amdgcn_sched_barrier(0);  // one head after the other, or all are widened at once
+                float v[NB][2 * P], r = 1.0f;
+#pragma unroll
+                for (int k = 0; k < NB; ++k) rx[a][k].values(b[k].on && (!BACK || c.norm), v[k]);
                 if (c.norm) {
                     float ss = 0.0f;
 #pragma unroll
                     for (int k = 0; k < NB; ++k)
 #pragma unroll
-                        for (int e = 0; e < 2 * P; ++e) ss += v[a][k][e] * v[a][k][e];
+                        for (int e = 0; e < 2 * P; ++e) ss += v[k][e] * v[k][e];
                     r = 1.0f / sqrtf(lanes_sum<L>(ss) * inv + c.eps);
                 }
                 if (!BACK) {
@@ -167,22 +184,23 @@ __global__ __launch_bounds__(256) void k_rot(RotCall c) {
                     for (int k = 0; k < NB; ++k) {
                         if (c.norm)
 #pragma unroll
-                            for (int e = 0; e < 2 * P; ++e) v[a][k][e] *= r * w[k][e];
-                        if (b[k].pair >= 0) turn<P, PAIRS, false>(v[a][k], co[k], si[k]);
-                        if (b[k].on) rot_store<DT, P>(out + (h + a) * oh, b[k], v[a][k]);
+                            for (int e = 0; e < 2 * P; ++e) v[k][e] *= r * w[k][e];
+                        if (b[k].pair >= 0) turn<P, PAIRS, false>(v[k], co[k], si[k]);
+                        if (b[k].on) rot_store<DT, P>(out + (h + a) * oh, b[k], v[k]);
                     }
                 } else {
-                    float dot = 0.0f;
+                    float g[NB][2 * P], dot = 0.0f;
 #pragma unroll
                     for (int k = 0; k < NB; ++k) {
-                        if (b[k].pair >= 0) turn<P, PAIRS, true>(g[a][k], co[k], si[k]);
+                        ry[BACK ? a : 0][k].values(b[k].on, g[k]);
+                        if (b[k].pair >= 0) turn<P, PAIRS, true>(g[k], co[k], si[k]);
                         if (c.norm)
 #pragma unroll
                             for (int e = 0; e < 2 * P; ++e) {
-                                v[a][k][e] *= r;
-                                dw[k][e] += g[a][k][e] * v[a][k][e];
-                                g[a][k][e] *= w[k][e];
-                                dot += g[a][k][e] * v[a][k][e];
+                                v[k][e] *= r;
+                                dw[k][e] += g[k][e] * v[k][e];
+                                g[k][e] *= w[k][e];
+                                dot += g[k][e] * v[k][e];
                             }
                     }
                     if (c.norm) dot = lanes_sum<L>(dot) * inv;
@@ -190,11 +208,12 @@ __global__ __launch_bounds__(256) void k_rot(RotCall c) {
                     for (int k = 0; k < NB; ++k) {
                         if (c.norm)
 #pragma unroll
-                            for (int e = 0; e < 2 * P; ++e) g[a][k][e] = r * (g[a][k][e] - v[a][k][e] * dot);
-                        if (b[k].on) rot_store<DT, P>(out + (h + a) * oh, b[k], g[a][k]);
+                            for (int e = 0; e < 2 * P; ++e) g[k][e] = r * (g[k][e] - v[k][e] * dot);
+                        if (b[k].on) rot_store<DT, P>(out + (h + a) * oh, b[k], g[k]);
                     }
                 }
             }
+            if (h + AHEAD < h1) fetch(h + AHEAD);
         }
     }
     if (!BACK || !c.part) return;
@@ -204,25 +223,26 @@ __global__ __launch_bounds__(256) void k_rot(RotCall c) {
 #pragma unroll
         for (int e = 0; e < 2 * P; ++e) sums[(group * NB * 2 * P + k * 2 * P + e) * L + lane] = dw[k][e];
     __syncthreads();
-    if (group > 0) return;
     float *part = c.part + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * c.dim;
+    constexpr int COLS = L * NB * 2 * P;
+    for (int q = threadIdx.x; q < COLS; q += 256) {
+        const int j = q % L, e = q / L % (2 * P), k = q / L / (2 * P);
+        Block<P> of;
+        of.place(c, j + k * L);
+        const int i = e < P ? of.lo + e : of.hi + e - P;
+        if (!of.on || i >= c.dim) continue;
+        float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-        if (!b[k].on) continue;
-#pragma unroll
-        for (int e = 0; e < 2 * P; ++e) {
-            float sum = 0.0f;
-            for (int q = 0; q < GROUPS; ++q) sum += sums[(q * NB * 2 * P + k * 2 * P + e) * L + lane];
-            const int i = e < P ? b[k].lo + e : b[k].hi + e - P;
-            if (i < c.dim) part[i] = sum;
-        }
+        for (int y = 0; y < GROUPS; ++y) sum += sums[y * COLS + q];
+        part[i] = sum;
     }
 }
 
-// The workgroups' sums of a side in their order: 8 threads take every eighth.
+// The workgroups' sums of a side in their order: 32 threads take every 32nd of a
+// column's, then their sums are added.
 template <class DT>
-__global__ __launch_bounds__(256) void k_rot_join(RotCall c) {
-    __shared__ float lds[8][32];
+__global__ __launch_bounds__(1024) void k_rot_join(RotCall c) {
+    __shared__ float lds[32][33];
     const int which = blockIdx.y, x = threadIdx.x % 32, y = threadIdx.x / 32, i = blockIdx.x * 32 + x;
     const RotSide &s = c.side[which];
     const int cq = (c.side[0].heads + HEADS - 1) / HEADS, ck = (c.side[1].heads + HEADS - 1) / HEADS;
@@ -231,13 +251,13 @@ __global__ __launch_bounds__(256) void k_rot_join(RotCall c) {
     float sum = 0.0f;
     if (i < c.dim)
 #pragma unroll 8
-        for (int p = y; p < n; p += 8) sum += part[(size_t)p * c.dim + i];
+        for (int p = y; p < n; p += 32) sum += part[(size_t)p * c.dim + i];
     lds[y][x] = sum;
     __syncthreads();
     if (y > 0 || i >= c.dim || !s.dw) return;
     sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += lds[k][x];
+    for (int k = 0; k < 32; ++k) sum += lds[k][x];
     reinterpret_cast<typename DT::S *>(s.dw)[i] = round_to<DT>(sum);
 }
 
@@ -254,23 +274,19 @@ void run(const RotCall &c, hipStream_t s) {
     else
         hipLaunchKernelGGL((k_rot<DT, P, L, NB, false, BACK>), dim3(x, chunks), dim3(256), 0, s, d);
     if (BACK && c.part)
-        hipLaunchKernelGGL(k_rot_join<DT>, dim3((c.dim + 31) / 32, c.side[1].heads ? 2 : 1), dim3(256), 0, s, d);
+        hipLaunchKernelGGL(k_rot_join<DT>, dim3((c.dim + 31) / 32, c.side[1].heads ? 2 : 1), dim3(1024), 0, s, d);
 }
 
-// Lanes of a row: as many as it has blocks.
-template <class DT, int P, bool BACK>
+// Lanes of a row: as many as it has blocks (of 256 values at most).
+template <class DT, int P, bool BACK, int L = 8>
 void lanes(const RotCall &c, hipStream_t s) {
     const int n = (c.dim + 2 * P - 1) / (2 * P);
-    if (n <= 8)
-        run<DT, P, 8, 1, BACK>(c, s);
-    else if (n <= 16)
-        run<DT, P, 16, 1, BACK>(c, s);
-    else if (n <= 32)
-        run<DT, P, 32, 1, BACK>(c, s);
-    else if (n <= 64)
-        run<DT, P, 64, 1, BACK>(c, s);
-    else
-        run<DT, P, 64, 2, BACK>(c, s);
+    if (n <= L)
+        run<DT, P, L, 1, BACK>(c, s);
+    else if constexpr (L < 64 && L * 2 * P < 256)
+        lanes<DT, P, BACK, 2 * L>(c, s);
+    else if constexpr (L * 2 * P < 256)
+        run<DT, P, L, 2, BACK>(c, s);
 }
 
 // The widest piece that divides both halves of the turned part and of the rest.
