@@ -58,13 +58,13 @@ struct RotCall {
     const double *freq;      // [rot / 2] radians a position
     const int *pos;          // or null: the token's index
     long long pos_t, pos_b;
-    float *part;             // backward: [parts][2][dim] sums of the weight gradients, or null
-    int T, B, dim, rot, pairs, norm, dtype, parts;
+    float *part;             // backward: [runs][parts][dim] sums of the weight gradients, or null
+    int T, B, dim, rot, pairs, norm, dtype, run, parts;
     float eps, scale;
 };
-// Runs of heads that a workgroup takes of a token, and workgroups that keep sums of a run's weight gradients.
-int rot_runs(int heads);
-int rot_parts(long long tokens, int runs);
+// Heads that a workgroup takes of a token, how many runs of these a token has, and workgroups that keep sums of a run's
+// weight gradients.
+void rot_plan(long long tokens, int heads, int kv_heads, int dim, int *run, int *runs, int *parts);
 hipError_t launch_rot_forward(const RotCall &c, hipStream_t s);
 hipError_t launch_rot_backward(const RotCall &c, hipStream_t s);
 

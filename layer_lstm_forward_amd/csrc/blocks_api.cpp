@@ -67,10 +67,9 @@ RotView rot_view(const lstm_view *v) {
 lstm_status rot_size(const lstm_rotary_shape *s, size_t *bytes) {
     *bytes = 0;
     if (!s->norm) return LSTM_OK;
-    const size_t runs = rot_runs(s->heads) + rot_runs(s->kv_heads);
-    return add_bytes(bytes, runs, (size_t)rot_parts((long long)s->T * s->B, (int)runs), (size_t)s->dim, sizeof(float))
-               ? LSTM_OK
-               : LSTM_ERR_SHAPE;
+    int run, runs, parts;
+    rot_plan((long long)s->T * s->B, s->heads, s->kv_heads, s->dim, &run, &runs, &parts);
+    return add_bytes(bytes, (size_t)runs, (size_t)parts, (size_t)s->dim, sizeof(float)) ? LSTM_OK : LSTM_ERR_SHAPE;
 }
 
 RotCall rot_call(const lstm_rotary_shape *s, const void *wq, const void *wk, const double *freq,
@@ -91,6 +90,8 @@ RotCall rot_call(const lstm_rotary_shape *s, const void *wq, const void *wk, con
     c.dtype = s->dtype;
     c.eps = s->eps;
     c.scale = s->scale;
+    int runs;
+    rot_plan((long long)s->T * s->B, s->heads, s->kv_heads, s->dim, &c.run, &runs, &c.parts);
     return c;
 }
 

@@ -13,8 +13,7 @@
 namespace lstm_amd {
 namespace {
 
-constexpr int HEADS = 8;  // of a token, a lane's
-constexpr int AHEAD = 4;  // of them, loaded at a time
+constexpr int AHEAD = 4;  // heads loaded at a time
 
 // What lane `j` of a row holds: values lo..lo+P-1 and hi..hi+P-1, turned pair
 // by pair (half layout: lo[e] with hi[e]; neighbours: the 2P values from lo on).
@@ -111,17 +110,17 @@ __device__ inline float lanes_sum(float v) {
     return v;
 }
 
-// Workgroup (x, y): tokens from x on, the y-th run of HEADS heads (queries
+// Workgroup (x, y): tokens from x on, the y-th run of c.run heads (queries
 // first).  NB blocks a lane.
 template <class DT, int P, int L, int NB, bool PAIRS, bool BACK>
 __global__ __launch_bounds__(256) void k_rot(RotCall c) {
     constexpr int GROUPS = 256 / L;
     __shared__ float sums[BACK ? GROUPS * L * NB * 2 * P : 1];
     const int lane = threadIdx.x % L, group = threadIdx.x / L;
-    const int cq = (c.side[0].heads + HEADS - 1) / HEADS;
+    const int cq = (c.side[0].heads + c.run - 1) / c.run;
     const int which = (int)blockIdx.y >= cq;
     const RotSide &s = c.side[which];
-    const int h0 = (blockIdx.y - (which ? cq : 0)) * HEADS, h1 = min(h0 + HEADS, s.heads);
+    const int h0 = (blockIdx.y - (which ? cq : 0)) * c.run, h1 = min(h0 + c.run, s.heads);
     constexpr long long ES = sizeof(typename DT::S);
     const float inv = 1.0f / (float)c.dim;
     Block<P> b[NB];
@@ -245,7 +244,7 @@ __global__ __launch_bounds__(1024) void k_rot_join(RotCall c) {
     __shared__ float lds[32][33];
     const int which = blockIdx.y, x = threadIdx.x % 32, y = threadIdx.x / 32, i = blockIdx.x * 32 + x;
     const RotSide &s = c.side[which];
-    const int cq = (c.side[0].heads + HEADS - 1) / HEADS, ck = (c.side[1].heads + HEADS - 1) / HEADS;
+    const int cq = (c.side[0].heads + c.run - 1) / c.run, ck = (c.side[1].heads + c.run - 1) / c.run;
     const int n = (which ? ck : cq) * c.parts;
     const float *part = c.part + (which ? (size_t)cq * c.parts * c.dim : 0);
     float sum = 0.0f;
@@ -263,16 +262,14 @@ __global__ __launch_bounds__(1024) void k_rot_join(RotCall c) {
 
 template <class DT, int P, int L, int NB, bool BACK>
 void run(const RotCall &c, hipStream_t s) {
-    const int chunks = rot_runs(c.side[0].heads) + rot_runs(c.side[1].heads);
-    const long long n = ((long long)c.T * c.B + 256 / L - 1) / (256 / L);
-    const long long most = BACK ? rot_parts((long long)c.T * c.B, chunks) : 65536;
-    const unsigned x = (unsigned)(n < most ? n : most);
+    const int runs = (c.side[0].heads + c.run - 1) / c.run + (c.side[1].heads + c.run - 1) / c.run;
+    const long long n = ((long long)c.T * c.B + 256 / L - 1) / (256 / L), most = BACK ? c.parts : 65536;
     RotCall d = c;
-    d.parts = (int)x;
+    d.parts = (int)(n < most ? n : most);
     if (P > 1 && c.pairs)
-        hipLaunchKernelGGL((k_rot<DT, P, L, NB, true, BACK>), dim3(x, chunks), dim3(256), 0, s, d);
+        hipLaunchKernelGGL((k_rot<DT, P, L, NB, true, BACK>), dim3(d.parts, runs), dim3(256), 0, s, d);
     else
-        hipLaunchKernelGGL((k_rot<DT, P, L, NB, false, BACK>), dim3(x, chunks), dim3(256), 0, s, d);
+        hipLaunchKernelGGL((k_rot<DT, P, L, NB, false, BACK>), dim3(d.parts, runs), dim3(256), 0, s, d);
     if (BACK && c.part)
         hipLaunchKernelGGL(k_rot_join<DT>, dim3((c.dim + 31) / 32, c.side[1].heads ? 2 : 1), dim3(1024), 0, s, d);
 }
@@ -306,12 +303,18 @@ hipError_t pieces(const RotCall &c, hipStream_t s) {
 
 }  // namespace
 
-int rot_runs(int heads) { return (heads + HEADS - 1) / HEADS; }
-
-// Enough workgroups to fill the card, and few enough that joining their sums is cheap.
-int rot_parts(long long tokens, int runs) {
-    const int most = runs < 16 ? 2048 / runs : 128;
-    return tokens < most ? (int)tokens : most;
+// Heads of a run: a token's angles are computed once a run, so the more the
+// better, while there are about eight workgroups a CU (131072 tokens of 24 heads
+// of 128 bf16: 358 us forward in runs of 8, 304 in runs of 16; 16 tokens: 8.2
+// against 12.2 us).  Workgroups that keep sums of a run's weight gradients:
+// enough to fill the card, few enough that joining their sums is cheap.
+void rot_plan(long long tokens, int heads, int kv_heads, int dim, int *run, int *runs, int *parts) {
+    const long long groups = tokens * (heads + kv_heads) * dim / 4096;  // of runs of one head
+    *run = 32;
+    while (*run > 4 && groups / *run < 2048) *run /= 2;
+    *runs = (heads + *run - 1) / *run + (kv_heads + *run - 1) / *run;
+    const int most = *runs < 16 ? 2048 / *runs : 128;
+    *parts = tokens < most ? (int)tokens : most;
 }
 
 hipError_t launch_rot_forward(const RotCall &c, hipStream_t s) {
