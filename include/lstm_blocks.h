@@ -88,7 +88,8 @@ lstm_status lstm_gated_recurrence_step(const lstm_gated_recurrence_shape *shape,
 /* --------------------------------------------------------------------- rotary
  * Queries and keys of a layer, head by head: the norm of the head, then the
  * rotation of its first rotary_dim values by the token's position p.
- *     u = x weight / sqrt(mean(x^2) + eps)   (norm 0: u = x)
+ *     u = x weight / sqrt(mean(x^2) + eps)   (norm 0: u = x; the squares are
+ *                                             summed in fp32)
  *     (u_a, u_b) -> m (u_a cos(p f_j) - u_b sin(p f_j), u_b cos + u_a sin)
  * for the pairs j = 0 .. rotary_dim / 2 - 1, (a, b) = (j, j + rotary_dim / 2),
  * or (2j, 2j + 1) where interleaved.  Values past rotary_dim are not turned. */
@@ -140,9 +141,11 @@ lstm_status lstm_rotary_backward(const lstm_rotary_shape *shape, const lstm_view
  *     g = x w_gate^T    u = x w_up^T    h = act(g) u    y = h w_down^T
  * The products run on the matrix cores and are summed in fp32.  LSTM_BF16: h
  * and, in the backward call, the kept g and u and the gradients of g and u are
- * rounded to bf16 as operands, each once.  LSTM_F32: every operand is split
- * into three bf16 terms, whose six largest products are summed (2^-24 of each
- * operand); a value that is not finite spoils the outputs it reaches as NaN. */
+ * rounded as operands, each once (h and the gradients to 8 bits; g and u are
+ * kept with 16).  LSTM_F32: every operand is split into three bf16 terms, whose
+ * six largest products are summed (2^-24 of each operand; values below 2^-100
+ * keep fewer bits); a value that is not finite spoils the outputs it reaches,
+ * as NaN.  Up to 64 rows are multiplied in fp32 itself. */
 typedef enum {
     LSTM_ACT_SILU = 0,    /* g s(g) */
     LSTM_ACT_GELU = 1,    /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
@@ -152,7 +155,7 @@ typedef enum {
 typedef struct {
     int dtype;
     int activation;        /* lstm_activation */
-    int rows;              /* tokens, >= 0 */
+    int rows;              /* tokens, 0..2^30; times the widest of the others at most 2^38 */
     int in, hidden, out;   /* 1..2^18 */
 } lstm_gated_mlp_shape;
 

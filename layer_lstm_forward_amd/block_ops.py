@@ -164,12 +164,13 @@ def _channels(t, batch_first):
 
 def _recurrence_args(x, forget, input_gate, state, lead_axes, what):
     code = _code(x, "x")
-    if x.dim() != lead_axes + 1:
+    size = x.shape
+    if len(size) != lead_axes + 1:
         raise ValueError(f"x must be {what}")
-    _sequence(x, x, "x", x.shape)
-    _sequence(forget, x, "forget", x.shape)
+    _sequence(x, x, "x", size)
+    _sequence(forget, x, "forget", size)
     if input_gate is not None:
-        _sequence(input_gate, x, "input_gate", x.shape)
+        _sequence(input_gate, x, "input_gate", size)
     return code
 
 
@@ -193,7 +194,7 @@ def gated_recurrence(x, forget, input_gate=None, state=None, lengths=None, batch
     with _On(x.device, stream) as on:
         lens = _lengths(lengths, T, B, x.device)
         if out is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = x.new_empty(x.shape)
             last = torch.empty(B, width, dtype=torch.float32, device=x.device)
             if on.other is not None:
                 on.give(y, last)
@@ -232,8 +233,8 @@ def gated_recurrence_backward(x, forget, y, dy, input_gate=None, state=None, dst
     with _On(x.device, stream) as on:
         lens = _lengths(lengths, T, B, x.device)
         if out is None:
-            dx, df = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
-            di = None if input_gate is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            dx, df = x.new_empty(x.shape), x.new_empty(x.shape)
+            di = None if input_gate is None else x.new_empty(x.shape)
             if on.other is not None:
                 on.give(dx, df, di)
         else:
@@ -273,7 +274,7 @@ def gated_recurrence_step(x, forget, state, input_gate=None, slots=None, out=Non
         _dense(slots, x, "slots", (B,), torch.int32)
     with _On(x.device, stream) as on:
         if out is None:
-            out = torch.empty(B, width, dtype=x.dtype, device=x.device)
+            out = x.new_empty(x.shape)
             if on.other is not None:
                 on.give(out)
         else:
@@ -315,14 +316,15 @@ class _Rotary:
 
     def __init__(self, q, k, frequencies, positions, q_weight, k_weight, norm, eps, interleaved, scale, batch_first):
         code = _code(q, "q")
-        if q.dim() not in (3, 4):
+        size = q.shape
+        if len(size) not in (3, 4):
             raise ValueError("q must be [T, B, heads, dim] ([B, T, heads, dim] with batch_first), or [B, heads, dim]")
-        self.lead = lead = tuple(q.shape[:-2])
-        H, D = q.shape[-2:]
-        _sequence(q, q, "q", q.shape)
+        self.lead = lead = size[:-2]
+        H, D = size[-2:]
+        _sequence(q, q, "q", size)
         G = 0
         if k is not None:
-            if k.dim() != q.dim():
+            if k.dim() != len(size):
                 raise ValueError("q and k must have as many axes")
             G = k.shape[-2]
             _sequence(k, q, "k", lead + (G, D))
@@ -335,14 +337,15 @@ class _Rotary:
         if frequencies.dim() != 1:
             raise ValueError("frequencies must be one axis of float64 values")
         _dense(frequencies, q, "frequencies", frequencies.shape, torch.float64)
-        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None:
-                if not norm:
-                    raise ValueError(f"{what} needs norm=True")
-                _dense(w, q, what, (D,))
+        if q_weight is not None or k_weight is not None:
+            if not norm:
+                raise ValueError("q_weight and k_weight need norm=True")
+            for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+                if w is not None:
+                    _dense(w, q, what, (D,))
         self.positions = None
         if positions is not None:
-            if positions.dtype != torch.int32 or positions.device != q.device or tuple(positions.shape) != lead:
+            if positions.dtype != torch.int32 or positions.device != q.device or positions.shape != lead:
                 raise ValueError(f"positions must be an int32 tensor of shape {list(lead)} on {q.device}")
             s = positions.stride()
             t, b = (0, s[0]) if len(lead) == 1 else (s[1], s[0]) if batch_first else s
@@ -367,8 +370,8 @@ def rotary(q, k, frequencies, positions=None, q_weight=None, k_weight=None, norm
     a = _Rotary(q, k, frequencies, positions, q_weight, k_weight, norm, eps, interleaved, scale, batch_first)
     with _On(q.device, stream) as on:
         if out is None:
-            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            qo = q.new_empty(q.shape)
+            ko = None if k is None else k.new_empty(k.shape)
             if on.other is not None:
                 on.give(qo, ko)
         else:
@@ -397,8 +400,8 @@ def rotary_backward(q, k, frequencies, dq_out, dk_out, positions=None, q_weight=
         _sequence(dk_out, q, "dk_out", k.shape)
     with _On(q.device, stream) as on:
         if out is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            dk = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            dq = q.new_empty(q.shape)
+            dk = None if k is None else k.new_empty(k.shape)
             if on.other is not None:
                 on.give(dq, dk)
         else:
@@ -408,8 +411,8 @@ def rotary_backward(q, k, frequencies, dq_out, dk_out, positions=None, q_weight=
                 _sequence(dk, q, "dk", k.shape)
         dwq = dwk = None
         if norm:
-            dwq = torch.empty(q.shape[-1], dtype=q.dtype, device=q.device)
-            dwk = None if k is None else torch.empty_like(dwq)
+            dwq = q.new_empty(q.shape[-1])
+            dwk = None if k is None else q.new_empty(q.shape[-1])
             if on.other is not None:
                 on.give(dwq, dwk)
         nbytes = lstm_rotary_backward_workspace_size(a.shape)
@@ -463,7 +466,7 @@ def _mlp_forward(x, w_gate, w_up, w_down, activation, keep, stream):
     _code(x, "x")
     with _On(x.device, stream) as on:
         a = _Mlp(x, w_gate, w_up, w_down, activation)
-        y = torch.empty(*x.shape[:-1], a.out, dtype=x.dtype, device=x.device)
+        y = x.new_empty(x.shape[:-1] + (a.out,))
         held = lstm_gated_mlp_reserve_size(a.shape) if keep else 0
         reserve = torch.empty(held, dtype=torch.uint8, device=x.device) if keep else None
         nbytes = lstm_gated_mlp_workspace_size(a.shape)
@@ -503,8 +506,8 @@ def gated_mlp_backward(dy, x, w_gate, w_up, w_down, reserve, activation="silu", 
         held = lstm_gated_mlp_reserve_size(a.shape)
         if reserve.dtype != torch.uint8 or reserve.device != x.device or reserve.numel() != held:
             raise ValueError("reserve must be as gated_mlp_train returned it for this x")
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dws = [torch.empty(w.shape, dtype=w.dtype, device=x.device) for w in (w_gate, w_up, w_down)]
+        dx = x.new_empty(x.shape)
+        dws = [w.new_empty(w.shape) for w in (w_gate, w_up, w_down)]
         nbytes = lstm_gated_mlp_backward_workspace_size(a.shape)
         ws = on.scratch(nbytes)
         if on.other is not None:

@@ -97,13 +97,14 @@ RotCall rot_call(const lstm_rotary_shape *s, const void *wq, const void *wk, con
 
 // ---------------------------------------------------------------- gated MLP
 constexpr int kMaxFeatures = 1 << 18;
+constexpr int kMaxTokensMlp = 1 << 30;     // rows: the kernels count tiles of them in int
 constexpr long long kMaxProduct = 1ll << 38;  // elements of a matrix: 2^22 tiles of 256 x 256
 
 lstm_status mlp_check(const lstm_gated_mlp_shape *s) {
     if (!s) return LSTM_ERR_ARG;
     if (!dtype_ok(s->dtype)) return LSTM_ERR_DTYPE;
     if (s->activation < LSTM_ACT_SILU || s->activation > LSTM_ACT_SIGMOID) return LSTM_ERR_ARG;
-    if (s->rows < 0 || s->in < 1 || s->hidden < 1 || s->out < 1) return LSTM_ERR_SHAPE;
+    if (s->rows < 0 || s->rows > kMaxTokensMlp || s->in < 1 || s->hidden < 1 || s->out < 1) return LSTM_ERR_SHAPE;
     if (s->in > kMaxFeatures || s->hidden > kMaxFeatures || s->out > kMaxFeatures) return LSTM_ERR_SHAPE;
     const long long wide = s->in > s->hidden ? (s->in > s->out ? s->in : s->out) : (s->hidden > s->out ? s->hidden : s->out);
     if (s->rows * wide > kMaxProduct) return LSTM_ERR_SHAPE;

@@ -149,7 +149,8 @@ def _mlp(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=2), -3), (dict(activation=3), -1), (dict(activation=-1), -1), (dict(rows=-1), -2), (dict(width=0), -2),
     (dict(hidden=0), -2), (dict(out=0), -2), (dict(width=(1 << 18) + 1), -2), (dict(hidden=(1 << 18) + 1), -2),
-    (dict(out=(1 << 18) + 1), -2), (dict(rows=1 << 21, hidden=1 << 18), -2), (None, -1)])
+    (dict(out=(1 << 18) + 1), -2), (dict(rows=1 << 21, hidden=1 << 18), -2), (dict(rows=(1 << 30) + 1), -2),
+    (None, -1)])
 def test_mlp_shape_checks(kw, code):
     s = None if kw is None else _mlp(**kw)
     n, lib, big = ctypes.c_size_t(), ops._lib(), 1 << 50
@@ -244,6 +245,10 @@ from tests.test_ops_streams_cpu import MAIN, NOTES, SIDE, check, device, put  # 
 
 @pytest.fixture
 def kernels(monkeypatch):
+    from tests import test_ops_streams_cpu as streams
+    make = streams.torch.Tensor.new_empty
+    monkeypatch.setattr(streams.Device, "new_empty",
+                        lambda t, *a: NOTES.append(("allocation", streams.NOW[0])) or make(t, *a), raising=False)
     for name in dir(ops):
         if name.startswith("lstm_") and callable(getattr(ops, name)) and not isinstance(getattr(ops, name), type):
             size = name.endswith("_size")

@@ -377,3 +377,297 @@ def test_mlp_no_rows():
     assert dx.shape == (0, 4)
     for d, v in zip(dws, w):
         assert d.shape == v.shape and not d.any()
+
+
+# ------------------------------------------------------- streams and graphs
+def _fresh(dtype):
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    put = lambda *s: torch.randn(*s, generator=gen, device=DEV).to(dt)  # noqa: E731
+    return dict(x=put(900, 2, 40), f=put(900, 2, 40), i=put(900, 2, 40), few=put(6, 40), pool=put(6, 40).float(),
+                q=put(30, 2, 5, 24), k=put(30, 2, 3, 24), w=put(24), rows=put(300, 72), wg=put(200, 72),
+                wu=put(200, 72), wd=put(72, 200), freq=pkg.rotary_frequencies(24, device=DEV))
+
+
+def _everything(a):
+    y, last = pkg.gated_recurrence(a["x"], a["f"], a["i"])
+    out = [y, last, *pkg.gated_recurrence_backward(a["x"], a["f"], y, a["x"], a["i"])[:3]]
+    short = [a[n][:50] for n in ("x", "f")]
+    y, last = pkg.gated_recurrence(*short)
+    out += [y, last, *pkg.gated_recurrence_backward(*short, y, short[0])[:2]]
+    out += [pkg.gated_recurrence_step(a["few"], a["few"], a["pool"]), a["pool"]]
+    more = dict(norm=True, q_weight=a["w"])
+    q, k = pkg.rotary(a["q"], a["k"], a["freq"], **more)
+    out += [q, k, *pkg.rotary_backward(a["q"], a["k"], a["freq"], q, k, **more)]
+    weights = (a["wg"], a["wu"], a["wd"])
+    for n in (7, 300):
+        y, kept = pkg.gated_mlp_train(a["rows"][:n], *weights)
+        out += [y, *pkg.gated_mlp_backward(y, a["rows"][:n], *weights, kept)]
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_another_stream(dtype):
+    import torch
+    a = _fresh(dtype)
+    pool = a["pool"].clone()
+    want = [t.clone() for t in _everything(a)]
+    a["pool"].copy_(pool)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = _everything(a)
+    side.synchronize()
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_graph_replays(dtype):
+    """Two graphs, replayed in turn with eager calls between, and their inputs changed."""
+    import torch
+    a = _fresh(dtype)
+    pool, x = a["pool"].clone(), a["rows"].clone()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        _everything(a)
+    side.synchronize()
+    graphs = []
+    for _ in range(2):
+        a["pool"].copy_(pool)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = _everything(a)
+        graphs.append((g, got))
+    for turn in range(6):
+        g, got = graphs[turn % 2]
+        a["rows"].copy_(x * (1 + turn))
+        a["pool"].copy_(pool)
+        want = [t.clone() for t in _everything(a)]
+        a["pool"].copy_(pool)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for y, z in zip(want, got):
+            assert torch.equal(y, z)
+        (torch.randn(1000, device=DEV) @ torch.randn(1000, device=DEV)).item()
+
+
+# -------------------------------------------------- offsets that pass 32 bits
+FAR = 2 ** 31 + 24  # elements from one batch row to the next
+
+
+def _far(t):
+    """t [T, 2, ...] with its batch rows FAR elements apart."""
+    import torch
+    row = t[:, 0].numel()
+    flat = torch.empty(FAR + row, dtype=t.dtype, device=DEV)
+    inner = t[:, 0].contiguous().stride()
+    out = flat.as_strided(t.shape, (inner[0], FAR) + inner[1:])
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("T", [40, 1500])
+def test_recurrence_past_32_bits(T):
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(1)
+    x, f, dy = (torch.randn(T, 2, 24, generator=gen, device=DEV).to(torch.bfloat16) for _ in range(3))
+    y, last = pkg.gated_recurrence(x, f)
+    want = [y, *pkg.gated_recurrence_backward(x, f, y, dy)[:2]]
+    fx, ff, fy, fdy, fdx, fdf = (_far(t) for t in (x, f, torch.zeros_like(x), dy, torch.zeros_like(x),
+                                                   torch.zeros_like(x)))
+    _, far_last = pkg.gated_recurrence(fx, ff, out=(fy, torch.empty_like(last)))
+    pkg.gated_recurrence_backward(fx, ff, fy, fdy, out=(fdx, fdf, None))
+    for a, b in zip(want + [last], (fy, fdx, fdf, far_last)):
+        assert torch.equal(a, b)
+
+
+def test_recurrence_step_pool_past_32_bits():
+    import torch
+    n, W = 2 ** 20 + 5, 2052  # 2^31 + floats: 8.6 GB
+    pool = torch.zeros(n, W, device=DEV)
+    x = torch.randn(3, W, device=DEV)
+    slots = torch.tensor([n - 1, 0, n - 2], dtype=torch.int32, device=DEV)
+    state = torch.randn(3, W, device=DEV)
+    pool[slots.long()] = state
+    y = pkg.gated_recurrence_step(x, x, pool, slots=slots)
+    assert torch.equal(y, pkg.gated_recurrence_step(x, x, state)) and torch.equal(pool[slots.long()], state)
+    assert not pool[1:-2].any()
+
+
+def test_rotary_past_32_bits():
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(2)
+    q, d = (torch.randn(6, 2, 3, 32, generator=gen, device=DEV).to(torch.bfloat16) for _ in range(2))
+    freq = pkg.rotary_frequencies(32, device=DEV)
+    want, _ = pkg.rotary(q, None, freq, norm=True)
+    wd, _, ww, _ = pkg.rotary_backward(q, None, freq, d, None, norm=True)
+    fq, fo, fd, fdq = _far(q), _far(torch.zeros_like(q)), _far(d), _far(torch.zeros_like(q))
+    pkg.rotary(fq, None, freq, norm=True, out=(fo, None))
+    _, _, gw, _ = pkg.rotary_backward(fq, None, freq, fd, None, norm=True, out=(fdq, None))
+    assert torch.equal(want, fo) and torch.equal(wd, fdq) and torch.equal(ww, gw)
+
+
+def test_mlp_past_32_bits():
+    """Hidden values past 2^32 elements: chosen rows and hidden units against fp64."""
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    rows, K, F = 2 ** 19 + 5, 16, 8200
+    put = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device=DEV) * std).to(torch.bfloat16)  # noqa: E731
+    x, dy = put(rows, K), put(rows, K)
+    wg, wu, wd = put(F, K, std=0.25), put(F, K, std=0.25), put(K, F, std=F ** -0.5)
+    y, kept = pkg.gated_mlp_train(x, wg, wu, wd)
+    dx, dg, du, dd = pkg.gated_mlp_backward(dy, x, wg, wu, wd, kept)
+
+    def near(got, want):  # each rounding to 8 bits is off by 2^-9 rms at most; up to four of them
+        assert float((got.double() - want).norm()) < 2 ** -7 * float(want.norm())
+
+    def parts(x, dy, wg, wu, wd):
+        x, dy, wg, wu, wd = (t.double() for t in (x, dy, wg, wu, wd))
+        g, u = x @ wg.T, x @ wu.T
+        p = torch.sigmoid(g)
+        dh = dy @ wd
+        return g * p * u, dh * u * (p + g * p * (1 - p)), dh * g * p
+
+    for at in (slice(0, 3), slice(rows - 5, rows)):
+        h, a, b = parts(x[at], dy[at], wg, wu, wd)
+        near(y[at], h @ wd.double().T)
+        near(dx[at], a @ wg.double() + b @ wu.double())
+    at = slice(F - 4, F)
+    h, a, b = parts(x, dy, wg[at], wu[at], wd[:, at])
+    near(dg[at], a.T @ x.double())
+    near(du[at], b.T @ x.double())
+    near(dd[:, at], dy.double().T @ h)
+
+
+# ------------------------------------------------------------------ together
+class Block:
+    """norm -> q, k, v -> rotary -> linear attention -> norm -> gated recurrence -> norm -> gated MLP, each with its
+    residual sum, as a model has them; the same in fp64 for its differences."""
+
+    W, H, D, HIDDEN, T, B = 48, 2, 24, 72, 21, 3
+
+    def __init__(self):
+        rng = np.random.default_rng(8)
+        W, n = self.W, {}
+        for name, shape in (("g1", (W,)), ("qkv", (W, 3 * W)), ("nq", (self.D,)), ("nk", (self.D,)), ("mix", (W, W)),
+                            ("g2", (W,)), ("rec", (W, 3 * W)), ("g3", (W,)), ("wg", (self.HIDDEN, W)),
+                            ("wu", (self.HIDDEN, W)), ("wd", (W, self.HIDDEN))):
+            scale = shape[-1 if name.startswith("w") else 0] ** -0.5
+            n[name] = 1 + 0.1 * rng.standard_normal(shape) if len(shape) == 1 else scale * rng.standard_normal(shape)
+        n["x"] = rng.standard_normal((self.T, self.B, W))
+        self.p = {k: v.astype(np.float32) for k, v in n.items()}
+        self.decay = np.log(np.array([0.9, 0.99], np.float32))
+        self.start = np.array([0, 100, 7], np.int32)
+        self.dy = rng.standard_normal((self.T, self.B, W)).astype(np.float32)
+        self.freq = pkg.rotary_frequencies(self.D, device="cpu").numpy()
+
+    def exact(self, p):
+        from oracle import ops as base
+        T, B, W, H, D = self.T, self.B, self.W, self.H, self.D
+        norm = lambda z, g: base.layer_norm(z.reshape(-1, W), g)[0].reshape(T, B, W)  # noqa: E731
+        first = lambda t: t.transpose(1, 0, *range(2, t.ndim))  # noqa: E731
+        q, k, v = (norm(p["x"], p["g1"]) @ p["qkv"]).reshape(T, B, 3, H, D).transpose(2, 0, 1, 3, 4)
+        pos = np.arange(T)[:, None] + self.start
+        q = ref.rotary(q, pos, self.freq, p["nq"], norm=True)
+        k = ref.rotary(k, pos, self.freq, p["nk"], norm=True)
+        o, _ = base.linear_attention(first(q), first(k), first(v), self.decay, D ** -0.5)
+        z1 = p["x"] + first(o).reshape(T, B, W) @ p["mix"]
+        parts = np.split(norm(z1, p["g2"]) @ p["rec"], 3, -1)
+        z2 = z1 + first(ref.gated_recurrence(*(first(t) for t in parts))[0])
+        m = ref.gated_mlp(norm(z2, p["g3"]).reshape(-1, W), p["wg"], p["wu"], p["wd"], "silu")
+        return z2 + m.reshape(T, B, W)
+
+    def forward(self, p):
+        import torch
+        T, B, W, H, D, t = self.T, self.B, self.W, self.H, self.D, {}
+        t["n1"], t["m1"], t["r1"], _ = pkg.layer_norm(p["x"], p["g1"])
+        wide = (t["n1"].view(-1, W) @ p["qkv"]).view(T, B, 3, H, D)
+        t["q0"], t["k0"], t["v"] = wide.unbind(2)
+        t["rot"] = dict(positions=torch.arange(T, dtype=torch.int32, device=DEV)[:, None] + dev(self.start),
+                        q_weight=p["nq"], k_weight=p["nk"], norm=True)
+        t["freq"] = dev(self.freq)
+        t["q"], t["k"] = pkg.rotary(t["q0"], t["k0"], t["freq"], **t["rot"])
+        t["o"], _ = pkg.linear_attention(t["q"], t["k"], t["v"], dev(self.decay))
+        mixed = (t["o"].reshape(-1, W) @ p["mix"]).view(T, B, W)
+        t["n2"], t["m2"], t["r2"], t["z1"] = pkg.layer_norm(mixed, p["g2"], residual=p["x"])
+        t["xr"], t["f"], t["i"] = (t["n2"].view(-1, W) @ p["rec"]).view(T, B, 3 * W).split(W, -1)
+        t["rec"], _ = pkg.gated_recurrence(t["xr"], t["f"], t["i"])
+        t["n3"], t["m3"], t["r3"], t["z2"] = pkg.layer_norm(t["rec"], p["g3"], residual=t["z1"])
+        m, t["kept"] = pkg.gated_mlp_train(t["n3"], p["wg"], p["wu"], p["wd"])
+        return t["z2"] + m, t
+
+    def backward(self, p, t, dy):
+        import torch
+        T, B, W, H, D, g = self.T, self.B, self.W, self.H, self.D, {}
+        dn3, g["wg"], g["wu"], g["wd"] = pkg.gated_mlp_backward(dy, t["n3"], p["wg"], p["wu"], p["wd"], t["kept"])
+        dz2, g["g3"], _ = pkg.layer_norm_backward(dn3, t["z2"], t["m3"], t["r3"], p["g3"], dsum=dy)
+        wide = torch.empty(T, B, 3 * W, device=DEV)
+        pkg.gated_recurrence_backward(t["xr"], t["f"], t["rec"], dz2, t["i"], out=wide.split(W, -1))
+        wide = wide.view(-1, 3 * W)
+        g["rec"] = t["n2"].view(-1, W).T @ wide
+        dz1, g["g2"], _ = pkg.layer_norm_backward((wide @ p["rec"].T).view(T, B, W), t["z1"], t["m2"], t["r2"],
+                                                  p["g2"], dsum=dz2)
+        flat = dz1.view(-1, W)
+        g["mix"] = t["o"].reshape(-1, W).T @ flat
+        do = (flat @ p["mix"].T).view(T, B, H, D)
+        wide = torch.empty(T, B, 3, H, D, device=DEV)
+        dq, dk, dv = wide.unbind(2)
+        pkg.linear_attention_backward(t["q"], t["k"], t["v"], dev(self.decay), do, out=(dq, dk, dv))
+        _, _, g["nq"], g["nk"] = pkg.rotary_backward(t["q0"], t["k0"], t["freq"], dq, dk, out=(dq, dk), **t["rot"])
+        wide = wide.view(-1, 3 * W)
+        g["qkv"] = t["n1"].view(-1, W).T @ wide
+        dx, g["g1"], _ = pkg.layer_norm_backward((wide @ p["qkv"].T).view(T, B, W), p["x"], t["m1"], t["r1"], p["g1"],
+                                                 dsum=dz1)
+        g["x"] = dx
+        return g
+
+
+def test_block_forward_and_gradients():
+    b = Block()
+    p64 = {n: v.astype(np.float64) for n, v in b.p.items()}
+    p = {n: dev(v) for n, v in b.p.items()}
+    want = b.exact(p64)
+    y, t = b.forward(p)
+    # fp32 throughout: chains of sums of at most 144 values of size one, norms in between
+    assert np.max(np.abs(host(y) - want)) < 2000 * U32 * np.max(np.abs(want))
+    grads = b.backward(p, t, dev(b.dy))
+    rng = np.random.default_rng(9)
+    for name, value in p64.items():
+        u = rng.standard_normal(value.shape)
+        h = 1e-5
+        slope = ((b.exact({**p64, name: value + h * u}) - b.exact({**p64, name: value - h * u})) * b.dy).sum() / (2 * h)
+        got = float((host(grads[name]) * u).sum())
+        # differences: h^2 of a third derivative; gradients: sums of n products in fp32, each off by some hundred U32
+        size = float(np.sqrt((host(grads[name]) ** 2).sum() * (u ** 2).mean()))
+        assert abs(got - slope) < 1e-5 * abs(slope) + 4000 * U32 * size + 1e-6, (name, got, slope)
+
+
+def test_block_token_by_token():
+    """Serving: the same block on single tokens with states carried along."""
+    import torch
+    b = Block()
+    p = {n: dev(v) for n, v in b.p.items()}
+    want, _ = b.forward(p)
+    B, W, H, D = b.B, b.W, b.H, b.D
+    state, memory = torch.zeros(B, H, D, D, device=DEV), torch.zeros(B, W, device=DEV)
+    freq, decay = dev(b.freq), dev(b.decay)
+    for i in range(b.T):
+        x = p["x"][i]
+        n1 = pkg.layer_norm(x, p["g1"])[0]
+        q, k, v = (n1 @ p["qkv"]).view(B, 3, H, D).unbind(1)
+        q, k = pkg.rotary(q, k, freq, positions=dev(b.start + i), q_weight=p["nq"], k_weight=p["nk"], norm=True)
+        o = pkg.linear_attention_step(q, k, v, decay, state)
+        n2, _, _, z1 = pkg.layer_norm(o.view(B, W) @ p["mix"], p["g2"], residual=x)
+        xr, f, g = (n2 @ p["rec"]).split(W, -1)
+        r = pkg.gated_recurrence_step(xr, f, memory, input_gate=g)
+        n3, _, _, z2 = pkg.layer_norm(r, p["g3"], residual=z1)
+        y = z2 + pkg.gated_mlp(n3, p["wg"], p["wu"], p["wd"])
+        assert float((y - want[i]).abs().max()) < 2000 * U32 * float(want.abs().max())
