@@ -3,7 +3,27 @@
 //     GATE   g = x Wg^T, u = x Wu^T, h = act(g) u
 //     STORE  y = h Wd^T;  dx = dg Wg + du Wu;  dWg = dg^T x, dWu = du^T x, dWd = dy^T h
 //     DGATE  dh = dy Wd, dg = dh u act'(g), du = dh act(g)
-// One kernel body runs all of them on v_mfma_f32_32x32x16_bf16.
+// One kernel body, k_mlp, runs all of them on v_mfma_f32_32x32x16_bf16; up to 64
+// rows of a forward call go to k_mlp_few, which is bound by the weights' traffic.
+//
+// An fp32 matrix is three bf16 ones (its value rounded, the rest rounded, the
+// rest), and its product the six largest of the nine between them, one after the
+// other in the same sums: 128 TFLOP/s of fp32 products in a training step of
+// 8191 x 512 x 1408, against 76 of the library's fp32 products there and 153 on
+// large matrices; the fp32 matrix instructions end at 157.
+//
+// k_mlp is bound by the matrix cores and their power: with every load, LDS read
+// and store taken out it gives 1410 to 1495 TFLOP/s on random values (the clock
+// falls to 1.5 GHz), whole 1120 to 1190 for y, dx and the weights' gradients at
+// 16384 x 2048 x 5632 (the library 870 to 1190 for the same products).  There the
+// matrix cores are busy half of the time, and the waits for loads and barriers
+// take a fifth.  Measured on the same sizes: 128 x 128 tiles, two workgroups a
+// CU, 950 to 970; 256 x 128 in stages of 32, two workgroups a CU, 900 to 990;
+// 256 x 256 in four stages of 32, 1020 to 1080; lines fetched into the L2 a
+// stage ahead of their loads, 1030 to 1050.  GATE and DGATE lose to what they
+// read and write with all CUs at once: 800 TFLOP/s with g and u kept, 1050
+// without; 680 (each workgroup's results wait for nothing but are not hidden
+// behind another's products; starting the XCDs apart did not help).
 #include <type_traits>
 
 #include "blocks.h"
@@ -648,7 +668,8 @@ __global__ __launch_bounds__(256) void k_mlp_join(MlpCall c) {
 }
 
 // ------------------------------------------------------------------ few rows
-// Up to 16 NT rows x: the weights' traffic is all that counts.  A workgroup
+// Up to 16 NT rows x: the weights' traffic is all that counts (4 x 1024 x 2816
+// bf16: 5.1 + 7.0 us for 17 MB, against 22 in four launches of 64-row tiles).  A workgroup
 // takes 16 rows of a weight (GATE: of gate and of up), its NW waves every NW-th
 // 128 bytes of k.  Weights go from memory to registers as fragments (lane (m, g):
 // row m, 16 bytes at 16 g of each 64), several on their way at a time, and meet
@@ -821,7 +842,8 @@ using Tile1 = MlpTile<128, 128, 64, 2, 2>;
 using Tile2 = MlpTile<64, 128, 64, 3, 2>;
 
 // Of each tile: the microseconds of 64 of the contraction in each workgroup when
-// all run, and of a unit besides.
+// all run, and of a unit besides, as measured at 16384 x 2048 x 5632 (256 x 256:
+// 168 us for 88 of them) and at 256 rows (64 x 128: 26 us for 32).
 struct Tile {
     int m, n, held;
     float stage, unit;

@@ -9,9 +9,13 @@
 // fill the card the sequence is cut into segments: one launch takes each
 // segment's own map (carry -> A carry + B, A the product of its 1 - z), one
 // joins them, and one walks the segments from the carries that they begin with.
+// Bound by memory: 512 x 256 x 2048 bf16 304 us forward, 597 backward (5.3 and
+// 5.4 TB/s, as a copy).  In segments the inputs are read twice: 16384 tokens of
+// 2048 channels 23 + 6 + 35 us, where one read would take 38.
 // k_gr_tile, for little work: a workgroup spreads the tokens of 32 channels over
-// its threads and scans their maps: one launch, and memory is
-// read once, but each tile waits for its loads.
+// its threads and scans their maps: one launch, and memory is read once, but the
+// scan's steps wait for each other (333 x 5 x 1001 fp32 with an input gate:
+// 12 + 17 us, against 33 + 53 in segments; 512 x 256 x 2048 bf16 570 + 946).
 #include <type_traits>
 
 #include "blocks.h"
