@@ -54,6 +54,7 @@ lstm_status lstm_gated_recurrence_backward_workspace_size(const lstm_gated_recur
  *   y            view, written; must not overlap an input or itself
  *   state_out    like state: the state after each row's last token, or NULL.
  *                It may be the memory of `state`.
+ *   workspace    16-byte aligned
  * LSTM_ERR_ARG: NULL argument; LSTM_ERR_SHAPE: T, B or width outside their
  * limits, or B * width above 2^31 - 1; LSTM_ERR_WORKSPACE: workspace too short. */
 lstm_status lstm_gated_recurrence_forward(const lstm_gated_recurrence_shape *shape, const lstm_view *x,

@@ -15,8 +15,7 @@ import struct
 
 import layer_lstm_forward_amd as _base
 from . import ops as _ops
-from .ops import (_On, _Struct, _addr, _check, _code, _dense, _lengths, _pack_view, _sequence, _view, _width,
-                  lstm_view)
+from .ops import (_On, _Struct, _addr, _check, _code, _dense, _lengths, _pack_view, _sequence, _view, _width)
 
 _vp, _i, _sz, _ll, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float
 

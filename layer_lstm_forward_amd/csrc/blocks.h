@@ -23,12 +23,14 @@ struct GrCall {
     float *s1;             // state after the last, or null
     const float *ds1;      // gradient of s1, or null
     float *ds0;            // gradient of s0, or null
-    float *seg;            // workspace: [2][nseg][B][width], or null (one segment)
+    unsigned *ticket;            // GR_CHAIN: workspace, gr_words bytes: a counter, and 256 bytes on the words
+    unsigned long long *words;
     int T, B, width, dtype;
-    int nseg, seg_tokens;
+    int way, tiles;        // GrWay; tiles of a chain (set by its launch)
 };
-// Segments a sequence is cut into, and their tokens; 0: one, in tiles.
-void gr_plan(int T, int B, int width, int dtype, bool backward, int *nseg, int *seg_tokens);
+enum GrWay { GR_TILES = 0, GR_LANES = 1, GR_CHAIN = 2 };
+GrWay gr_plan(int T, int B, int width, int dtype, bool backward);
+size_t gr_words(int T, int B, int width);
 hipError_t launch_gr_forward(const GrCall &c, hipStream_t s);
 hipError_t launch_gr_backward(const GrCall &c, hipStream_t s);
 

@@ -14,6 +14,8 @@ using namespace lstm_amd;
 
 namespace {
 
+bool aligned(const void *p) { return (uintptr_t)p % 16 == 0; }
+
 bool dtype_ok(int d) { return d == LSTM_F32 || d == LSTM_BF16; }
 
 // ----------------------------------------------------------- gated recurrence
@@ -37,11 +39,14 @@ lstm_status gr_size(const lstm_gated_recurrence_shape *s, bool backward, GrCall 
     const lstm_status rc = gr_check(s);
     if (rc != LSTM_OK) return rc;
     if (!bytes) return LSTM_ERR_ARG;
-    gr_plan(s->T, s->B, s->width, s->dtype, backward, &c->nseg, &c->seg_tokens);
-    *bytes = 0;
-    if (c->nseg > 1 && !add_bytes(bytes, 2 * (size_t)c->nseg, (size_t)s->B, (size_t)s->width, sizeof(float)))
-        return LSTM_ERR_SHAPE;
+    c->way = gr_plan(s->T, s->B, s->width, s->dtype, backward);
+    *bytes = c->way == GR_CHAIN ? gr_words(s->T, s->B, s->width) : 0;
     return LSTM_OK;
+}
+
+void gr_workspace(GrCall *c, void *workspace) {
+    c->ticket = static_cast<unsigned *>(workspace);
+    c->words = reinterpret_cast<unsigned long long *>(static_cast<char *>(workspace) + 256);
 }
 
 // ------------------------------------------------------------------- rotary
@@ -348,8 +353,6 @@ Backward backward_of(const lstm_gated_mlp_shape *s, const void *x, long long xs,
     return f;
 }
 
-bool aligned(const void *p) { return (uintptr_t)p % 16 == 0; }
-
 }  // namespace
 
 extern "C" {
@@ -374,6 +377,7 @@ lstm_status lstm_gated_recurrence_forward(const lstm_gated_recurrence_shape *s, 
     if (rc != LSTM_OK) return rc;
     if (!view_ok(x) || !view_ok(forget) || (input && !input->data) || !view_ok(y)) return LSTM_ERR_ARG;
     if (need && (!workspace || workspace_bytes < need)) return LSTM_ERR_WORKSPACE;
+    if (need && !aligned(workspace)) return LSTM_ERR_ARG;
     int dev = 0;
     if ((rc = current_device(&dev)) != LSTM_OK) return rc;
     const void *ptrs[] = {x->data, forget->data, input ? input->data : nullptr, y->data, lengths, state, state_out,
@@ -386,7 +390,7 @@ lstm_status lstm_gated_recurrence_forward(const lstm_gated_recurrence_shape *s, 
     c.lengths = lengths;
     c.s0 = state;
     c.s1 = state_out;
-    c.seg = static_cast<float *>(workspace);
+    gr_workspace(&c, workspace);
     c.T = s->T;
     c.B = s->B;
     c.width = s->width;
@@ -408,6 +412,7 @@ lstm_status lstm_gated_recurrence_backward(const lstm_gated_recurrence_shape *s,
         !view_ok(dforget) || (dinput && !dinput->data) || (input != nullptr) != (dinput != nullptr))
         return LSTM_ERR_ARG;
     if (need && (!workspace || workspace_bytes < need)) return LSTM_ERR_WORKSPACE;
+    if (need && !aligned(workspace)) return LSTM_ERR_ARG;
     int dev = 0;
     if ((rc = current_device(&dev)) != LSTM_OK) return rc;
     const void *ptrs[] = {x->data, forget->data, input ? input->data : nullptr, y->data, dy->data, dx->data,
@@ -426,7 +431,7 @@ lstm_status lstm_gated_recurrence_backward(const lstm_gated_recurrence_shape *s,
     c.s0 = state;
     c.ds1 = dstate_out;
     c.ds0 = dstate;
-    c.seg = static_cast<float *>(workspace);
+    gr_workspace(&c, workspace);
     c.T = s->T;
     c.B = s->B;
     c.width = s->width;

@@ -3,19 +3,23 @@
 //     z = s(-f) (= 1 - a),  w = s(i) or z,  h_t = h_{t-1} - z h_{t-1} + w x_t
 //     D_t = dy_t + E_{t+1},  E_t = D_t - z D_t  (E: what reaches h_{t-1})
 //     dx = w D,  df = D (h_{t-1} - [w = z] x) z a,  di = D x w (1 - w)
-// Two ways, chosen by an estimate of their times (gr_plan):
-// k_gr_lanes: a thread walks the tokens of V neighbouring channels of a batch
-// row, the next tokens' values under way meanwhile.  Where the channels do not
-// fill the card the sequence is cut into segments: one launch takes each
-// segment's own map (carry -> A carry + B, A the product of its 1 - z), one
-// joins them, and one walks the segments from the carries that they begin with.
-// Bound by memory: 512 x 256 x 2048 bf16 304 us forward, 597 backward (5.3 and
-// 5.4 TB/s, as a copy).  In segments the inputs are read twice: 16384 tokens of
-// 2048 channels 23 + 6 + 35 us, where one read would take 38.
-// k_gr_tile, for little work: a workgroup spreads the tokens of 32 channels over
-// its threads and scans their maps: one launch, and memory is read once, but the
-// scan's steps wait for each other (333 x 5 x 1001 fp32 with an input gate:
-// 12 + 17 us, against 33 + 53 in segments; 512 x 256 x 2048 bf16 570 + 946).
+// Three ways, chosen by an estimate of their times (gr_plan):
+// k_gr_lanes: a thread walks the tokens of four neighbouring channels of a batch
+// row, the next tokens' values under way meanwhile.  Bound by memory: 512 x 256 x
+// 2048 bf16 304 us forward, 597 backward (5.3 and 5.4 TB/s, as a copy).
+// k_gr_tile, for little work: a workgroup spreads a tile of tokens of 32 channels
+// over its threads, composes their maps (carry -> A carry + B, A the product of
+// the 1 - z), scans them and walks the tokens again from the carries that this
+// gives: one launch, and memory is read once, but the steps of a tile wait for
+// each other (333 x 5 x 1001 fp32 with an input gate: 12 + 17 us; 512 x 256 x
+// 2048 bf16 570 + 946).
+// k_gr_tile in a chain, where channels are too few and tokens many: a workgroup a
+// tile, which hands its map on, finds the carry that it begins with from the
+// maps of the tiles before it, and hands on the carry that it ends with.  One
+// read of everything, and the results' bits do not depend on which tile is when
+// (16384 x 1 x 2048 bf16 64 us forward, 128 backward, the memory's time 38 and 75;
+// a launch for the maps of segments, one to join and one to walk them read it
+// twice: 70 and 113; fp32 119 and 173 against 122 and 319).
 #include <type_traits>
 
 #include "blocks.h"
@@ -24,8 +28,6 @@
 
 namespace lstm_amd {
 namespace {
-
-constexpr int LN = 8;  // lanes of a token's channels in a tile: 32 channels
 
 template <class DT, int V>
 __device__ inline void gr_load(const char *p, float *v) {
@@ -54,6 +56,21 @@ struct Raw {
     typename DT::S s[V];
     __device__ void load(const char *p) { __builtin_memcpy(s, p, sizeof(s)); }
     __device__ float at(int e) const { return DT::to_f(s[e]); }
+    __device__ void fill(float v) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[e] = round_to<DT>(v);
+    }
+    // Hides where the values come from: what is made of them before is made again
+    // behind, instead of being kept in more registers than they take.
+    __device__ void forget() {
+        if constexpr (sizeof(s) % 4 == 0) {
+            uint32_t w[sizeof(s) / 4];
+            __builtin_memcpy(w, s, sizeof(s));
+#pragma unroll
+            for (unsigned i = 0; i < sizeof(s) / 4; ++i) asm volatile("" : "+v"(w[i]));
+            __builtin_memcpy(s, w, sizeof(s));
+        }
+    }
 };
 
 template <class DT>
@@ -88,39 +105,33 @@ __device__ inline bool gr_place(const GrCall &c, int *b, int *ch, int *own) {
     return true;
 }
 
-// SUM: the segment's map, to the workspace; else the outputs.  Backward the
-// tokens count from the segment's end.
-template <class DT, int V, bool INPUT, bool BACK, bool SUM>
+// Backward the tokens count from the row's end.
+template <class DT, int V, bool INPUT, bool BACK>
 __global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
     // tokens loaded at a time, and as many under way: with more tensors fewer
-    constexpr int U = BACK && !SUM ? 4 : 8;
+    constexpr int U = BACK ? 4 : 8;
     int b, ch, own;
     if (!gr_place<V>(c, &b, &ch, &own)) return;
-    const int sg = blockIdx.y, n = gr_length(c, b), t0 = sg * c.seg_tokens, t1 = min(t0 + c.seg_tokens, c.T);
-    const int end = min(t1, n), count = end - t0;  // of the tokens that count
-    const size_t slab = (size_t)c.B * c.width, at = (size_t)b * c.width + ch;
-    float h[V], A[V];
+    const int count = gr_length(c, b);  // tokens that count
+    const size_t at = (size_t)b * c.width + ch;
+    const float *first = BACK ? c.ds1 : c.s0;
+    float h[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = 0.0f, A[e] = 1.0f;
-    if (!SUM) {
-        const float *s = c.nseg > 1 ? c.seg + sg * slab : BACK ? c.ds1 : c.s0;
-        if (s) __builtin_memcpy(h, s + at, sizeof(h));
-    }
+    for (int e = 0; e < V; ++e) h[e] = 0.0f;
+    if (first) __builtin_memcpy(h, first + at, sizeof(h));
     struct Tokens {
         Raw<DT, V> x[U], f[U], g[U], d[U], p[U];
     } q[2];
-    auto token = [&](int o) { return BACK ? end - 1 - o : t0 + o; };
+    auto token = [&](int o) { return BACK ? count - 1 - o : o; };
     auto fetch = [&](Tokens &k, int o) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int t = token(min(o + u, count - 1));  // past the end: the last token again
             k.f[u].load(gr_at<DT>(c.f, b, ch, t));
             if (BACK) k.d[u].load(gr_at<DT>(c.dy, b, ch, t));
-            if (!BACK || !SUM) {
-                k.x[u].load(gr_at<DT>(c.x, b, ch, t));
-                if (INPUT) k.g[u].load(gr_at<DT>(c.i, b, ch, t));
-            }
-            if (BACK && !SUM) k.p[u].load(gr_at<DT>(c.y, b, ch, max(t - 1, 0)));
+            k.x[u].load(gr_at<DT>(c.x, b, ch, t));
+            if (INPUT) k.g[u].load(gr_at<DT>(c.i, b, ch, t));
+            if (BACK) k.p[u].load(gr_at<DT>(c.y, b, ch, max(t - 1, 0)));
         }
     };
     auto walk = [&](Tokens &k, int o) {
@@ -129,7 +140,7 @@ __global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
             if (o + u >= count) break;
             const int t = token(o + u);
             float r[3][V], was[V];
-            if (BACK && !SUM) {
+            if (BACK) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) was[e] = k.p[u].at(e);
                 if (t == 0) {
@@ -141,7 +152,7 @@ __global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float z, a;
-                if (BACK && !SUM)
+                if (BACK)
                     gates(k.f[u].at(e), z, a);
                 else
                     z = sigmoid_f(-k.f[u].at(e));
@@ -150,26 +161,22 @@ __global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
                     h[e] = fmaf(w, k.x[u].at(e), fmaf(-z, h[e], h[e]));
                     r[0][e] = h[e];
                 } else {
-                    const float D = k.d[u].at(e) + h[e];
-                    if (!SUM) {
-                        const float x = k.x[u].at(e);
-                        if (INPUT) {
-                            float v, w;
-                            gates(k.g[u].at(e), v, w);
-                            r[0][e] = w * D;
-                            r[1][e] = D * was[e] * (z * a);
-                            r[2][e] = D * x * (w * v);
-                        } else {
-                            r[0][e] = z * D;
-                            r[1][e] = D * (was[e] - x) * (z * a);
-                        }
+                    const float D = k.d[u].at(e) + h[e], x = k.x[u].at(e);
+                    if (INPUT) {
+                        float v, w;
+                        gates(k.g[u].at(e), v, w);
+                        r[0][e] = w * D;
+                        r[1][e] = D * was[e] * (z * a);
+                        r[2][e] = D * x * (w * v);
+                    } else {
+                        r[0][e] = z * D;
+                        r[1][e] = D * (was[e] - x) * (z * a);
                     }
                     h[e] = fmaf(-z, D, D);
                 }
-                if (SUM) A[e] = fmaf(-z, A[e], A[e]);
             }
-            if (!SUM && !BACK) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), r[0], own);
-            if (!SUM && BACK) {
+            if (!BACK) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), r[0], own);
+            if (BACK) {
                 gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.dx, b, ch, t)), r[0], own);
                 gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.df, b, ch, t)), r[1], own);
                 if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, t)), r[2], own);
@@ -183,14 +190,8 @@ __global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
         if (o + 2 * U < count) fetch(q[0], o + 2 * U);
         walk(q[1], o + U);
     }
-    if (SUM) {
-        float *s = c.seg + sg * slab + at;
-        gr_store<F32, V>(reinterpret_cast<char *>(s), h, own);
-        gr_store<F32, V>(reinterpret_cast<char *>(s + c.nseg * slab), A, own);
-        return;
-    }
     const float zero[V] = {};
-    for (int t = max(end, t0); t < t1; ++t) {
+    for (int t = count; t < c.T; ++t) {
         if (!BACK) {
             gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), zero, own);
         } else {
@@ -199,63 +200,145 @@ __global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
             if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, t)), zero, own);
         }
     }
-    // the state is what the row's last token leaves (or a row of none has)
-    float *const last = BACK ? (sg == 0 ? c.ds0 : nullptr) : (n > t0 || sg == 0) && n <= t1 ? c.s1 : nullptr;
+    float *const last = BACK ? c.ds0 : c.s1;
     if (last) gr_store<F32, V>(reinterpret_cast<char *>(last + at), h, own);
 }
 
-// Each segment's B becomes the carry that it begins with: 16 threads a channel
-// compose a sixteenth of the segments' maps each, then walk them from the
-// carries that these give.
-template <bool BACK>
-__global__ __launch_bounds__(256) void k_gr_join(GrCall c) {
-    __shared__ float maps[2][16][16];
-    const size_t slab = (size_t)c.B * c.width;
-    const int x = threadIdx.x % 16, y = threadIdx.x / 16;
-    const size_t at = blockIdx.x * 16ull + x;
-    const int per = (c.nseg + 15) / 16, k0 = min(y * per, c.nseg), k1 = min(k0 + per, c.nseg);
-    auto segment = [&](int k) { return c.seg + (BACK ? c.nseg - 1 - k : k) * slab + at; };
-    float A = 1.0f, B = 0.0f;
-    if (at < slab)
-#pragma unroll 8
-        for (int k = k0; k < k1; ++k) {
-            const float *s = segment(k);
-            const float b = *s, a = s[c.nseg * slab];
-            B = fmaf(a, B, b);
-            A *= a;
-        }
-    maps[0][y][x] = A;
-    maps[1][y][x] = B;
-    __syncthreads();
-    if (at >= slab) return;
-    const float *first = BACK ? c.ds1 : c.s0;
-    float carry = first ? first[at] : 0.0f;
-    for (int i = 0; i < y; ++i) carry = fmaf(maps[0][i][x], carry, maps[1][i][x]);
-#pragma unroll 8
-    for (int k = k0; k < k1; ++k) {
-        float *s = segment(k);
-        const float b = *s, a = s[c.nseg * slab];
-        *s = carry;
-        carry = fmaf(a, carry, b);
-    }
+// A tile's threads: LN lanes of V channels x TC runs of U tokens.  CHAIN: a
+// workgroup takes one tile of a row, else all of them.
+template <int LN_, int TC_, int U_, bool CHAIN_>
+struct GrTile {
+    static constexpr int LN = LN_, TC = TC_, U = U_, THREADS = LN * TC, WAVES = THREADS / 64;
+    static constexpr bool CHAIN = CHAIN_;
+};
+// Of a chain: as many tokens a thread as its registers hold, at least kChainRun.
+constexpr int kChainLanes = 16, kChainRuns = 16, kChainRun = 8;
+template <class DT, bool INPUT, bool BACK>
+using GrChain = GrTile<kChainLanes, kChainRuns, std::is_same_v<DT, BF16> && !INPUT && !BACK ? 16 : kChainRun, true>;
+constexpr int chain_tiles(int T, int run) { return (T - 1) / (kChainRuns * run) + 1; }
+
+// What the tiles of a chain hand on, a 64-bit word a channel, written and read at
+// the coherence point and 0 when the launch begins: the tile's map, A with its
+// sign set (A is not negative) beside B, and the carry after the tile, beside a 1.
+enum { GR_MAP, GR_CARRY, GR_KINDS };
+__device__ inline unsigned long long *gr_word(const GrCall &c, int kind, int tile, size_t at) {
+    return c.words + ((size_t)kind * c.tiles + tile) * ((size_t)c.B * c.width) + at;
 }
 
-// A tile's threads: LN lanes x TC runs of U tokens.
-template <int TC_, int U_>
-struct GrTile {
-    static constexpr int TC = TC_, U = U_, THREADS = LN * TC, WAVES = THREADS / 64;
-};
+__global__ __launch_bounds__(256) void k_gr_clear(u32x4 *p, size_t n) {
+    for (size_t i = blockIdx.x * 256ull + threadIdx.x; i < n; i += gridDim.x * 256ull) p[i] = u32x4{0, 0, 0, 0};
+}
+
+// The carry that a tile begins with: that after the nearest tile before it which
+// has handed its own on, taken through the maps of the tiles between.  The runs
+// look at WINDOW tiles before theirs, again until one of them has (workgroups
+// are numbered as they start, so those before this one run or are done, and the
+// first waits for nobody).  Every tile's carry is its own map of the carry
+// before it, so it does not matter which one is found: the bits are the same.
+// The first wave takes the maps in turn, hands on the carry after this tile (its
+// map is P, Q), and tells the others.
+template <int V, class TL>
+__device__ inline void gr_carry_in(const GrCall &c, int tile, int l, int run, size_t at, int own, bool more,
+                                   const float *P, const float *Q, float *carry) {
+    constexpr int TC = TL::TC, LN = TL::LN, K = 1, WINDOW = K * TC;
+    __shared__ float seen[WINDOW][LN][2][V];  // the map, or the carry in the place of B
+    __shared__ int state[WINDOW][LN];         // 0: nothing yet, 1: the map, 2: the carry
+    __shared__ float begin[LN][V];
+    int st[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) st[k] = 0;
+    int found = -1;
+    while (tile > 0) {
+        unsigned long long m[K][V], w[K][V];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = max(tile - 1 - run - k * TC, 0);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                w[k][e] = xload(gr_word(c, GR_CARRY, j, at) + e);
+                m[k][e] = st[k] == 0 ? xload(gr_word(c, GR_MAP, j, at) + e) : 0;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int back = run + k * TC;
+            bool map = back < tile && st[k] == 0, all = back < tile;
+#pragma unroll
+            for (int e = 0; e < V; ++e) map = map && xtag(m[k][e]) != 0, all = all && xtag(w[k][e]) != 0;
+            if (map && !all) {
+                st[k] = 1;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    seen[back][l][0][e] = fabsf(__uint_as_float(xtag(m[k][e])));
+                    seen[back][l][1][e] = __uint_as_float((uint32_t)m[k][e]);
+                }
+            }
+            if (all) {
+                st[k] = 2;
+#pragma unroll
+                for (int e = 0; e < V; ++e) seen[back][l][1][e] = __uint_as_float((uint32_t)w[k][e]);
+            }
+            state[back][l] = st[k];
+        }
+        __syncthreads();
+        unsigned maps = 0, carries = 0;
+#pragma unroll
+        for (int back = 0; back < WINDOW; ++back) {
+            const int s = state[back][l];
+            maps |= (s == 1 ? 1u : 0u) << back;
+            carries |= (s == 2 ? 1u : 0u) << back;
+        }
+        found = __ffs((int)carries) - 1;
+        const unsigned nearer = carries ? (carries & -carries) - 1 : 0;
+        if (__syncthreads_and(carries && (maps & nearer) == nearer)) break;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    if (threadIdx.x < 64) {
+        if (tile > 0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) carry[e] = seen[found][l][1][e];
+#pragma unroll
+            for (int back = WINDOW - 1; back >= 0; --back)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float next = fmaf(seen[back][l][0][e], carry[e], seen[back][l][1][e]);
+                    carry[e] = back < found ? next : carry[e];
+                }
+        }
+        if (run == 0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (more && e >= own)
+                    xstore(gr_word(c, GR_CARRY, tile, at) + e, xword(1, __float_as_uint(fmaf(P[e], carry[e], Q[e]))));
+                begin[l][e] = carry[e];
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < V; ++e) carry[e] = begin[l][e];
+}
 
 // Each thread composes the maps of its U tokens, the workgroup scans the
 // threads' maps, and each thread walks its tokens again from the carry that it
 // begins with.  Backward the tokens count from the row's end.
 template <class DT, int V, bool INPUT, bool BACK, class TL>
 __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
-    constexpr int U = TL::U, TC = TL::TC, WAVES = TL::WAVES;
+    constexpr int U = TL::U, TC = TL::TC, LN = TL::LN, WAVES = TL::WAVES, TILE = TC * U;
+    constexpr bool CHAIN = TL::CHAIN;
     __shared__ float maps[2][WAVES][LN][2 * V];  // the waves' maps of a tile, in turn
     const int l = threadIdx.x % LN, run = threadIdx.x / LN, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    const int slabs = (c.width + LN * V - 1) / (LN * V), b = blockIdx.x / slabs;
-    const int from = (blockIdx.x % slabs * LN + l) * V, ch = min(from, c.width - V), own = from - ch;
+    const int slabs = (c.width + LN * V - 1) / (LN * V);
+    int group = blockIdx.x, tile = 0;
+    if constexpr (CHAIN) {  // numbered as they start: all tiles before this one have started
+        __shared__ unsigned number;
+        if (threadIdx.x == 0) number = atomicAdd(c.ticket, 1u);
+        __syncthreads();
+        tile = (int)(number / (unsigned)(c.B * slabs));
+        group = (int)(number % (unsigned)(c.B * slabs));
+    }
+    const int b = group / slabs;
+    const int from = (group % slabs * LN + l) * V, ch = min(from, c.width - V), own = from - ch;
     const int count = gr_length(c, b);  // tokens that count
     const size_t at = (size_t)b * c.width + ch;
     const float *first = BACK ? c.ds1 : c.s0;
@@ -264,48 +347,72 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
 #pragma unroll
     for (int e = 0; e < V; ++e) carry[e] = 0.0f;
     if (first) __builtin_memcpy(carry, first + at, sizeof(carry));
-    auto tokens = [&](int o) { return BACK ? count - 1 - o : o; };
     struct Tokens {
         Raw<DT, V> x[U], f[U], g[U], d[U], h[U];
     };
-    auto fetch = [&](Tokens &q, int o0) {
+    // Token o + u of a walk is u steps from token o: pieces of whole rows and tiles
+    // (plain) take their addresses from that alone.
+    auto at_token = [&](const GrView &v, int o) { return gr_at<DT>(v, b, ch, BACK ? count - 1 - o : o); };
+    auto step = [&](const GrView &v) { return (BACK ? -v.t : v.t) * (long long)sizeof(typename DT::S); };
+    auto fetch = [&](auto plain, Tokens &q, int o) {
+        auto get = [&](const GrView &v, Raw<DT, V> *to) {
+            const char *p = at_token(v, decltype(plain)::value ? o : 0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = tokens(min(o0 + u, count - 1));  // past the end: the last token again
-            q.f[u].load(gr_at<DT>(c.f, b, ch, t));
-            if (BACK) q.d[u].load(gr_at<DT>(c.dy, b, ch, t));
-            q.x[u].load(gr_at<DT>(c.x, b, ch, t));
-            if (INPUT) q.g[u].load(gr_at<DT>(c.i, b, ch, t));
-            if (BACK) q.h[u].load(gr_at<DT>(c.y, b, ch, max(t - 1, 0)));
+            for (int u = 0; u < U; ++u)  // past the end: the last token again
+                to[u].load(p + (decltype(plain)::value ? u : min(o + u, count - 1)) * step(v));
+        };
+        get(c.f, q.f);
+        if (BACK) get(c.dy, q.d);
+        get(c.x, q.x);
+        if (INPUT) get(c.i, q.g);
+        if (BACK) {
+            const char *p = at_token(c.y, o);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (decltype(plain)::value && u + 1 < U)
+                    q.h[u].load(p + (u + 1) * step(c.y));
+                else  // the first token has none before it
+                    q.h[u].load(gr_at<DT>(c.y, b, ch, max(count - 2 - min(o + u, count - 1), 0)));
         }
     };
     int turn = 0;
-    for (int o0 = 0; o0 < count; o0 += TC * U, turn ^= 1) {
+    for (int o0 = tile * TILE; o0 < count; o0 += TILE, turn ^= 1) {
         const int mine = o0 + run * U;
+        const bool plain = o0 + TILE <= count && c.width % V == 0;
         Tokens q;
-        fetch(q, mine);
-        // the thread's own map
-        float A[V], B[V], z[U][V], w[INPUT && !BACK ? U : 1][V];
-        auto in = [&](int u, int e) {  // x or dy, 0 past the end
-            return mine + u < count ? BACK ? q.d[u].at(e) : q.x[u].at(e) : 0.0f;
-        };
-        auto gate = [&](int u, int e) { return INPUT ? w[INPUT && !BACK ? u : 0][e] : z[u][e]; };
+        if (plain) {
+            fetch(std::true_type{}, q, mine);
+        } else {
+            fetch(std::false_type{}, q, mine);
+            // a token past the end changes nothing: z = 0 and x or dy = 0
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (mine + u >= count) {
+                    q.f[u].fill(__builtin_huge_valf());
+                    q.x[u].fill(0.0f);
+                    if (INPUT) q.g[u].fill(0.0f);
+                    if (BACK) q.d[u].fill(0.0f);
+                }
+        }
+        // the thread's own map; forward also those up to each of its tokens
+        float A[V], B[V], to[BACK ? 1 : U][2][V];
 #pragma unroll
         for (int e = 0; e < V; ++e) A[e] = 1.0f, B[e] = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool on = mine + u < count;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                z[u][e] = on ? sigmoid_f(-q.f[u].at(e)) : 0.0f;
+                const float z = sigmoid_f(-q.f[u].at(e));
+                A[e] = fmaf(-z, A[e], A[e]);
                 if (BACK) {
-                    const float D = in(u, e) + B[e];
-                    B[e] = fmaf(-z[u][e], D, D);
+                    const float D = q.d[u].at(e) + B[e];
+                    B[e] = fmaf(-z, D, D);
                 } else {
-                    if (INPUT) w[INPUT && !BACK ? u : 0][e] = on ? sigmoid_f(q.g[u].at(e)) : 0.0f;
-                    B[e] = fmaf(gate(u, e), in(u, e), fmaf(-z[u][e], B[e], B[e]));
+                    const float w = INPUT ? sigmoid_f(q.g[u].at(e)) : z;
+                    B[e] = fmaf(w, q.x[u].at(e), fmaf(-z, B[e], B[e]));
+                    to[BACK ? 0 : u][0][e] = A[e];
+                    to[BACK ? 0 : u][1][e] = B[e];
                 }
-                A[e] = fmaf(-z[u][e], A[e], A[e]);
             }
         }
         // Scan: the threads of a wave with the same channels (LN lanes apart),
@@ -332,6 +439,27 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
         }
         __syncthreads();  // (the other buffer's readers are past this barrier's predecessor)
         float h[V];
+        if constexpr (CHAIN) {
+            const bool more = o0 + TILE < count;
+            float P[V], Q[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) P[e] = 1.0f, Q[e] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float a = maps[turn][w][l][e];
+                    Q[e] = fmaf(a, Q[e], maps[turn][w][l][V + e]);
+                    P[e] *= a;
+                }
+            if (more && tile > 0 && run == 0)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (e >= own)
+                        xstore(gr_word(c, GR_MAP, tile, at) + e,
+                               xword(__float_as_uint(P[e]) | 0x80000000u, __float_as_uint(Q[e])));
+            gr_carry_in<V, TL>(c, tile, l, run, at, own, more, P, Q, carry);
+        }
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
 #pragma unroll
@@ -343,50 +471,65 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) h[e] = fmaf(A[e], h[e], B[e]);
+        auto walk = [&](auto plain) {
+            constexpr bool PLAIN = decltype(plain)::value;
+            char *const p[3] = {const_cast<char *>(at_token(BACK ? c.dx : c.y, mine)),
+                                const_cast<char *>(BACK ? at_token(c.df, mine) : nullptr),
+                                const_cast<char *>(BACK && INPUT ? at_token(c.di, mine) : nullptr)};
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (mine + u >= count) break;
-            const int t = tokens(mine + u);
-            if (!BACK) {
+            for (int u = 0; u < U; ++u) {
+                if (!PLAIN && mine + u >= count) break;
+                const int part = PLAIN ? 0 : own;
+                if (!BACK) {
+                    float y[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) h[e] = fmaf(gate(u, e), in(u, e), fmaf(-z[u][e], h[e], h[e]));
-                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), h, own);
-            } else {
-                float was[V], dx[V], df[V], di[V];
+                    for (int e = 0; e < V; ++e) y[e] = fmaf(to[BACK ? 0 : u][0][e], h[e], to[BACK ? 0 : u][1][e]);
+                    gr_store<DT, V>(p[0] + u * step(c.y), y, part);
+                    if (last && (!PLAIN || u == U - 1) && mine + u == count - 1) gr_store<F32, V>(reinterpret_cast<char *>(last + at), y, part);
+                } else {
+                    q.f[u].forget();
+                    q.d[u].forget();
+                    float was[V], dx[V], df[V], di[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) was[e] = q.h[u].at(e);
-                if (t == 0) {
+                    for (int e = 0; e < V; ++e) was[e] = q.h[u].at(e);
+                    if ((!PLAIN || u == U - 1) && mine + u == count - 1) {  // the row's first token
 #pragma unroll
-                    for (int e = 0; e < V; ++e) was[e] = 0.0f;
-                    if (c.s0) __builtin_memcpy(was, c.s0 + at, sizeof(was));
-                }
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float D = in(u, e) + h[e], x = q.x[u].at(e);
-                    float zz, a;
-                    gates(q.f[u].at(e), zz, a);
-                    if (INPUT) {
-                        float v, w;
-                        gates(q.g[u].at(e), v, w);
-                        dx[e] = w * D;
-                        df[e] = D * was[e] * (zz * a);
-                        di[e] = D * x * (w * v);
-                    } else {
-                        dx[e] = zz * D;
-                        df[e] = D * (was[e] - x) * (zz * a);
+                        for (int e = 0; e < V; ++e) was[e] = 0.0f;
+                        if (c.s0) __builtin_memcpy(was, c.s0 + at, sizeof(was));
                     }
-                    h[e] = fmaf(-z[u][e], D, D);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float D = q.d[u].at(e) + h[e], x = q.x[u].at(e);
+                        float z, a;
+                        gates(q.f[u].at(e), z, a);
+                        if (INPUT) {
+                            float v, w;
+                            gates(q.g[u].at(e), v, w);
+                            dx[e] = w * D;
+                            df[e] = D * was[e] * (z * a);
+                            di[e] = D * x * (w * v);
+                        } else {
+                            dx[e] = z * D;
+                            df[e] = D * (was[e] - x) * (z * a);
+                        }
+                        h[e] = fmaf(-z, D, D);
+                    }
+                    gr_store<DT, V>(p[0] + u * step(c.dx), dx, part);
+                    gr_store<DT, V>(p[1] + u * step(c.df), df, part);
+                    if (INPUT) gr_store<DT, V>(p[2] + u * step(c.di), di, part);
+                    if (last && (!PLAIN || u == U - 1) && mine + u == count - 1) gr_store<F32, V>(reinterpret_cast<char *>(last + at), h, part);
                 }
-                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.dx, b, ch, t)), dx, own);
-                gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.df, b, ch, t)), df, own);
-                if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, t)), di, own);
             }
-        }
-        // the state after the last token
-        if (last && mine < count && mine + U >= count) gr_store<F32, V>(reinterpret_cast<char *>(last + at), h, own);
+        };
+        if (plain)
+            walk(std::true_type{});
+        else
+            walk(std::false_type{});
+        if (CHAIN) break;
     }
     const float zero[V] = {};
-    for (int t = count + run; t < c.T; t += TC) {
+    const int stop = CHAIN ? min(c.T, (tile + 1) * TILE) : c.T;
+    for (int t = max(count, tile * TILE) + run; t < stop; t += TC) {
         if (!BACK) {
             gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), zero, own);
         } else {
@@ -395,7 +538,7 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
             if (INPUT) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.di, b, ch, t)), zero, own);
         }
     }
-    if (last && count == 0 && run == 0) gr_store<F32, V>(reinterpret_cast<char *>(last + at), carry, own);
+    if (last && count == 0 && run == 0 && tile == 0) gr_store<F32, V>(reinterpret_cast<char *>(last + at), carry, own);
 }
 
 template <class DT, int V, bool INPUT>
@@ -430,31 +573,34 @@ __global__ __launch_bounds__(64) void k_gr_step(GrStep c) {
 // 16 bytes, give half as many waves: 512 x 256 x 2048 backward 745 us against 598.)
 int piece(int width) { return width >= 4 ? 4 : 1; }
 
-constexpr int kU = 4;  // tokens of a tile's thread
+long long groups_of(int B, int width, int lanes, int V) { return B * (long long)((width + lanes * V - 1) / (lanes * V)); }
 
 template <class DT, int V, bool INPUT, bool BACK>
-void run_piece(const GrCall &c, hipStream_t s) {
-    if (c.nseg == 0) {
-        const dim3 grid((unsigned)(c.B * (long long)((c.width + LN * V - 1) / (LN * V))));
-        auto go = [&](auto tile) {
-            using TL = decltype(tile);
-            hipLaunchKernelGGL((k_gr_tile<DT, V, INPUT, BACK, TL>), grid, dim3(TL::THREADS), 0, s, c);
-        };
-        if (c.T <= 8 * kU)
-            go(GrTile<8, kU>{});
-        else if (c.T <= 32 * kU)
-            go(GrTile<32, kU>{});
+void run_piece(GrCall c, hipStream_t s) {
+    auto tiles = [&](auto tile) {
+        using TL = decltype(tile);
+        c.tiles = TL::CHAIN ? chain_tiles(c.T, TL::U) : 1;
+        const unsigned n = (unsigned)(groups_of(c.B, c.width, TL::LN, V) * c.tiles);
+        if (TL::CHAIN) {
+            const size_t pieces = 16 + (size_t)GR_KINDS * c.tiles * c.B * c.width / 2;  // of 16 bytes: counter, words
+            hipLaunchKernelGGL(k_gr_clear, dim3((unsigned)(pieces < 256 * 1024 ? (pieces + 255) / 256 : 1024)), dim3(256),
+                               0, s, reinterpret_cast<u32x4 *>(c.ticket), pieces);
+        }
+        hipLaunchKernelGGL((k_gr_tile<DT, V, INPUT, BACK, TL>), dim3(n), dim3(TL::THREADS), 0, s, c);
+    };
+    if (c.way == GR_CHAIN) {
+        tiles(GrChain<DT, INPUT, BACK>{});
+    } else if (c.way == GR_TILES) {
+        if (c.T <= 32)
+            tiles(GrTile<8, 8, 4, false>{});
+        else if (c.T <= 128)
+            tiles(GrTile<8, 32, 4, false>{});
         else
-            go(GrTile<64, kU>{});
-        return;
+            tiles(GrTile<8, 64, 4, false>{});
+    } else {
+        const long long threads = (long long)c.B * ((c.width + V - 1) / V);
+        hipLaunchKernelGGL((k_gr_lanes<DT, V, INPUT, BACK>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, c);
     }
-    const long long threads = (long long)c.B * ((c.width + V - 1) / V);
-    const dim3 grid((unsigned)((threads + 255) / 256), c.nseg);
-    if (c.nseg > 1) {
-        hipLaunchKernelGGL((k_gr_lanes<DT, V, INPUT, BACK, true>), grid, dim3(256), 0, s, c);
-        hipLaunchKernelGGL(k_gr_join<BACK>, dim3((unsigned)(((long long)c.B * c.width + 15) / 16)), dim3(256), 0, s, c);
-    }
-    hipLaunchKernelGGL((k_gr_lanes<DT, V, INPUT, BACK, false>), grid, dim3(256), 0, s, c);
 }
 
 template <class DT, bool INPUT, bool BACK>
@@ -489,33 +635,34 @@ hipError_t run_step(const GrStep &c, hipStream_t s) {
 
 }  // namespace
 
-// The way with the least estimated time.  nseg 0: tiles.
-void gr_plan(int T, int B, int width, int dtype, bool backward, int *nseg, int *seg_tokens) {
+// Bytes of a chain's workspace: the counter that numbers its workgroups, and its words.
+size_t gr_words(int T, int B, int width) {
+    return 256 + ((size_t)GR_KINDS * chain_tiles(T, kChainRun) * B * width * 8 + 255) / 256 * 256;
+}
+
+// The way with the least estimated time.
+GrWay gr_plan(int T, int B, int width, int dtype, bool backward) {
     const int V = piece(width);
     const double lanes = (double)B * ((width + V - 1) / V);
-    const double groups = (double)B * ((width + LN * V - 1) / (LN * V));
-    const double bytes = (double)T * B * width * (dtype == LSTM_BF16 ? 2 : 4) * (backward ? 6 : 3);
+    const double stream = (double)T * B * width * (dtype == LSTM_BF16 ? 2 : 4) * (backward ? 6 : 3) / 5e6;  // at 5 TB/s
     // Tiles of 256 tokens take 4 us alone and 9 where a CU has always one (6 and 15 backward).
-    const double tiles = (T + 255) / 256;
-    const double turns = groups * tiles / 256;
-    double least = 3.0 + (backward ? 6.0 : 4.0) * tiles;
-    if (turns > 1 && 3.0 + (backward ? 15.0 : 9.0) * turns > least) least = 3.0 + (backward ? 15.0 : 9.0) * turns;
-    *nseg = 0;
-    *seg_tokens = T;
-    // Lanes: 2.5 us for eight tokens that a thread waits for, 5 TB/s, and with
-    // segments two launches more and two thirds of the reads again.
-    for (int n = 1; n <= 512 && (n == 1 || T / n >= 16); n *= 2) {
-        const int per = (T + n - 1) / n;
-        double wait = (per + 7) / 8 * (backward ? 4.0 : 2.5), stream = bytes / 5e6;
-        if (lanes * n < 32768) stream *= 32768 / (lanes * n);
-        double us = 3.0 + (wait > stream ? wait : stream);
-        if (n > 1) us += 10.0 + ((per + 7) / 8 * 2.5 > stream * 0.6 ? (per + 7) / 8 * 2.5 : stream * 0.6);
-        if (us < least) {
-            least = us;
-            *seg_tokens = per;
-            *nseg = (T + per - 1) / per;
-        }
+    const double n = (T + 255) / 256, turns = groups_of(B, width, 8, V) * n / 256;
+    const double alone = (backward ? 6.0 : 4.0) * n, busy = turns > 1 ? (backward ? 15.0 : 9.0) * turns : 0.0;
+    double least = 3.0 + (alone > busy ? alone : busy);
+    GrWay way = GR_TILES;
+    // Lanes: 2.5 us for eight tokens that a thread waits for (4 backward), all of the memory's rate from 32768 on.
+    const double wait = (T + 7) / 8 * (backward ? 4.0 : 2.5), rate = lanes < 32768 ? stream * 32768 / lanes : stream;
+    const double walk = 3.0 + (wait > rate ? wait : rate);
+    if (walk < least) {
+        least = walk;
+        way = GR_LANES;
     }
+    // A chain: two launches, and the memory's time by 1.35, or 0.2 us for the carry's way past a tile; its grid holds
+    // 2^24 workgroups.
+    const int parts = chain_tiles(T, kChainRun);
+    const double chain = 14.0 + (1.35 * stream > 0.2 * parts ? 1.35 * stream : 0.2 * parts);
+    if (parts > 1 && groups_of(B, width, kChainLanes, V) * parts < (1 << 24) && chain < least) way = GR_CHAIN;
+    return way;
 }
 
 hipError_t launch_gr_forward(const GrCall &c, hipStream_t s) { return launch<false>(c, s); }

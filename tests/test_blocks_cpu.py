@@ -89,6 +89,17 @@ def test_recurrence_argument_checks():
     assert fwd(s, [_v(), _v(), _v(), _v()]) == -4  # good arguments, but no device memory
 
 
+@needs_lib
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_recurrence_workspace_alignment(dtype):
+    """Where the workspace holds words that travel whole, it is taken at its alignment or refused."""
+    s = _rec(T=4096, B=1, dtype=dtype)
+    for off, code in ((8, -1), (4, -1), (1, -1), (16, -4)):  # the last: good arguments, but no device memory
+        assert ops.lstm_gated_recurrence_forward(s, _v(), _v(), None, 0, 0, _v(), 0, FAKE + off, 1 << 50, 0) == code
+        assert ops.lstm_gated_recurrence_backward(s, _v(), _v(), None, 0, 0, _v(), _v(), 0, _v(), _v(), None, 0,
+                                                  FAKE + off, 1 << 50, 0) == code
+
+
 def _rot(**kw):
     return ops.lstm_rotary_shape(**{**dict(dtype=0, T=5, B=2, heads=4, kv_heads=2, dim=16, rotary_dim=8, interleaved=0,
                                            norm=1, eps=1e-6, scale=1.0), **kw})

@@ -149,9 +149,57 @@ def test_recurrence_many_channels(T, B, W, gates, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,W,gates", [(1500, 2, 9, 1), (3000, 1, 130, 2), (4097, 1, 3, 1), (1025, 5, 67, 2)])
+def test_recurrence_in_a_chain(T, B, W, gates, dtype):
+    """Few channels and many tokens: tiles that hand their carries on, rows that end in the first, inside and at the end
+    of one, or have none."""
+    Rec(T, B, W, dtype, gates, lengths=[T, T - 700, 0, 128, 3][:B]).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,B,W,gates", [(1500, 2, 9, 1), (3000, 1, 130, 2), (4097, 1, 3, 1)])
 def test_recurrence_in_segments(T, B, W, gates, dtype):
     Rec(T, B, W, dtype, gates, lengths=[T] if B == 1 else [T - 700, T]).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_recurrence_chain_gives_the_same_bits(dtype):
+    """Which of the tiles before it a tile finds first is a matter of time; the results are not."""
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(6)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, f, dy = (torch.randn(9000, 1, 200, generator=gen, device=DEV).to(dt) for _ in range(3))
+    f += 3
+    want = None
+    for _ in range(5):
+        y, last = pkg.gated_recurrence(x, f)
+        got = [y, last, *pkg.gated_recurrence_backward(x, f, y, dy)[:2]]
+        assert want is None or all(torch.equal(a, b) for a, b in zip(want, got))
+        want = got
+
+
+@pytest.mark.parametrize("T,B,W", [(40, 2, 24), (1500, 1, 24), (11, 300, 1000)])
+def test_recurrence_not_finite_and_saturated(T, B, W):
+    """A token that is not a number reaches its channel's later tokens alone; gates at both ends keep and take exactly."""
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(7)
+    x, f = (torch.randn(T, B, W, generator=gen, device=DEV) for _ in range(2))
+    want, _ = pkg.gated_recurrence(x, f)
+    for bad in (float("nan"), float("inf")):
+        z = x.clone()
+        z[T // 2, 0, 5] = bad
+        got, _ = pkg.gated_recurrence(z, f)
+        hit = torch.zeros_like(got, dtype=torch.bool)
+        hit[T // 2:, 0, 5] = True
+        assert torch.equal(got[~hit], want[~hit]) and not torch.isfinite(got[hit]).any()
+    S = torch.randn(B, W, generator=gen, device=DEV)
+    for logit in (200.0, float("inf")):
+        y, last = pkg.gated_recurrence(x, torch.full_like(f, logit), state=S)
+        assert torch.equal(y, S.expand_as(y)) and torch.equal(last, S)
+        y, last = pkg.gated_recurrence(x, torch.full_like(f, -logit), state=S)
+        assert torch.equal(y, x) and torch.equal(last, x[-1])
 
 
 def test_recurrence_long_memory():
@@ -365,6 +413,119 @@ def test_mlp_strided(dtype):
 def test_mlp_large_tiles(dtype):
     """Enough rows and columns for the largest tiles in every product, edges that end inside them."""
     mlp_case(4100, 264, 1800, 520, dtype)
+
+
+def _mlp_check(x, wg, wu, wd, dy, dtype, kind="silu"):
+    """mlp_case's comparison on the device, for sizes that take the host too long."""
+    import torch
+    y, kept = pkg.gated_mlp_train(x, wg, wu, wd, activation=kind)
+    got = (y, *pkg.gated_mlp_backward(dy, x, wg, wu, wd, kept, activation=kind))
+    x, wg, wu, wd, dy = (t.double() for t in (x, wg, wu, wd, dy))
+    ab = [t.abs() for t in (x, wg, wu, wd, dy)]
+    rows, K = x.shape
+    F, O = wd.shape[1], wd.shape[0]
+    rough = U16 if dtype == "bf16" else 0.0
+    chain = lambda n: (n + 40) * U32  # noqa: E731
+    g, u = x @ wg.T, x @ wu.T
+    p = torch.sigmoid(g)
+    a, slope = g * p, p + g * p * (1 - p)
+    eg, eu = chain(K) * (ab[0] @ ab[1].T), chain(K) * (ab[0] @ ab[2].T)
+    gate = (24 + 4 * g.abs()) * U32
+    h = a * u
+    eh = 1.2 * eg * u.abs() + a.abs() * eu + 2 * gate * h.abs() + rough * h.abs()
+    dh, edh = dy @ wd, chain(O) * (ab[4] @ ab[3])
+    eg, eu = eg + rough * g.abs(), eu + rough * u.abs()
+    dg, du = dh * u * slope, dh * a
+    edg = (u * slope).abs() * edh + (dh * slope).abs() * eu + (dh * u).abs() * (eg + gate) + rough * dg.abs()
+    edu = a.abs() * edh + dh.abs() * (1.2 * eg + gate * a.abs()) + rough * du.abs()
+    adg, adu = dg.abs(), du.abs()
+    want = (h @ wd.T, dg @ wg + du @ wu, dg.T @ x, du.T @ x, dy.T @ h)
+    tols = (eh @ ab[3].T + chain(F) * (h.abs() @ ab[3].T),
+            (edg + chain(2 * F) * adg) @ ab[1] + (edu + chain(2 * F) * adu) @ ab[2],
+            (edg + chain(rows) * adg).T @ ab[0], (edu + chain(rows) * adu).T @ ab[0],
+            ab[4].T @ (eh + chain(rows) * h.abs()))
+    for v, w, tol, what in zip(got, want, tols, ("y", "dx", "dw_gate", "dw_up", "dw_down")):
+        bad = (v.double() - w).abs() > 1.01 * tol + rough * w.abs() + 1e-30
+        assert v.shape == w.shape and torch.isfinite(v).all() and not bad.any(), (what, int(bad.sum()))
+        # the bounds grow with every sum; a piece that is missing or doubled shows in the whole
+        assert float((v.double() - w).norm()) < (5e-3 if rough else 5e-6) * float(w.norm()), what
+
+
+@pytest.mark.parametrize("dtype,odd", [("f32", True), ("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("rows,width,hidden", [
+    (70, 40, 72), (2050, 2056, 72), (4100, 40, 2600), (8200, 1032, 136), (8200, 136, 4104), (2050, 2056, 1032),
+    (2050, 264, 4104), (70, 2056, 4104), (12000, 136, 4104), (12000, 2056, 136), (8200, 2056, 1032),
+    (2050, 2056, 2600), (12000, 2056, 264), (6000, 40, 72), (12000, 264, 136), (200, 1032, 2600), (8200, 2056, 4104)])
+def test_mlp_every_tile(rows, width, hidden, dtype, odd):
+    """Each product in each tile, whole, split along the contraction, and some tiles whole and some split: whatever the
+    launch rule chooses between 70 and 12000 rows."""
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(rows + hidden)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    K, F = (width - 5, hidden - 3) if odd else (width, hidden)
+    put = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device=DEV) * std).to(dt)  # noqa: E731
+    _mlp_check(put(rows, K), put(F, K, std=K ** -0.5), put(F, K, std=K ** -0.5), put(K, F, std=F ** -0.5),
+               put(rows, K), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_mlp_some_gradients(dtype):
+    """Any of the gradients alone through the C interface (where the split of their sums may be another one)."""
+    import itertools
+    import torch
+    from layer_lstm_forward_amd import block_ops as ops
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(4)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    put = lambda *s: torch.randn(*s, generator=gen, device=DEV).to(dt)  # noqa: E731
+    x, wg, wu, wd, dy = put(300, 72), put(200, 72), put(200, 72), put(64, 200), put(300, 64)
+    _, kept = pkg.gated_mlp_train(x, wg, wu, wd)
+    want = pkg.gated_mlp_backward(dy, x, wg, wu, wd, kept)
+    shape = ops._pack_mlp(1 if dtype == "bf16" else 0, 0, 300, 72, 200, 64)
+    n = ops.lstm_gated_mlp_backward_workspace_size(shape)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    for wanted in itertools.product((0, 1), repeat=4):
+        out = [torch.full_like(t, float("nan")) if k else None for t, k in zip(want, wanted)]
+        rc = ops.lstm_gated_mlp_backward(shape, x.data_ptr(), 72, wg.data_ptr(), wu.data_ptr(), wd.data_ptr(),
+                                         kept.data_ptr(), kept.numel(), dy.data_ptr(), 64,
+                                         *(None if t is None else t.data_ptr() for t in out), ws.data_ptr(), n,
+                                         torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        for a, b in zip(out, want):
+            assert a is None or torch.allclose(a.float(), b.float(), rtol=2 ** -6 if dtype == "bf16" else 1e-4,
+                                               atol=1e-2 if dtype == "bf16" else 1e-4)
+
+
+@pytest.mark.parametrize("rows", [9, 300])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_mlp_not_finite_rows_stay_alone(rows, dtype):
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(8)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    put = lambda *s: torch.randn(*s, generator=gen, device=DEV).to(dt)  # noqa: E731
+    x, wg, wu, wd, dy = put(rows, 40), put(50, 40), put(50, 40), put(24, 50), put(rows, 24)
+    y, kept = pkg.gated_mlp_train(x, wg, wu, wd)
+    dx = pkg.gated_mlp_backward(dy, x, wg, wu, wd, kept)[0]
+    keep = torch.arange(rows, device=DEV) != rows // 2
+    for bad in (float("nan"), float("inf")):
+        z = x.clone()
+        z[rows // 2, 3] = bad
+        got, held = pkg.gated_mlp_train(z, wg, wu, wd)
+        assert torch.equal(got[keep], y[keep]) and not torch.isfinite(got[~keep]).all()
+        d = dy.clone()
+        d[rows // 2, 3] = bad
+        got = pkg.gated_mlp_backward(d, x, wg, wu, wd, kept)[0]
+        assert torch.equal(got[keep], dx[keep]) and not torch.isfinite(got[~keep]).all()
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "sigmoid"])
+def test_mlp_large_values(kind):
+    """Activations at their ends: no product of 0 and infinity."""
+    for dtype in ("f32", "bf16"):
+        for rows in (9, 90):
+            mlp_case(rows, 24, 40, 16, dtype, kind, big=1e4)
 
 
 def test_mlp_no_rows():
