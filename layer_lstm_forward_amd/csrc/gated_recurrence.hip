@@ -17,9 +17,9 @@
 // tile, which hands its map on, finds the carry that it begins with from the
 // maps of the tiles before it, and hands on the carry that it ends with.  One
 // read of everything, and the results' bits do not depend on which tile is when
-// (16384 x 1 x 2048 bf16 64 us forward, 128 backward, the memory's time 38 and 75;
+// (16384 x 1 x 2048 bf16 65 us forward, 128 backward, the memory's time 38 and 75;
 // a launch for the maps of segments, one to join and one to walk them read it
-// twice: 70 and 113; fp32 119 and 173 against 122 and 319).
+// twice: 70 and 113; fp32 112 and 180 against 122 and 319).
 #include <type_traits>
 
 #include "blocks.h"
@@ -211,8 +211,14 @@ struct GrTile {
     static constexpr int LN = LN_, TC = TC_, U = U_, THREADS = LN * TC, WAVES = THREADS / 64;
     static constexpr bool CHAIN = CHAIN_;
 };
-// Of a chain: as many tokens a thread as its registers hold, at least kChainRun.
-constexpr int kChainLanes = 16, kChainRuns = 16, kChainRun = 8;
+// Of a chain: as many tokens a thread as its registers hold, at least kChainRun: a
+// tile costs its workgroup 2.6 us that do not depend on its length (65536 x 1 x 2048
+// bf16 309 us with 8 tokens a thread, 223 with 16, of 16 threads a channel; three
+// workgroups a CU instead of two, whose registers spill, 313).  32 threads a channel
+// halve the carry's way past the tiles (131072 x 1 x 256 bf16 100 -> 70 us, backward
+// 238 -> 131), and cost what is bound by memory up to a tenth (65536 x 1 x 2048
+// backward 423 -> 463).
+constexpr int kChainLanes = 16, kChainRuns = 32, kChainRun = 8;
 template <class DT, bool INPUT, bool BACK>
 using GrChain = GrTile<kChainLanes, kChainRuns, std::is_same_v<DT, BF16> && !INPUT && !BACK ? 16 : kChainRun, true>;
 constexpr int chain_tiles(int T, int run) { return (T - 1) / (kChainRuns * run) + 1; }
@@ -230,56 +236,47 @@ __global__ __launch_bounds__(256) void k_gr_clear(u32x4 *p, size_t n) {
 }
 
 // The carry that a tile begins with: that after the nearest tile before it which
-// has handed its own on, taken through the maps of the tiles between.  The runs
-// look at WINDOW tiles before theirs, again until one of them has (workgroups
-// are numbered as they start, so those before this one run or are done, and the
-// first waits for nobody).  Every tile's carry is its own map of the carry
-// before it, so it does not matter which one is found: the bits are the same.
+// has handed its own on, taken through the maps of the tiles between.  Each run
+// looks at one of the TC tiles before this one, again until one of them has
+// (workgroups are numbered as they start, so those before this one run or are
+// done, and the first waits for nobody).  Every tile's carry is its own map of the
+// carry before it, so it does not matter which one is found: the bits are the same.
 // The first wave takes the maps in turn, hands on the carry after this tile (its
 // map is P, Q), and tells the others.
 template <int V, class TL>
 __device__ inline void gr_carry_in(const GrCall &c, int tile, int l, int run, size_t at, int own, bool more,
                                    const float *P, const float *Q, float *carry) {
-    constexpr int TC = TL::TC, LN = TL::LN, K = 1, WINDOW = K * TC;
+    constexpr int WINDOW = TL::TC, LN = TL::LN;
+    static_assert(WINDOW <= 32, "a bit a tile");
     __shared__ float seen[WINDOW][LN][2][V];  // the map, or the carry in the place of B
     __shared__ int state[WINDOW][LN];         // 0: nothing yet, 1: the map, 2: the carry
     __shared__ float begin[LN][V];
-    int st[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) st[k] = 0;
-    int found = -1;
+    const int j = max(tile - 1 - run, 0);
+    int st = 0, found = -1;
     while (tile > 0) {
-        unsigned long long m[K][V], w[K][V];
+        unsigned long long m[V], w[V];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int j = max(tile - 1 - run - k * TC, 0);
+        for (int e = 0; e < V; ++e) {
+            w[e] = xload(gr_word(c, GR_CARRY, j, at) + e);
+            m[e] = st == 0 ? xload(gr_word(c, GR_MAP, j, at) + e) : 0;
+        }
+        bool map = run < tile && st == 0, all = run < tile;
+#pragma unroll
+        for (int e = 0; e < V; ++e) map = map && xtag(m[e]) != 0, all = all && xtag(w[e]) != 0;
+        if (map && !all) {
+            st = 1;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                w[k][e] = xload(gr_word(c, GR_CARRY, j, at) + e);
-                m[k][e] = st[k] == 0 ? xload(gr_word(c, GR_MAP, j, at) + e) : 0;
+                seen[run][l][0][e] = fabsf(__uint_as_float(xtag(m[e])));
+                seen[run][l][1][e] = __uint_as_float((uint32_t)m[e]);
             }
         }
+        if (all) {
+            st = 2;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int back = run + k * TC;
-            bool map = back < tile && st[k] == 0, all = back < tile;
-#pragma unroll
-            for (int e = 0; e < V; ++e) map = map && xtag(m[k][e]) != 0, all = all && xtag(w[k][e]) != 0;
-            if (map && !all) {
-                st[k] = 1;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    seen[back][l][0][e] = fabsf(__uint_as_float(xtag(m[k][e])));
-                    seen[back][l][1][e] = __uint_as_float((uint32_t)m[k][e]);
-                }
-            }
-            if (all) {
-                st[k] = 2;
-#pragma unroll
-                for (int e = 0; e < V; ++e) seen[back][l][1][e] = __uint_as_float((uint32_t)w[k][e]);
-            }
-            state[back][l] = st[k];
+            for (int e = 0; e < V; ++e) seen[run][l][1][e] = __uint_as_float((uint32_t)w[e]);
         }
+        state[run][l] = st;
         __syncthreads();
         unsigned maps = 0, carries = 0;
 #pragma unroll
@@ -657,10 +654,10 @@ GrWay gr_plan(int T, int B, int width, int dtype, bool backward) {
         least = walk;
         way = GR_LANES;
     }
-    // A chain: two launches, and the memory's time by 1.35, or 0.2 us for the carry's way past a tile; its grid holds
+    // A chain: two launches, and the memory's time by 1.35, or 0.25 us for the carry's way past a tile; its grid holds
     // 2^24 workgroups.
     const int parts = chain_tiles(T, kChainRun);
-    const double chain = 14.0 + (1.35 * stream > 0.2 * parts ? 1.35 * stream : 0.2 * parts);
+    const double chain = 14.0 + (1.35 * stream > 0.25 * parts ? 1.35 * stream : 0.25 * parts);
     if (parts > 1 && groups_of(B, width, kChainLanes, V) * parts < (1 << 24) && chain < least) way = GR_CHAIN;
     return way;
 }
