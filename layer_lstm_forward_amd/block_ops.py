@@ -503,7 +503,8 @@ def gated_mlp_backward(dy, x, w_gate, w_up, w_down, reserve, activation="silu", 
         _ops._same(dy, x, "dy", x.shape[:-1] + (a.out,))
         d, ds, _ = _tokens(dy, "dy")
         held = lstm_gated_mlp_reserve_size(a.shape)
-        if reserve.dtype != torch.uint8 or reserve.device != x.device or reserve.numel() != held:
+        if reserve.dtype != torch.uint8 or reserve.device != x.device or reserve.numel() != held \
+                or not reserve.is_contiguous():
             raise ValueError("reserve must be as gated_mlp_train returned it for this x")
         dx = x.new_empty(x.shape)
         dws = [w.new_empty(w.shape) for w in (w_gate, w_up, w_down)]

@@ -655,10 +655,10 @@ GrWay gr_plan(int T, int B, int width, int dtype, bool backward) {
         way = GR_LANES;
     }
     // A chain: two launches, and the memory's time by 1.35, or 0.25 us for the carry's way past a tile; its grid holds
-    // 2^24 workgroups.
+    // 2^23 workgroups (of 2^9 threads).
     const int parts = chain_tiles(T, kChainRun);
     const double chain = 14.0 + (1.35 * stream > 0.25 * parts ? 1.35 * stream : 0.25 * parts);
-    if (parts > 1 && groups_of(B, width, kChainLanes, V) * parts < (1 << 24) && chain < least) way = GR_CHAIN;
+    if (parts > 1 && groups_of(B, width, kChainLanes, V) * parts < (1 << 23) && chain < least) way = GR_CHAIN;
     return way;
 }
 

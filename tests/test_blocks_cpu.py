@@ -329,3 +329,13 @@ def test_refusals(kernels):
         with pytest.raises(ValueError):
             call()
     assert not [n for n in NOTES if n[0] == "kernels"]
+
+
+def test_refuses_a_reserve_with_gaps(kernels):
+    import torch
+    x, w, wd = put(5, 2, 8), put(6, 8), put(3, 6)
+    wide = torch.zeros(128, dtype=torch.uint8).as_subclass(type(x))
+    with pytest.raises(ValueError):
+        pkg.gated_mlp_backward(put(5, 2, 3), x, w, w, wd, wide[::2])
+    assert not [n for n in NOTES if n[0] == "kernels"]
+    pkg.gated_mlp_backward(put(5, 2, 3), x, w, w, wd, wide[:64])

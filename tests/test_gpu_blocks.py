@@ -585,6 +585,26 @@ def test_another_stream(dtype):
         assert torch.equal(x, y)
 
 
+def test_two_long_recurrences_at_once():
+    """Two chains of tiles on two streams: each waits for tiles of its own alone."""
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(8)
+    x, f = (torch.randn(6000, 1, 1000, generator=gen, device=DEV).bfloat16() for _ in range(2))
+    turned = x.flip(2).contiguous()
+    want = [pkg.gated_recurrence(a, f) for a in (x, turned)]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for k, a in enumerate((x, turned)):
+            got[k].append(pkg.gated_recurrence(a, f, stream=sides[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for y, last in got[k]:
+            assert torch.equal(y, want[k][0]) and torch.equal(last, want[k][1])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_graph_replays(dtype):
     """Two graphs, replayed in turn with eager calls between, and their inputs changed."""
