@@ -332,7 +332,7 @@ Backward backward_of(const lstm_gated_mlp_shape *s, const void *x, long long xs,
     f.dx.p[0].lists = 2;
     f.dw = mlp_call(s, MLP_STORE, 1, 1);
     f.dw.count = 0;
-    const bool sizes = workspace == nullptr;
+    const bool sizes = !dx && !dwg && !dwu && !dwd;  // a call wants something (its workspace may be of no bytes)
     if (dwg || sizes) f.dw.p[f.dw.count++] = stored(s, f.hidden.dgate, ox, s->hidden, s->in, s->rows, dwg);
     if (dwu || sizes) f.dw.p[f.dw.count++] = stored(s, f.hidden.dup, ox, s->hidden, s->in, s->rows, dwu);
     if (dwd || sizes) f.dw.p[f.dw.count++] = stored(s, oy, r.product, s->out, s->hidden, s->rows, dwd);
@@ -604,6 +604,7 @@ lstm_status lstm_gated_mlp_backward(const lstm_gated_mlp_shape *s, const void *x
     const void *ptrs[] = {s->rows ? x : nullptr, w_gate, w_up, w_down, s->rows ? reserve : nullptr,
                           s->rows ? dy : nullptr, dx, dw_gate, dw_up, dw_down, need ? workspace : nullptr};
     if (!all_on_device(ptrs, 11, dev)) return LSTM_ERR_DEVICE;
+    if (!dx && !dw_gate && !dw_up && !dw_down) return LSTM_OK;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const Backward f = backward_of(s, x, x_stride, w_gate, w_up, w_down, reserve, dy, dy_stride, dx, dw_gate, dw_up,
                                    dw_down, workspace);

@@ -540,6 +540,29 @@ def test_mlp_no_rows():
         assert d.shape == v.shape and not d.any()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_mlp_no_rows_and_some_gradients(dtype):
+    """Without rows a workspace may have no bytes; gradients that are not wanted stay out all the same."""
+    import itertools
+    import torch
+    from layer_lstm_forward_amd import block_ops as ops
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    w = [torch.ones(64, 64, dtype=dt, device=DEV) for _ in range(3)]
+    shape = ops._pack_mlp(1 if dtype == "bf16" else 0, 0, 0, 64, 64, 64)
+    n = ops.lstm_gated_mlp_backward_workspace_size(shape)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV) if n else None
+    assert (ws is None) == (dtype == "bf16") and ops.lstm_gated_mlp_reserve_size(shape) == 0
+    for wanted in itertools.product((0, 1), repeat=3):
+        out = [torch.full_like(t, 3.0) if k else None for t, k in zip(w, wanted)]
+        print(dtype, wanted, flush=True)
+        rc = ops.lstm_gated_mlp_backward(shape, None, 64, *(t.data_ptr() for t in w), None, 0, None, 64, None,
+                                         *(None if t is None else t.data_ptr() for t in out),
+                                         None if ws is None else ws.data_ptr(), n,
+                                         torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert rc == 0 and all(t is None or not t.any() for t in out)
+
+
 # ------------------------------------------------------- streams and graphs
 def _fresh(dtype):
     import torch
@@ -598,7 +621,7 @@ def test_two_long_recurrences_at_once():
     got = [[], []]
     for _ in range(4):
         for k, a in enumerate((x, turned)):
-            got[k].append(pkg.gated_recurrence(a, f, stream=sides[k]))
+            got[k].append(pkg.gated_recurrence(a, f, stream=sides[k].cuda_stream))
     torch.cuda.synchronize()
     for k in range(2):
         for y, last in got[k]:
