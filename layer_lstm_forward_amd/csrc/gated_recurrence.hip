@@ -11,7 +11,7 @@
 // over its threads, composes their maps (carry -> A carry + B, A the product of
 // the 1 - z), scans them and walks the tokens again from the carries that this
 // gives: one launch, and memory is read once, but the steps of a tile wait for
-// each other (333 x 5 x 1001 fp32 with an input gate: 12 + 17 us; 512 x 256 x
+// each other (333 x 5 x 1001 fp32 with an input gate: 12 + 18 us; 512 x 256 x
 // 2048 bf16 570 + 946).
 // k_gr_tile in a chain, where channels are too few and tokens many: a workgroup a
 // tile, which hands its map on, finds the carry that it begins with from the
