@@ -31,7 +31,9 @@ extern "C" {
  * as given before it (their logits f and i), and a state h:
  *     a_t = s(f_t)        w_t = s(i_t), or 1 - a_t without an input gate
  *     h_t = a_t h_{t-1} + w_t x_t         y_t = h_t
- * computed from 1 - a_t = s(-f_t), which keeps its digits for gates near 1. */
+ * computed from the smaller of a_t and 1 - a_t = s(-f_t), so that gates keep
+ * their digits near 0 and near 1 (gates below 2^-126 are 0).  An infinite
+ * state stays infinite, past a gate of 0, too. */
 typedef struct {
     int dtype;  /* lstm_dtype of x, the gates, y and their gradients */
     int T, B;   /* >= 1; T at most 2^30 */

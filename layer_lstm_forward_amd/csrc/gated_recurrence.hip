@@ -1,7 +1,7 @@
 // gated_recurrence.hip -- the gated linear recurrence, whole sequences forward
 // and backward, and single tokens.
-//     z = s(-f) (= 1 - a),  w = s(i) or z,  h_t = h_{t-1} - z h_{t-1} + w x_t
-//     D_t = dy_t + E_{t+1},  E_t = D_t - z D_t  (E: what reaches h_{t-1})
+//     a = s(f),  z = s(-f) = 1 - a,  w = s(i) or z,  h_t = a h_{t-1} + w x_t
+//     D_t = dy_t + E_{t+1},  E_t = a D_t  (E: what reaches h_{t-1})
 //     dx = w D,  df = D (h_{t-1} - [w = z] x) z a,  di = D x w (1 - w)
 // Three ways, chosen by an estimate of their times (gr_plan):
 // k_gr_lanes: a thread walks the tokens of four neighbouring channels of a batch
@@ -9,7 +9,7 @@
 // 2048 bf16 304 us forward, 597 backward (5.3 and 5.4 TB/s, as a copy).
 // k_gr_tile, for little work: a workgroup spreads a tile of tokens of 32 channels
 // over its threads, composes their maps (carry -> A carry + B, A the product of
-// the 1 - z), scans them and walks the tokens again from the carries that this
+// the a), scans them and walks the tokens again from the carries that this
 // gives: one launch, and memory is read once, but the steps of a tile wait for
 // each other (333 x 5 x 1001 fp32 with an input gate: 12 + 18 us; 512 x 256 x
 // 2048 bf16 570 + 946).
@@ -82,13 +82,32 @@ __device__ inline int gr_length(const GrCall &c, int b) {
     return c.lengths ? min(max(c.lengths[b], 0), c.T) : c.T;
 }
 
-// s(-f) and s(f), each with all its digits.
-__device__ inline void gates(float f, float &z, float &a) {
-    const float e = __builtin_amdgcn_exp2f(fabsf(f) * -1.4426950408889634f), big = __builtin_amdgcn_rcpf(1.0f + e);
-    const float small = e * big;
-    z = f < 0.0f ? big : small;
-    a = f < 0.0f ? small : big;
-}
+// s(f) and s(-f) of a logit, the smaller of them as precise as the larger, to (|f| + 3) 2^-23 of itself (0 below
+// 2^-126).  What is kept of a value is taken from the smaller one, too: h - s(-f) h where the gate is near 1 and s(f) h
+// where it is near 0; either form alone loses the digits of the other's end (s(f) 1e3 at f = -16 as 1e3 - s(16) 1e3 is
+// off by 6%).
+struct Gate {
+    float f, small, big;
+    __device__ explicit Gate(float logit) : f(logit) {
+        const float e = __builtin_amdgcn_exp2f(fabsf(f) * -1.4426950408889634f);
+        big = __builtin_amdgcn_rcpf(1.0f + e);
+        small = e * big;
+    }
+    __device__ float on() const { return f < 0.0f ? small : big; }   // s(f)
+    __device__ float off() const { return f > 0.0f ? small : big; }  // s(-f)
+    __device__ float slope() const { return small * big; }           // s'(f)
+    __device__ float share() const { return f > 0.0f ? -small : small; }
+    // s(f) h; an infinite h stays what it is (h - part is 0 of finite ones).
+    __device__ float keep(float h) const {
+        const float part = __builtin_amdgcn_fmed3f(h, -3.4028235e38f, 3.4028235e38f);
+        return fmaf(share(), part, f > 0.0f ? h : h - part);
+    }
+    // s(f) A of a map's factor, 0 < A <= 1.
+    __device__ float keep_factor(float A) const { return fmaf(share(), A, f > 0.0f ? A : kLeast); }
+    // Factors do not become 0, so that an infinite carry stays infinite however many gates lie between; 2^-149 of any
+    // finite one is nothing.
+    static constexpr float kLeast = 1.4e-45f;
+};
 
 // The thread's batch row and first channel.  Where the width is no multiple of
 // V the last piece ends with the row, and its first `own` values are read but
@@ -105,9 +124,11 @@ __device__ inline bool gr_place(const GrCall &c, int *b, int *ch, int *own) {
     return true;
 }
 
-// Backward the tokens count from the row's end.
+// Backward the tokens count from the row's end.  Of bf16 without an input gate four waves a SIMD, for two spilled
+// registers (256 x 512 x 2048 forward 315 us against 329 with 131 registers; with the gate three waves instead of two
+// 440 against 422).
 template <class DT, int V, bool INPUT, bool BACK>
-__global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
+__global__ __launch_bounds__(256, !BACK && !INPUT && sizeof(typename DT::S) == 2 ? 4 : 1) void k_gr_lanes(GrCall c) {
     // tokens loaded at a time, and as many under way: with more tensors fewer
     constexpr int U = BACK ? 4 : 8;
     int b, ch, own;
@@ -151,28 +172,23 @@ __global__ __launch_bounds__(256) void k_gr_lanes(GrCall c) {
             }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                float z, a;
-                if (BACK)
-                    gates(k.f[u].at(e), z, a);
-                else
-                    z = sigmoid_f(-k.f[u].at(e));
+                const Gate a(k.f[u].at(e));
                 if (!BACK) {
-                    const float w = INPUT ? sigmoid_f(k.g[u].at(e)) : z;
-                    h[e] = fmaf(w, k.x[u].at(e), fmaf(-z, h[e], h[e]));
+                    const float w = INPUT ? sigmoid_f(k.g[u].at(e)) : a.off();
+                    h[e] = fmaf(w, k.x[u].at(e), a.keep(h[e]));
                     r[0][e] = h[e];
                 } else {
                     const float D = k.d[u].at(e) + h[e], x = k.x[u].at(e);
                     if (INPUT) {
-                        float v, w;
-                        gates(k.g[u].at(e), v, w);
-                        r[0][e] = w * D;
-                        r[1][e] = D * was[e] * (z * a);
-                        r[2][e] = D * x * (w * v);
+                        const Gate w(k.g[u].at(e));
+                        r[0][e] = w.on() * D;
+                        r[1][e] = D * was[e] * a.slope();
+                        r[2][e] = D * x * w.slope();
                     } else {
-                        r[0][e] = z * D;
-                        r[1][e] = D * (was[e] - x) * (z * a);
+                        r[0][e] = a.off() * D;
+                        r[1][e] = D * (was[e] - x) * a.slope();
                     }
-                    h[e] = fmaf(-z, D, D);
+                    h[e] = a.keep(D);
                 }
             }
             if (!BACK) gr_store<DT, V>(const_cast<char *>(gr_at<DT>(c.y, b, ch, t)), r[0], own);
@@ -399,14 +415,13 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float z = sigmoid_f(-q.f[u].at(e));
-                A[e] = fmaf(-z, A[e], A[e]);
+                const Gate a(q.f[u].at(e));
+                A[e] = a.keep_factor(A[e]);
                 if (BACK) {
-                    const float D = q.d[u].at(e) + B[e];
-                    B[e] = fmaf(-z, D, D);
+                    B[e] = a.keep(q.d[u].at(e) + B[e]);
                 } else {
-                    const float w = INPUT ? sigmoid_f(q.g[u].at(e)) : z;
-                    B[e] = fmaf(w, q.x[u].at(e), fmaf(-z, B[e], B[e]));
+                    const float w = INPUT ? sigmoid_f(q.g[u].at(e)) : a.off();
+                    B[e] = fmaf(w, q.x[u].at(e), a.keep(B[e]));
                     to[BACK ? 0 : u][0][e] = A[e];
                     to[BACK ? 0 : u][1][e] = B[e];
                 }
@@ -421,7 +436,7 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
             for (int e = 0; e < V; ++e) {
                 const float a = __shfl_up(A[e], s), p = __shfl_up(B[e], s);
                 B[e] = on ? fmaf(A[e], p, B[e]) : B[e];
-                A[e] = on ? A[e] * a : A[e];
+                A[e] = on ? fmaf(A[e], a, Gate::kLeast) : A[e];
             }
         }
         if (lane >= 64 - LN)
@@ -447,7 +462,7 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
                 for (int e = 0; e < V; ++e) {
                     const float a = maps[turn][w][l][e];
                     Q[e] = fmaf(a, Q[e], maps[turn][w][l][V + e]);
-                    P[e] *= a;
+                    P[e] = fmaf(P[e], a, Gate::kLeast);
                 }
             if (more && tile > 0 && run == 0)
 #pragma unroll
@@ -497,19 +512,17 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float D = q.d[u].at(e) + h[e], x = q.x[u].at(e);
-                        float z, a;
-                        gates(q.f[u].at(e), z, a);
+                        const Gate a(q.f[u].at(e));
                         if (INPUT) {
-                            float v, w;
-                            gates(q.g[u].at(e), v, w);
-                            dx[e] = w * D;
-                            df[e] = D * was[e] * (z * a);
-                            di[e] = D * x * (w * v);
+                            const Gate w(q.g[u].at(e));
+                            dx[e] = w.on() * D;
+                            df[e] = D * was[e] * a.slope();
+                            di[e] = D * x * w.slope();
                         } else {
-                            dx[e] = z * D;
-                            df[e] = D * (was[e] - x) * (z * a);
+                            dx[e] = a.off() * D;
+                            df[e] = D * (was[e] - x) * a.slope();
                         }
-                        h[e] = fmaf(-z, D, D);
+                        h[e] = a.keep(D);
                     }
                     gr_store<DT, V>(p[0] + u * step(c.dx), dx, part);
                     gr_store<DT, V>(p[1] + u * step(c.df), df, part);
@@ -559,8 +572,9 @@ __global__ __launch_bounds__(64) void k_gr_step(GrStep c) {
     __builtin_memcpy(h, s, sizeof(h));
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const float z = sigmoid_f(-f[e]), w = INPUT ? sigmoid_f(g[e]) : z;
-        h[e] = fmaf(w, x[e], fmaf(-z, h[e], h[e]));
+        const Gate a(f[e]);
+        const float w = INPUT ? sigmoid_f(g[e]) : a.off();
+        h[e] = fmaf(w, x[e], a.keep(h[e]));
     }
     __builtin_memcpy(s, h, sizeof(h));
     gr_store<DT, V>(y, h);

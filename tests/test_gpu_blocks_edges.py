@@ -1,0 +1,147 @@
+"""The operators of include/lstm_blocks.h on the GPU at the ends of what their arguments hold, against the fp64 oracle.
+
+Tolerances as in test_gpu_blocks.py: bounds on rounding, element by element, carried through the same formulas as the
+values."""
+import numpy as np
+import pytest
+
+import layer_lstm_forward_amd as pkg
+from oracle import blocks as ref
+from tests.test_gpu_blocks import Rec
+from tests.test_gpu_ops import DEV, U16, U32, close, dev, draw, host
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------- gated recurrence
+class Sharp(Rec):
+    """A case whose bounds are relative to what a gate keeps: the smaller of a = s(f) and z = s(-f) is off by
+    cf = (8 + 2 |f|) U32 of itself, and what is kept, a h, by cf min(a, z) h and a rounding of a h."""
+
+    def bounds(self):
+        B, T, W = self.x.shape
+        f, x = self.f.astype(np.float64), np.abs(self.x.astype(np.float64))
+        a, z = ref.logistic(f), ref.logistic(-f)
+        cf = (8 + 2 * np.abs(f)) * U32
+        w, cw = (z, cf) if self.i is None else (ref.logistic(self.i), (8 + 2 * np.abs(self.i)) * U32)
+        rough = U16 if self.dtype == "bf16" else 0.0
+        n = [T] * B if self.lengths is None else self.lengths
+        ey, es, mag, eh = np.zeros((B, T, W)), np.zeros((B, W)), np.zeros((B, T + 1, W)), np.zeros((B, T + 1, W))
+        ex, ef, ei, eds = np.zeros((B, T, W)), np.zeros((B, T, W)), np.zeros((B, T, W)), np.zeros((B, W))
+        off = cf * np.minimum(a, z)
+        for b in range(B):
+            h = np.zeros(W) if self.S is None else np.abs(self.S[b].astype(np.float64))
+            e = np.zeros(W)
+            mag[b, 0] = h
+            for t in range(n[b]):
+                e = a[b, t] * e + off[b, t] * h + cw[b, t] * w[b, t] * x[b, t]
+                h = a[b, t] * h + w[b, t] * x[b, t]
+                e = e + 6 * U32 * h
+                ey[b, t], eh[b, t + 1], mag[b, t + 1] = e + rough * h, e, h
+            es[b] = e
+            D = np.zeros(W) if self.dS is None else np.abs(self.dS[b].astype(np.float64))
+            e = np.zeros(W)
+            for t in range(n[b] - 1, -1, -1):
+                D = D + np.abs(self.dy[b, t])
+                e = e + 4 * U32 * D
+                was = mag[b, t] + (x[b, t] if self.i is None else 0.0)
+                far = eh[b, t] + (rough * mag[b, t] if t else 0.0) + 2 * U32 * was
+                s = a[b, t] * z[b, t]
+                ex[b, t] = w[b, t] * (e + (cw[b, t] + 2 * U32 + rough) * D)
+                ef[b, t] = s * (e * was + D * far + (2 * cf[b, t] + 6 * U32 + rough) * D * was)
+                if self.i is not None:
+                    v = w[b, t] * ref.logistic(-np.asarray(self.i[b, t], np.float64))
+                    ei[b, t] = v * x[b, t] * (e + (2 * cw[b, t] + 6 * U32 + rough) * D)
+                e = a[b, t] * e + (off[b, t] + 6 * U32 * a[b, t]) * D
+                D = a[b, t] * D
+            eds[b] = e
+        return [v + 1e-30 for v in (ey, es, ex, ef, ei, eds)]
+
+
+def resets(T, B, W, dtype, gates=2, lengths=None):
+    """Tokens that write values of a thousand into the state, tokens that reset it (logits -8 to -20) and many that
+    keep it and write next to nothing, so that after a reset the state is what the reset left of it."""
+    c = Sharp(T, B, W, dtype, gates, lengths=lengths, seed=4)
+    rng = np.random.default_rng(T + W)
+    kind = rng.integers(0, 8, (B, T, W))
+    f = np.where(kind == 0, rng.uniform(-20, -8, kind.shape), rng.uniform(1, 8, kind.shape))
+    put = lambda v: host(dev(v.astype(np.float32), dtype)).astype(np.float32)  # noqa: E731
+    c.f = put(f)
+    if gates == 2:
+        c.i = put(np.where(kind == 1, 3.0, -18.0))
+        c.x = put(np.where(kind == 1, 1000.0, 1.0) * c.x)
+    else:
+        c.x = put(np.where(kind == 0, 1e-6, 1000.0) * c.x)
+    c.S, c.dS = c.S * np.float32(1000), c.dS * np.float32(1000)
+    return c
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,W,gates", [(1, 4, 33, 2), (40, 2, 24, 2), (40, 2, 24, 1), (333, 5, 1001, 2),
+                                         (130, 44, 1000, 1), (1500, 2, 9, 2)])
+def test_recurrence_resets(T, B, W, gates, dtype):
+    """What a gate near 0 leaves of a large state has all its digits (h - (1 - a) h would have none at a logit of -18),
+    in every way the recurrence runs."""
+    resets(T, B, W, dtype, gates).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_recurrence_step_resets(dtype):
+    import torch
+    W = 512
+    logits = np.linspace(-20, -8, W, dtype=np.float32)
+    f = host(dev(np.stack([logits, -logits]), dtype))
+    pool = np.random.default_rng(1).standard_normal((2, W)).astype(np.float32) * 1000
+    state, x = dev(pool), torch.zeros(2, W, device=DEV, dtype=torch.float32 if dtype == "f32" else torch.bfloat16)
+    y = pkg.gated_recurrence_step(x, dev(f.astype(np.float32), dtype), state)
+    want = ref.logistic(f) * pool
+    tol = ((8 + 2 * np.abs(f)) * np.minimum(ref.logistic(f), ref.logistic(-f)) + 2 * ref.logistic(f)) * U32 * np.abs(pool)
+    close(state, want, tol, "state")
+    close(y, want, tol + (U16 if dtype == "bf16" else 0.0) * np.abs(want), "y")
+
+
+def same_infinities(got, want, what):
+    """Infinite where the formula is and with its sign, nothing not a number, finite where the formula is."""
+    got = host(got)
+    assert not np.isnan(want).any() and got.shape == want.shape, what
+    assert np.array_equal(np.where(np.isinf(want), want, 0.0), np.where(np.isfinite(got), 0.0, got)), what
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,W,gates", [(1, 2, 24, 1), (40, 2, 24, 2), (400, 4, 500, 1), (130, 44, 1000, 2),
+                                         (1500, 2, 9, 1), (3000, 1, 130, 2)])
+def test_recurrence_infinities(T, B, W, gates, dtype):
+    """An infinite state, token or gradient stays an infinity of its sign, however many gates follow it."""
+    c = Rec(T, B, W, dtype, gates, seed=2)
+    c.f = host(dev(np.random.default_rng(3).standard_normal((B, T, W)).astype(np.float32) * 3, dtype)).astype(np.float32)
+    c.S[0, 0], c.S[-1, 2], c.x[0, T // 2, 4] = np.inf, -np.inf, -np.inf
+    c.dS[0, 6], c.dy[-1, T // 2, 8] = np.inf, -np.inf
+    x, f, i, dy = c.tensors()
+    S, dS = dev(c.S), dev(c.dS)
+    y, last = pkg.gated_recurrence(x, f, i, state=S)
+    dx, _, di, dstate = pkg.gated_recurrence_backward(x, f, y, dy, i, state=S, dstate=dS)
+    ry, rlast = ref.gated_recurrence(c.x, c.f, c.i, c.S)
+    for got, want, what in ((c.host(y), ry, "y"), (host(last), rlast, "state")):
+        same_infinities(dev(got), want, what)
+    rx, _, ri, rs = ref.gated_recurrence_backward(c.x, c.f, c.dy, c.i, c.S, c.dS)
+    same_infinities(dev(c.host(dx)), rx, "dx")
+    same_infinities(dstate, rs, "dstate")
+    if T == 1:
+        pool = S.clone()
+        out = pkg.gated_recurrence_step(x[0], f[0], pool, input_gate=None if i is None else i[0])
+        same_infinities(out, ry[:, 0], "step")
+        same_infinities(pool, rlast, "pool")
+
+
+@pytest.mark.parametrize("T,B,W", [(1, 2, 24), (40, 2, 24), (130, 44, 1000), (1500, 2, 9)])
+def test_recurrence_infinity_past_gates_of_zero(T, B, W):
+    """A gate that is 0 in 32 bits, by its logit or by underflow, leaves an infinite state infinite in every way."""
+    import torch
+    x = torch.ones(T, B, W, device=DEV)
+    S = torch.full((B, W), float("-inf"), device=DEV)
+    for logit in (-95.0, -200.0, float("-inf")):
+        f = torch.full_like(x, logit)
+        y, last = pkg.gated_recurrence(x, f, state=S)
+        assert torch.equal(y, S.expand_as(y)) and torch.equal(last, S)
+        pool = S.clone()
+        assert torch.equal(pkg.gated_recurrence_step(x[0], f[0], pool), S) and torch.equal(pool, S)
