@@ -56,7 +56,10 @@ lstm_status lstm_gated_recurrence_backward_workspace_size(const lstm_gated_recur
  *   y            view, written; must not overlap an input or itself
  *   state_out    like state: the state after each row's last token, or NULL.
  *                It may be the memory of `state`.
- *   workspace    16-byte aligned
+ *   workspace    16-byte aligned.  Where it has bytes, workgroups wait for
+ *                each other through it.  A wait ends after five seconds at the
+ *                latest, as it can where two calls at once share a workspace:
+ *                what depends on it is NaN then.
  * LSTM_ERR_ARG: NULL argument; LSTM_ERR_SHAPE: T, B or width outside their
  * limits, or B * width above 2^31 - 1; LSTM_ERR_WORKSPACE: workspace too short. */
 lstm_status lstm_gated_recurrence_forward(const lstm_gated_recurrence_shape *shape, const lstm_view *x,

@@ -23,8 +23,9 @@ struct GrCall {
     float *s1;             // state after the last, or null
     const float *ds1;      // gradient of s1, or null
     float *ds0;            // gradient of s0, or null
-    unsigned *ticket;            // GR_CHAIN: workspace, gr_words bytes: a counter, and 256 bytes on the words
-    unsigned long long *words;
+    unsigned *ticket;            // GR_CHAIN: workspace, gr_words bytes: a counter, 8 bytes on the word that says a
+    unsigned long long *words;   // wait was given up, 256 bytes on the words
+    long long patience;          // GR_CHAIN: clock ticks that a tile waits at most; below 0 none waits
     int T, B, width, dtype;
     int way, tiles;        // GrWay; tiles of a chain (set by its launch)
 };

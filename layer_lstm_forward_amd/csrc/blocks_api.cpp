@@ -44,9 +44,13 @@ lstm_status gr_size(const lstm_gated_recurrence_shape *s, bool backward, GrCall 
     return LSTM_OK;
 }
 
-void gr_workspace(GrCall *c, void *workspace) {
+void gr_workspace(GrCall *c, void *workspace, int dev) {
     c->ticket = static_cast<unsigned *>(workspace);
     c->words = reinterpret_cast<unsigned long long *>(static_cast<char *>(workspace) + 256);
+    if (c->way != GR_CHAIN) return;
+    int khz = 0;
+    if (hipDeviceGetAttribute(&khz, hipDeviceAttributeWallClockRate, dev) != hipSuccess) (void)hipGetLastError();
+    c->patience = (khz > 0 ? khz : 100000) * 1000ll * 5;  // five seconds
 }
 
 // ------------------------------------------------------------------- rotary
@@ -390,7 +394,7 @@ lstm_status lstm_gated_recurrence_forward(const lstm_gated_recurrence_shape *s, 
     c.lengths = lengths;
     c.s0 = state;
     c.s1 = state_out;
-    gr_workspace(&c, workspace);
+    gr_workspace(&c, workspace, dev);
     c.T = s->T;
     c.B = s->B;
     c.width = s->width;
@@ -431,7 +435,7 @@ lstm_status lstm_gated_recurrence_backward(const lstm_gated_recurrence_shape *s,
     c.s0 = state;
     c.ds1 = dstate_out;
     c.ds0 = dstate;
-    gr_workspace(&c, workspace);
+    gr_workspace(&c, workspace, dev);
     c.T = s->T;
     c.B = s->B;
     c.width = s->width;

@@ -247,6 +247,11 @@ __device__ inline unsigned long long *gr_word(const GrCall &c, int kind, int til
     return c.words + ((size_t)kind * c.tiles + tile) * ((size_t)c.B * c.width) + at;
 }
 
+// Not 0 once a tile has given up its wait.
+__device__ inline unsigned long long *gr_given_up(const GrCall &c) {
+    return reinterpret_cast<unsigned long long *>(c.ticket) + 1;
+}
+
 __global__ __launch_bounds__(256) void k_gr_clear(u32x4 *p, size_t n) {
     for (size_t i = blockIdx.x * 256ull + threadIdx.x; i < n; i += gridDim.x * 256ull) p[i] = u32x4{0, 0, 0, 0};
 }
@@ -257,6 +262,9 @@ __global__ __launch_bounds__(256) void k_gr_clear(u32x4 *p, size_t n) {
 // (workgroups are numbered as they start, so those before this one run or are
 // done, and the first waits for nobody).  Every tile's carry is its own map of the
 // carry before it, so it does not matter which one is found: the bits are the same.
+// A wait ends after c.patience ticks all the same (the words may have been cleared or
+// written by another call on the same workspace), or once another tile's has: the
+// carry is not a number then, and all workgroups come to their end.
 // The first wave takes the maps in turn, hands on the carry after this tile (its
 // map is P, Q), and tells the others.
 template <int V, class TL>
@@ -269,7 +277,24 @@ __device__ inline void gr_carry_in(const GrCall &c, int tile, int l, int run, si
     __shared__ float begin[LN][V];
     const int j = max(tile - 1 - run, 0);
     int st = 0, found = -1;
+    unsigned spins = 0;
+    long long since = 0;
     while (tile > 0) {
+        if (__builtin_expect(c.patience < 0 || (++spins & 255) == 0, 0)) {
+            const long long now = wall_clock64();
+            if (spins == 256) since = now;
+            const bool over = threadIdx.x == 0 && (now - since > c.patience || xload(gr_given_up(c)) != 0);
+            if (__syncthreads_or(c.patience < 0 || over)) {
+                found = 0;
+                if (run == 0) {
+                    xstore(gr_given_up(c), 1);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) seen[0][l][1][e] = __builtin_nanf("");
+                }
+                __syncthreads();
+                break;
+            }
+        }
         unsigned long long m[V], w[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -349,6 +374,7 @@ __global__ __launch_bounds__(TL::THREADS) void k_gr_tile(GrCall c) {
         __syncthreads();
         tile = (int)(number / (unsigned)(c.B * slabs));
         group = (int)(number % (unsigned)(c.B * slabs));
+        if (tile >= c.tiles) return;  // only where another call counts on the same workspace
     }
     const int b = group / slabs;
     const int from = (group % slabs * LN + l) * V, ch = min(from, c.width - V), own = from - ch;

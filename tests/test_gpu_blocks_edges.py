@@ -2,6 +2,8 @@
 
 Tolerances as in test_gpu_blocks.py: bounds on rounding, element by element, carried through the same formulas as the
 values."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -145,3 +147,66 @@ def test_recurrence_infinity_past_gates_of_zero(T, B, W):
         assert torch.equal(y, S.expand_as(y)) and torch.equal(last, S)
         pool = S.clone()
         assert torch.equal(pkg.gated_recurrence_step(x[0], f[0], pool), S) and torch.equal(pool, S)
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("t", ctypes.c_longlong), ("b", ctypes.c_longlong)]
+
+
+class _Call(ctypes.Structure):
+    """GrCall of csrc/blocks.h."""
+    _fields_ = [(n, _View) for n in ("x", "f", "i", "y", "dy", "dx", "df", "di")] + \
+        [(n, ctypes.c_void_p) for n in ("lengths", "s0", "s1", "ds1", "ds0", "ticket", "words")] + \
+        [("patience", ctypes.c_longlong)] + [(n, ctypes.c_int) for n in ("T", "B", "width", "dtype", "way", "tiles")]
+
+
+def _chain(x, f, patience, dy=None, y=None):
+    """A chain's launch with a patience of its own; returns (y, state) or (dx, dforget, dstate), and the workspace."""
+    import torch
+    from layer_lstm_forward_amd import block_ops as ops
+    T, B, W = x.shape
+    backward = dy is not None
+    c = _Call(T=T, B=B, width=W, dtype=0, way=2, patience=patience)
+    view = lambda t: _View(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    n = ops.lstm_gated_recurrence_workspace_size(ops._pack_recurrence(0, T, B, W))
+    assert n > 256
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    state, out = torch.empty(B, W, device=DEV), [torch.empty_like(x) for _ in range(2 if backward else 1)]
+    c.x, c.f, c.ticket, c.words = view(x), view(f), ws.data_ptr(), ws.data_ptr() + 256
+    if backward:
+        c.y, c.dy, c.dx, c.df, c.ds0 = view(y), view(dy), view(out[0]), view(out[1]), state.data_ptr()
+    else:
+        c.y, c.s1 = view(out[0]), state.data_ptr()
+    launch = getattr(ctypes.CDLL(pkg.LIB_PATH), "_ZN8lstm_amd%s%sERKNS_6GrCallEP12ihipStream_t" % (
+        ("18", "launch_gr_backward") if backward else ("17", "launch_gr_forward")))
+    launch.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    assert launch(ctypes.addressof(c), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    return out + [state], ws
+
+
+def test_recurrence_chain_gives_up():
+    """A chain whose tiles wait for nobody: the first is right, what depends on a wait is not a number, and the launch
+    comes to its end.  With patience the same launch is the library's call."""
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+    T, TILE = 5000, 256
+    x, f, dy = (torch.randn(T, 2, 9, generator=gen, device=DEV) for _ in range(3))
+    f += 4
+    y, last = pkg.gated_recurrence(x, f)
+    dx, df = pkg.gated_recurrence_backward(x, f, y, dy)[:2]
+    (gy, glast), _ = _chain(x, f, 10 ** 9)
+    assert torch.equal(gy, y) and torch.equal(glast, last)
+    (gx, gf, _), _ = _chain(x, f, 10 ** 9, dy=dy, y=y)
+    assert torch.equal(gx, dx) and torch.equal(gf, df)
+    (gy, glast), _ = _chain(x, f, -1)
+    assert torch.equal(gy[:TILE], y[:TILE]) and gy[TILE:].isnan().all() and glast.isnan().all()
+    (gx, gf, gs), _ = _chain(x, f, -1, dy=dy, y=y)
+    assert torch.equal(gx[T - TILE:], dx[T - TILE:]) and gx[:T - TILE].isnan().all() and gs.isnan().all()
+    # no tick of patience: a value is right or not a number, whichever tiles had to wait
+    (gy, _), ws = _chain(x, f, 0)
+    lost = gy.isnan()
+    assert torch.equal(gy[~lost], y[~lost]) and bool(lost.any()) == bool(ws[8:16].any())
+    again, _ = pkg.gated_recurrence(x, f)
+    assert torch.equal(again, y)
