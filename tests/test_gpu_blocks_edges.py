@@ -210,3 +210,51 @@ def test_recurrence_chain_gives_up():
     assert torch.equal(gy[~lost], y[~lost]) and bool(lost.any()) == bool(ws[8:16].any())
     again, _ = pkg.gated_recurrence(x, f)
     assert torch.equal(again, y)
+
+
+# ----------------------------------------------------------------- gated MLP
+def kept_values(kept, rows, F):
+    """g and u of a bf16 reserve: the upper 16 bits of each value, [rows][ld], and eight more in a plane of bytes behind
+    them, parts 256-byte aligned."""
+    ld, at, out = (F + 7) // 8 * 8, 0, []
+    raw = kept.cpu().numpy()
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    for _ in range(2):
+        high = raw[at:at + rows * ld * 2].view(np.uint16).astype(np.uint32)
+        at += up(rows * ld * 2)
+        low = raw[at:at + rows * ld].astype(np.uint32)
+        at += up(rows * ld)
+        out.append((high << 16 | low << 8).view(np.float32).reshape(rows, ld)[:, :F].astype(np.float64))
+    return out
+
+
+@pytest.mark.parametrize("rows", [9, 200, 3000])
+def test_mlp_keeps_g_and_u_to_nearest(rows):
+    """What is kept for the backward call is rounded to its 16 bits, off by half a step and to neither side."""
+    rng = np.random.default_rng(rows)
+    K, F = 24, 200
+    x, wg, wu = draw(rng, (rows, K), "bf16"), draw(rng, (F, K), "bf16"), draw(rng, (F, K), "bf16")
+    _, kept = pkg.gated_mlp_train(*(dev(v, "bf16") for v in (x, wg, wu, draw(rng, (16, F), "bf16"))))
+    for got, w in zip(kept_values(kept, rows, F), (wg, wu)):
+        want = x.astype(np.float64) @ w.T.astype(np.float64)
+        off = got - want
+        assert np.all(np.abs(off) <= 2.0 ** -16 * np.abs(want) + (K + 40) * U32 * (np.abs(x) @ np.abs(w).T)), "half a step"
+        # the mean of n errors of at most half a step, even by their signs: 6 standard deviations
+        side = np.sign(want) * off / np.abs(want)
+        assert abs(side.mean()) < 6 * 2.0 ** -16 / np.sqrt(3 * side.size) + 2.0 ** -16 / 256
+
+
+@pytest.mark.parametrize("rows", [9, 200])
+def test_mlp_keeps_the_ends(rows):
+    """The largest finite values stay finite, infinities and what is not a number stay what they are."""
+    x = np.full((rows, 4), 2.0 ** 63, np.float32)
+    # in eighths of the significand the largest fp32 value, 2^128 - 2^104; one hidden unit past it
+    part = np.array([2.0 ** 64, 2.0 ** 64 * (1 - 2.0 ** -8), 2.0 ** 56 * (1 - 2.0 ** -8), 2.0 ** 48 * (1 - 2.0 ** -7)])
+    w = np.tile(part.astype(np.float32), (40, 1))
+    w[1, 1] = 2.0 ** 64
+    x[3, 0] = np.nan
+    _, kept = pkg.gated_mlp_train(*(dev(v, "bf16") for v in (x, w, w, np.ones((8, 40), np.float32))))
+    for got in kept_values(kept, rows, 40):
+        assert np.isnan(got[3]).all()
+        got = np.delete(got, 3, 0)
+        assert np.all(got[:, 1] == np.inf) and np.all(np.delete(got, 1, 1) == 2.0 ** 128 - 2.0 ** 112)
