@@ -203,8 +203,8 @@ __device__ inline void finish(const MlpCall &c, const MlpProduct &p, Place at, i
                 if (i < left) o[i] = round_to<DT>(v[i]);
         }
     } else if constexpr (EPI == MLP_GATE) {
-        // columns past N are 0 (the operand's rows past N read as zeros), and
-        // so are act(0) 0: the next product may run over them
+        // columns past N are 0 (the operand's rows past N read as zeros), but for
+        // rows of x that are not finite; the next product runs over them
         if (c.gate.p) {
             Kept<F32_>::store(c.gate, at, v);
             Kept<F32_>::store(c.up, at, w);
@@ -212,7 +212,7 @@ __device__ inline void finish(const MlpCall &c, const MlpProduct &p, Place at, i
         float a[8];
         activate<false>(c.act, v, a, nullptr);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = a[i] * w[i];
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? a[i] * w[i] : 0.0f;
         store_planes<F32_>(c.product, at, v);
     } else {
         float g[8], u[8], a[8], slope[8];

@@ -258,3 +258,20 @@ def test_mlp_keeps_the_ends(rows):
         assert np.isnan(got[3]).all()
         got = np.delete(got, 3, 0)
         assert np.all(got[:, 1] == np.inf) and np.all(np.delete(got, 1, 1) == 2.0 ** 128 - 2.0 ** 112)
+
+
+@pytest.mark.parametrize("rows", [9, 90, 3000])
+@pytest.mark.parametrize("hidden", [40, 50])
+def test_mlp_infinities(rows, hidden):
+    """bf16: an infinite value of x makes the row's outputs infinite, of the formula's sign, also where the hidden
+    units do not fill their last piece."""
+    import torch
+    rng = np.random.default_rng(hidden)
+    K, O = 40, 24
+    x = draw(rng, (rows, K), "bf16")
+    wg, wu, wd = (np.abs(draw(rng, s, "bf16")) + 0.125 for s in ((hidden, K), (hidden, K), (O, hidden)))
+    wd[::2] *= -1
+    x[rows // 2, 3] = np.inf
+    y = host(pkg.gated_mlp(*(dev(v, "bf16") for v in (x, wg, wu, wd))))
+    want = np.where(np.arange(O) % 2, np.inf, -np.inf)
+    assert np.array_equal(y[rows // 2], want) and np.isfinite(np.delete(y, rows // 2, 0)).all()
