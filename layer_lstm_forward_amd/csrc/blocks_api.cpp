@@ -189,8 +189,8 @@ struct Operands {
     int n = 0;
     // `dense`: a weight, whose place is known to be aligned, so that the size
     // query knows whether it is copied; an activation's is not, and room for
-    // its copy is always there.
-    MlpOperand add(const void *p, long long ld, long long rows, int cols, bool dense) {
+    // its copy is always there.  Filled only where a launch of the call reads it.
+    MlpOperand add(const void *p, long long ld, long long rows, int cols, bool dense, bool read) {
         const bool sizes = k->base == nullptr;
         if (dense ? s->dtype == LSTM_BF16 && cols % 8 == 0 : !sizes && in_place(s, p, ld, cols)) {
             if (!dense) (void)k->operand(s, (size_t)rows, cols);
@@ -201,7 +201,7 @@ struct Operands {
             return o;
         }
         const MlpOperand o = k->operand(s, (size_t)rows, cols);
-        if (!sizes) copy[n++] = Copy{p, ld, rows, cols, o};
+        if (!sizes && read) copy[n++] = Copy{p, ld, rows, cols, o};
         return o;
     }
     hipError_t launch(hipStream_t st) const {
@@ -283,9 +283,10 @@ Forward forward_of(const lstm_gated_mlp_shape *s, const void *x, long long xs, c
     }
     f.ops.s = s;
     f.ops.k = &k;
-    const MlpOperand ox = f.ops.add(x, xs, s->rows, s->in, false);
-    const MlpOperand og = f.ops.add(wg, s->in, s->hidden, s->in, true), ou = f.ops.add(wu, s->in, s->hidden, s->in, true);
-    const MlpOperand od = f.ops.add(wd, s->hidden, s->out, s->hidden, true);
+    const MlpOperand ox = f.ops.add(x, xs, s->rows, s->in, false, true);
+    const MlpOperand og = f.ops.add(wg, s->in, s->hidden, s->in, true, true);
+    const MlpOperand ou = f.ops.add(wu, s->in, s->hidden, s->in, true, true);
+    const MlpOperand od = f.ops.add(wd, s->hidden, s->out, s->hidden, true, true);
     f.gate = mlp_call(s, MLP_GATE, 0, 0);
     f.gate.p[0] = product(ox, og, s->rows, s->hidden, s->in);
     f.gate.p[0].b[1] = ou;
@@ -308,6 +309,7 @@ Forward forward_of(const lstm_gated_mlp_shape *s, const void *x, long long xs, c
 struct Backward {
     Operands ops;
     MlpCall hidden, dx, dw;
+    bool want_hidden, want_dx;  // whether these are launched
     size_t bytes;
     bool ok;
 };
@@ -318,10 +320,13 @@ Backward backward_of(const lstm_gated_mlp_shape *s, const void *x, long long xs,
     Backward f{};
     f.ops.s = s;
     f.ops.k = &k;
-    const MlpOperand ox = f.ops.add(x, xs, s->rows, s->in, false);
-    const MlpOperand oy = f.ops.add(dy, ys, s->rows, s->out, false);
-    const MlpOperand og = f.ops.add(wg, s->in, s->hidden, s->in, true), ou = f.ops.add(wu, s->in, s->hidden, s->in, true);
-    const MlpOperand od = f.ops.add(wd, s->hidden, s->out, s->hidden, true);
+    f.want_hidden = s->rows && (dx || dwg || dwu);
+    f.want_dx = s->rows && dx;
+    const MlpOperand ox = f.ops.add(x, xs, s->rows, s->in, false, dwg || dwu);
+    const MlpOperand oy = f.ops.add(dy, ys, s->rows, s->out, false, true);
+    const MlpOperand og = f.ops.add(wg, s->in, s->hidden, s->in, true, f.want_dx);
+    const MlpOperand ou = f.ops.add(wu, s->in, s->hidden, s->in, true, f.want_dx);
+    const MlpOperand od = f.ops.add(wd, s->hidden, s->out, s->hidden, true, f.want_hidden);
     const Reserve r = reserve_of(s, reserve);
     f.hidden = mlp_call(s, MLP_DGATE, 0, 1);
     f.hidden.p[0] = product(oy, od, s->rows, s->hidden, s->out);
@@ -613,9 +618,9 @@ lstm_status lstm_gated_mlp_backward(const lstm_gated_mlp_shape *s, const void *x
     const Backward f = backward_of(s, x, x_stride, w_gate, w_up, w_down, reserve, dy, dy_stride, dx, dw_gate, dw_up,
                                    dw_down, workspace);
     if ((rc = launched(f.ops.launch(st))) != LSTM_OK) return rc;
-    if (s->rows && (dx || dw_gate || dw_up))
+    if (f.want_hidden)
         if ((rc = launched(launch_mlp(f.hidden, st))) != LSTM_OK) return rc;
-    if (s->rows && dx)
+    if (f.want_dx)
         if ((rc = launched(launch_mlp(f.dx, st))) != LSTM_OK) return rc;
     return f.dw.count ? launched(launch_mlp(f.dw, st)) : LSTM_OK;
 }

@@ -275,3 +275,43 @@ def test_mlp_infinities(rows, hidden):
     y = host(pkg.gated_mlp(*(dev(v, "bf16") for v in (x, wg, wu, wd))))
     want = np.where(np.arange(O) % 2, np.inf, -np.inf)
     assert np.array_equal(y[rows // 2], want) and np.isfinite(np.delete(y, rows // 2, 0)).all()
+
+
+@pytest.mark.parametrize("dtype,K", [("f32", 72), ("bf16", 71)])
+def test_mlp_copies_what_the_wanted_gradients_read(dtype, K):
+    """Operands go into the workspace (fp32, and bf16 rows that are no whole pieces) only for launches that read them:
+    bytes of the workspace that a call leaves as they were."""
+    import torch
+    from layer_lstm_forward_amd import block_ops as ops
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(4)
+    rows, F, O = 40, 520, 64
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    put = lambda *s: torch.randn(*s, generator=gen, device=DEV).to(dt)  # noqa: E731
+    x, wg, wu, wd, dy = put(rows, K), put(F, K), put(F, K), put(O, F), put(rows, O)
+    _, kept = pkg.gated_mlp_train(x, wg, wu, wd)
+    want = pkg.gated_mlp_backward(dy, x, wg, wu, wd, kept)
+    shape = ops._pack_mlp(1 if dtype == "bf16" else 0, 0, rows, K, F, O)
+    n = ops.lstm_gated_mlp_backward_workspace_size(shape)
+    planes, up = 1 if dtype == "bf16" else 3, lambda m: (m + 255) // 256 * 256
+    part = lambda r, c: planes * up(r * ((c + 7) // 8 * 8) * 2)  # noqa: E731
+    # the parts in their order: x, dy, gate and up weights, down weight (bf16: whole pieces here, no copy)
+    ends = np.cumsum([0, part(rows, K), part(rows, O), part(F, K), part(F, K), part(O, F) if planes == 3 else 0])
+    for wanted, reads in (((1, 0, 0, 0), (0, 1, 1, 1, 1)), ((0, 1, 0, 0), (1, 1, 0, 0, 1)),
+                          ((0, 0, 1, 0), (1, 1, 0, 0, 1)), ((0, 0, 0, 1), (0, 1, 0, 0, 0)),
+                          ((1, 1, 1, 1), (1, 1, 1, 1, 1))):
+        ws = torch.full((n,), 0x5A, dtype=torch.uint8, device=DEV)
+        out = [torch.full_like(t, float("nan")) if k else None for t, k in zip(want, wanted)]
+        rc = ops.lstm_gated_mlp_backward(shape, x.data_ptr(), K, wg.data_ptr(), wu.data_ptr(), wd.data_ptr(),
+                                         kept.data_ptr(), kept.numel(), dy.data_ptr(), O,
+                                         *(None if t is None else t.data_ptr() for t in out), ws.data_ptr(), n,
+                                         torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        for i in range(5):
+            if ends[i + 1] == ends[i] or (i == 1 and planes == 1):
+                continue
+            touched = bool((ws[ends[i]:ends[i + 1]] != 0x5A).any())
+            assert touched == bool(reads[i]), (wanted, i)
+        for a, b in zip(out, want):
+            assert a is None or torch.allclose(a.float(), b.float(), rtol=2 ** -6 if dtype == "bf16" else 1e-4,
+                                               atol=1e-2 if dtype == "bf16" else 1e-4)
