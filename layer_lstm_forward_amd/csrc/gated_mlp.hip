@@ -241,8 +241,7 @@ __device__ inline void finish(const MlpCall &c, const MlpProduct &p, Place at, i
 // that write 64 16-byte pieces to consecutive places, so the place decides
 // which piece a lane fetches.  Pieces are permuted inside a row such that the
 // lanes of a fragment read fall on all banks:
-//   rows of 64 values (128 bytes): piece p of row r lies at p ^ (r / 2 % 8), of
-//   32 values at p ^ (r / 4 % 4);
+//   rows (64 values, 128 bytes): piece p of row r lies at p ^ (r / 2 % 8);
 //   columns: 64-byte groups g of row k lie at g ^ (k % 4), with 128-byte rows
 //   (ROWS = 64) at g ^ (k / 2 % 2).
 template <int ROWS, int KS, bool COLS, bool DUAL>
@@ -250,17 +249,17 @@ struct Side {
     static constexpr int PER = ROWS * KS / 2048;         // loads of a wave for a stage
     static constexpr int RB = COLS ? ROWS * 2 : KS * 2;  // bytes of a row in LDS
     static constexpr int PP = RB / 16;                   // pieces of a row
-    static_assert(PER > 0 && (KS == 64 || KS == 32), "stage");
+    static_assert(PER > 0 && KS == 64, "stage");
     static __device__ int key_of(int row) {
         if (COLS) return ROWS == 64 ? (row >> 1) & 1 : row & 3;  // of 64-byte groups
-        return KS == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
+        return (row >> 1) & 7;
     }
     const char *seg[2];  // of this tile: first row (or column), k = 0
     long long ld2;       // bytes from row to row
     long long bytes[2];  // of the tile's part from seg on
     int K;
     unsigned off[PER];
-    int kpiece;          // first k of the lane's piece (rows)
+    int kpiece;          // first k of the lane's piece (rows): the same in all its loads, whose rows are 32 apart
 
     __device__ void init(int ld, int K_, int lane, int w) {
         K = K_;
