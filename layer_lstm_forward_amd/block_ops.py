@@ -308,6 +308,15 @@ def rotary_frequencies(rotary_dim, base=10000.0, factor=1.0, original_length=Non
     return torch.tensor(out, dtype=torch.float64, device=device)
 
 
+def _float32(value, what):
+    """A number as the ABI's float holds it, refused where it would become 0 or infinite there."""
+    value = float(value)
+    held = ctypes.c_float(value).value
+    if (held == 0.0 and value != 0.0) or (math.isinf(held) and not math.isinf(value)):
+        raise ValueError(f"{what} is outside the float32 range")
+    return value
+
+
 class _Rotary:
     """The checked arguments of a call, as the ABI takes them."""
 
@@ -350,7 +359,7 @@ class _Rotary:
             t, b = (0, s[0]) if len(lead) == 1 else (s[1], s[0]) if batch_first else s
             self.positions = _pack_positions(positions.data_ptr(), t, b)
         self.shape = _pack_rotary(code, T, B, H, G, D, 2 * frequencies.shape[0], int(bool(interleaved)),
-                                  int(bool(norm)), float(eps), float(scale))
+                                  int(bool(norm)), _float32(eps, "eps"), _float32(scale, "scale"))
 
 
 def rotary(q, k, frequencies, positions=None, q_weight=None, k_weight=None, norm=False, eps=1e-6, interleaved=False,
