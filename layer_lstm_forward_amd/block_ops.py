@@ -154,6 +154,13 @@ def lstm_gated_mlp_backward(shape, x, x_stride, w_gate, w_up, w_down, reserve, r
                                           dy_stride, dx, dw_gate, dw_up, dw_down, workspace, workspace_bytes, stream)
 
 
+def _output(t, like, what, shape):
+    """A tensor to write into: as _sequence, and no two of its elements in one place."""
+    _sequence(t, like, what, shape)
+    if any(n > 1 and s == 0 for n, s in zip(shape, t.stride())):
+        raise ValueError(f"{what} must not be an expanded tensor: it is written")
+
+
 # ---------------------------------------------------------- gated recurrence
 def _channels(t, batch_first):
     """The view of a [T, B, width] tensor."""
@@ -180,7 +187,7 @@ def gated_recurrence(x, forget, input_gate=None, state=None, lengths=None, batch
     x, forget, input_gate [T, B, width] ([B, T, width] with batch_first), any strides with a dense last axis (slices
     of one wide projection need no copy).  state: None or [B, width] float32, from an earlier call.
     lengths: None, B host ints in 0..T, or an int32 device tensor; tokens past a row's length are not read.
-    out: None or (y, state_out) to write into; state_out may be `state`.
+    out: None or (y, state_out) to write into; y must not share memory with an input, state_out may be `state`.
     Returns (y, state_out); y holds every h_t."""
     if torch is None:
         _need_torch()
@@ -199,7 +206,7 @@ def gated_recurrence(x, forget, input_gate=None, state=None, lengths=None, batch
                 on.give(y, last)
         else:
             y, last = out
-            _sequence(y, x, "y", x.shape)
+            _output(y, x, "y", x.shape)
             if last is not None:
                 _dense(last, x, "state_out", (B, width), torch.float32)
         nbytes = lstm_gated_recurrence_workspace_size(shape)
@@ -216,7 +223,7 @@ def gated_recurrence_backward(x, forget, y, dy, input_gate=None, state=None, dst
     """Gradients (dx, dforget, dinput_gate, dstate) of gated_recurrence() called with the same arguments.
 
     y: as that call returned it; dy: its gradient; dstate: gradient of the returned state, or None.  out: None or (dx,
-    dforget, dinput_gate) to write into.  dinput_gate and the last result, the gradient of `state`, are None where
+    dforget, dinput_gate) to write into, which must not share memory with an input.  dinput_gate and the last result, the gradient of `state`, are None where
     there was none."""
     if torch is None:
         _need_torch()
@@ -242,7 +249,7 @@ def gated_recurrence_backward(x, forget, y, dy, input_gate=None, state=None, dst
                 raise ValueError("dinput_gate must be given exactly where input_gate is")
             for t, what in ((dx, "dx"), (df, "dforget"), (di, "dinput_gate")):
                 if t is not None:
-                    _sequence(t, x, what, x.shape)
+                    _output(t, x, what, x.shape)
         dfirst = None if state is None else torch.empty_like(state)
         if on.other is not None:
             on.give(dfirst)
@@ -277,7 +284,7 @@ def gated_recurrence_step(x, forget, state, input_gate=None, slots=None, out=Non
             if on.other is not None:
                 on.give(out)
         else:
-            _sequence(out, x, "y", x.shape)
+            _output(out, x, "y", x.shape)
         view = lambda t: None if t is None else _pack_view(t.data_ptr(), 0, t.stride(0), 0)  # noqa: E731
         _check(lstm_gated_recurrence_step(_pack_recurrence(code, 1, B, width), view(x), view(forget),
                                           view(input_gate), _addr(slots), state.shape[0], state.data_ptr(), view(out),
@@ -372,7 +379,8 @@ def rotary(q, k, frequencies, positions=None, q_weight=None, k_weight=None, norm
     2 * len(frequencies) values of each head are turned, value j with value j + len(frequencies), or neighbours with
     interleaved=True.  positions: int32, of q's leading axes, any strides, or None (token t of a row stands at t).
     norm=True: x / sqrt(mean(x^2) + eps) * weight first, weights [dim] or None (ones).
-    scale: the turned values are multiplied by it.  out: None or (q, k) to write into, each of which may be its input."""
+    scale: the turned values are multiplied by it.  out: None or (q, k) to write into, each of which may be its input
+    itself and must not share memory with anything else."""
     if torch is None:
         _need_torch()
     a = _Rotary(q, k, frequencies, positions, q_weight, k_weight, norm, eps, interleaved, scale, batch_first)
@@ -384,9 +392,9 @@ def rotary(q, k, frequencies, positions=None, q_weight=None, k_weight=None, norm
                 on.give(qo, ko)
         else:
             qo, ko = out
-            _sequence(qo, q, "q of out", q.shape)
+            _output(qo, q, "q of out", q.shape)
             if k is not None:
-                _sequence(ko, q, "k of out", k.shape)
+                _output(ko, q, "k of out", k.shape)
         _check(lstm_rotary_forward(a.shape, a.view(q), a.view(k), _addr(q_weight), _addr(k_weight),
                                    frequencies.data_ptr(), a.positions, a.view(qo), a.view(ko), on.handle),
                "lstm_rotary_forward")
@@ -397,8 +405,8 @@ def rotary_backward(q, k, frequencies, dq_out, dk_out, positions=None, q_weight=
                     eps=1e-6, interleaved=False, scale=1.0, batch_first=False, out=None, stream=None):
     """Gradients (dq, dk, dq_weight, dk_weight) of rotary() called with the same arguments.
 
-    dq_out, dk_out: gradients of its results.  out: None or (dq, dk) to write into, which may be dq_out and dk_out.  The
-    weights' gradients are None without a norm; with norm=True they are given without weights too (the gradients of
+    dq_out, dk_out: gradients of its results.  out: None or (dq, dk) to write into, which may be dq_out and dk_out
+    themselves and must not share memory with anything else.  The weights' gradients are None without a norm; with norm=True they are given without weights too (the gradients of
     ones)."""
     if torch is None:
         _need_torch()
@@ -414,9 +422,9 @@ def rotary_backward(q, k, frequencies, dq_out, dk_out, positions=None, q_weight=
                 on.give(dq, dk)
         else:
             dq, dk = out
-            _sequence(dq, q, "dq", q.shape)
+            _output(dq, q, "dq", q.shape)
             if k is not None:
-                _sequence(dk, q, "dk", k.shape)
+                _output(dk, q, "dk", k.shape)
         dwq = dwk = None
         if norm:
             dwq = q.new_empty(q.shape[-1])
@@ -491,8 +499,10 @@ def gated_mlp(x, w_gate, w_up, w_down, activation="silu", stream=None):
     """The gated feed-forward block y = (act(x w_gate^T) * (x w_up^T)) w_down^T (lstm_gated_mlp_forward).
 
     x [..., in], w_gate and w_up [hidden, in], w_down [out, hidden]; activation "silu", "gelu" (its tanh form) or
-    "sigmoid".  Returns y [..., out].  The products are summed in 32 bits; bfloat16: the hidden values are rounded once
-    as an operand of the last product; float32: operands are split so that products keep 24 bits."""
+    "sigmoid".  Returns y [..., out].  Weights whose address is no multiple of 16 bytes are copied in every call, and so
+    is an x whose leading axes are not evenly spaced rows.  The products are summed in 32 bits; bfloat16: the hidden
+    values are rounded once as an operand of the last product; float32: operands are split so that products keep 24
+    bits."""
     return _mlp_forward(x, w_gate, w_up, w_down, activation, False, stream)[0]
 
 
