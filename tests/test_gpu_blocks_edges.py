@@ -315,3 +315,47 @@ def test_mlp_copies_what_the_wanted_gradients_read(dtype, K):
         for a, b in zip(out, want):
             assert a is None or torch.allclose(a.float(), b.float(), rtol=2 ** -6 if dtype == "bf16" else 1e-4,
                                                atol=1e-2 if dtype == "bf16" else 1e-4)
+
+
+# Ways of the recurrence (GrWay of csrc/blocks.h), as its rule chooses them.
+TILES, LANES, CHAIN = 0, 1, 2
+
+
+def way_of(T, B, W, dtype, backward):
+    plan = getattr(ctypes.CDLL(pkg.LIB_PATH), "_ZN8lstm_amd7gr_planEiiiib")
+    plan.argtypes, plan.restype = [ctypes.c_int] * 4 + [ctypes.c_bool], ctypes.c_int
+    return plan(T, B, W, 1 if dtype == "bf16" else 0, backward)
+
+
+@pytest.mark.parametrize("dtype,T,W,gates,tile", [("bf16", 34000, 9, 1, 512), ("bf16", 17000, 5, 2, 256),
+                                                  ("f32", 17000, 9, 1, 256), ("f32", 17000, 3, 2, 256)])
+def test_recurrence_chain_longer_than_the_look_back(dtype, T, W, gates, tile):
+    """Tiles look at the 32 before them: more than 64 of them, with gates that mostly remember, against fp64."""
+    assert way_of(T, 1, W, dtype, False) == way_of(T, 1, W, dtype, True) == CHAIN and T > 64 * tile
+    Rec(T, 1, W, dtype, gates, keep=9.0).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gates", [1, 2])
+def test_recurrence_rows_that_end_with_a_tile(gates, dtype):
+    """Tiles of 256 or 512 tokens: rows whose last token is a tile's, others' zeros behind it."""
+    assert way_of(1800, 6, 33, dtype, False) == way_of(1800, 6, 33, dtype, True) == CHAIN
+    Rec(1800, 6, 33, dtype, gates, lengths=[256, 512, 1024, 1536, 1800, 1]).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gates", [1, 2])
+def test_recurrence_lanes_over_many_tokens(gates, dtype):
+    """Threads that walk more than the tokens they have under way at first."""
+    T, B, W = 130, 44, 1000
+    assert way_of(T, B, W, dtype, False) == way_of(T, B, W, dtype, True) == LANES
+    Rec(T, B, W, dtype, gates, lengths=[T] + [(17 * b) % (T + 1) for b in range(1, B)]).check()
+
+
+@pytest.mark.parametrize("dtype,T,B,W,gates", [("f32", 333, 5, 1001, 2), ("bf16", 400, 4, 500, 1), ("f32", 400, 4, 500, 1),
+                                               ("bf16", 400, 4, 502, 2)])
+def test_recurrence_second_tile_of_a_workgroup(dtype, T, B, W, gates):
+    """Tiles one after the other in a workgroup: rows that end in the second, with the first, and before its end."""
+    assert way_of(T, B, W, dtype, False) == way_of(T, B, W, dtype, True) == TILES
+    Rec(T, B, W, dtype, gates, lengths=[T, 256, 300, 257, 0][:B]).check()
+    Rec(T, B, W, dtype, gates, batch_first=True, packed=True).check()
