@@ -114,7 +114,7 @@ __device__ inline float lanes_sum(float v) {
 // Workgroup (x, y): tokens from x on, the y-th run of c.run heads (queries
 // first).  NB blocks a lane.
 template <class DT, int P, int L, int NB, bool PAIRS, bool BACK>
-__global__ __launch_bounds__(256, BACK ? 2 : 4) void k_rot(RotCall c) {
+__global__ __launch_bounds__(256) void k_rot(RotCall c) {
     constexpr int GROUPS = 256 / L;
     __shared__ float sums[BACK ? GROUPS * L * NB * 2 * P : 1];
     const int lane = threadIdx.x % L, group = threadIdx.x / L;
