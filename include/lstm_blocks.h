@@ -151,7 +151,7 @@ lstm_status lstm_rotary_backward(const lstm_rotary_shape *shape, const lstm_view
  * kept with 16).  LSTM_F32: every operand is split into three bf16 terms, whose
  * six largest products are summed (2^-24 of each operand; values below 2^-100
  * keep fewer bits); a value that is not finite spoils the outputs it reaches,
- * as NaN.  Up to 64 rows are multiplied in fp32 itself. */
+ * as NaN.  Up to 64 rows of a forward call are multiplied in fp32 itself. */
 typedef enum {
     LSTM_ACT_SILU = 0,    /* g s(g) */
     LSTM_ACT_GELU = 1,    /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */

@@ -118,7 +118,7 @@ struct MlpPlan {
 };
 MlpPlan mlp_plan(const MlpCall &c);
 hipError_t launch_mlp(const MlpCall &c, hipStream_t s);
-// The products of the forward call for up to MLP_FEW rows, from the matrices as
+// The products of the forward call for few rows, MLP_FEW at most, from the matrices as
 // they are: w[0] and w[1] gate and up, out receives h [rows][ld] of the call's
 // dtype, zeros past N; or w[0] alone, out receives [rows][N].
 constexpr int MLP_FEW = 64;

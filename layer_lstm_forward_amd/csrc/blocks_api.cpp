@@ -250,6 +250,21 @@ MlpCall mlp_call(const lstm_gated_mlp_shape *s, int epilogue, int a_cols, int b_
 
 size_t most(size_t a, size_t b) { return a > b ? a : b; }
 
+// Forward calls of few rows go to the kernel that reads the weights as they are; its time grows with the rows, that of
+// the tiles hardly.  Whole calls, in x hidden, us in this kernel / in tiles:
+//     rows                 16           32           48           64
+//     bf16  1024 x 2816    18 / 24      18 / 24      21 / 25      24 / 25
+//           1536 x 4224    23 / 27      30 / 28      36 / 28      41 / 29
+//           2048 x 2816    18 / 26      22 / 26      27 / 27      30 / 28
+//           2048 x 5632    28 / 32      37 / 32      47 / 33      53 / 33
+//     fp32  1024 x 2816    24 / 60      35 / 61      47 / 61      52 / 62
+//           2048 x 5632    52 / 141     80 / 144    120 / 146    130 / 148
+// (of 17 and of 33 rows as of the next 16).
+bool few_rows(const lstm_gated_mlp_shape *s) {
+    if (s->dtype == LSTM_F32 || s->rows <= 16) return s->rows <= MLP_FEW;
+    return s->rows <= MLP_FEW && (long long)s->rows * (s->hidden + s->out) <= 240 * 1024;
+}
+
 // The launches of a forward call and its workspace.
 struct Forward {
     bool few;
@@ -263,7 +278,7 @@ Forward forward_of(const lstm_gated_mlp_shape *s, const void *x, long long xs, c
                    const void *wd, void *y, void *reserve, void *workspace) {
     Carver k{static_cast<char *>(workspace)};
     Forward f{};
-    f.few = s->rows <= MLP_FEW;
+    f.few = few_rows(s);
     const Reserve r = reserve_of(s, reserve);
     if (f.few) {
         const long long ld = padded(s->hidden);

@@ -3,8 +3,8 @@
 //     GATE   g = x Wg^T, u = x Wu^T, h = act(g) u
 //     STORE  y = h Wd^T;  dx = dg Wg + du Wu;  dWg = dg^T x, dWu = du^T x, dWd = dy^T h
 //     DGATE  dh = dy Wd, dg = dh u act'(g), du = dh act(g)
-// One kernel body, k_mlp, runs all of them on v_mfma_f32_32x32x16_bf16; up to 64
-// rows of a forward call go to k_mlp_few, which is bound by the weights' traffic.
+// One kernel body, k_mlp, runs all of them on v_mfma_f32_32x32x16_bf16; few rows
+// of a forward call go to k_mlp_few, which is bound by the weights' traffic.
 //
 // An fp32 matrix is three bf16 ones (its value rounded, the rest rounded, the
 // rest), and its product the six largest of the nine between them, one after the

@@ -9,7 +9,7 @@ import pytest
 
 import layer_lstm_forward_amd as pkg
 from oracle import blocks as ref
-from tests.test_gpu_blocks import Rec
+from tests.test_gpu_blocks import Rec, _mlp_check
 from tests.test_gpu_ops import DEV, U16, U32, close, dev, draw, host
 
 pytestmark = pytest.mark.gpu
@@ -359,3 +359,17 @@ def test_recurrence_second_tile_of_a_workgroup(dtype, T, B, W, gates):
     assert way_of(T, B, W, dtype, False) == way_of(T, B, W, dtype, True) == TILES
     Rec(T, B, W, dtype, gates, lengths=[T, 256, 300, 257, 0][:B]).check()
     Rec(T, B, W, dtype, gates, batch_first=True, packed=True).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [16, 17, 29, 30, 64, 65])
+def test_mlp_few_rows_of_a_wide_layer(rows, dtype):
+    """Both sides of the rule for few rows: by their number, and by their number times the layer's width."""
+    import torch
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(rows)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    put = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device=DEV) * std).to(dt)  # noqa: E731
+    K, F, O = 133, 8203, 130  # bf16: 29 rows are few, 30 are not
+    _mlp_check(put(rows, K), put(F, K, std=K ** -0.5), put(F, K, std=K ** -0.5), put(O, F, std=F ** -0.5),
+               put(rows, O), dtype)
