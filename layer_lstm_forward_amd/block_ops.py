@@ -428,7 +428,8 @@ def rotary_backward(q, k, frequencies, dq_out, dk_out, positions=None, q_weight=
         dwq = dwk = None
         if norm:
             dwq = q.new_empty(q.shape[-1])
-            dwk = None if k is None else q.new_empty(q.shape[-1])
+            if k is not None:  # (keys of no heads are not read, and sum up to nothing)
+                dwk = q.new_empty(q.shape[-1]) if k.shape[-2] else q.new_zeros(q.shape[-1])
             if on.other is not None:
                 on.give(dwq, dwk)
         nbytes = lstm_rotary_backward_workspace_size(a.shape)

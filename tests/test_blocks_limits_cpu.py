@@ -42,3 +42,14 @@ def test_expanded_outputs(kernels):  # noqa: F811
     one = put(1, 2, 8).expand(1, 2, 8)  # (an axis of one has any stride)
     pkg.gated_recurrence(one, one, out=(one.as_strided((1, 2, 8), (0, 8, 1)), S))
     pkg.rotary(wide, flat[..., None, :], f, out=(q, put(5, 2, 1, 8)))  # inputs may repeat
+
+
+def test_keys_of_no_heads(kernels, monkeypatch):  # noqa: F811
+    """The gradient of a weight that nothing reads is 0, not what its memory held."""
+    import torch
+    q = put(5, 2, 4, 8)
+    f, w = torch.zeros(4, dtype=torch.float64).as_subclass(type(q)), put(8)
+    monkeypatch.setattr(type(q), "new_empty", lambda t, *a: torch.full(a[0] if isinstance(a[0], tuple) else a, 7.0,
+                                                                       dtype=t.dtype).as_subclass(type(q)))
+    dwk = pkg.rotary_backward(q, q[:, :, :0], f, q, q[:, :, :0], q_weight=w, k_weight=w, norm=True)[3]
+    assert not dwk.any()

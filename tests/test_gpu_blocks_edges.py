@@ -373,3 +373,20 @@ def test_mlp_few_rows_of_a_wide_layer(rows, dtype):
     K, F, O = 133, 8203, 130  # bf16: 29 rows are few, 30 are not
     _mlp_check(put(rows, K), put(F, K, std=K ** -0.5), put(F, K, std=K ** -0.5), put(O, F, std=F ** -0.5),
                put(rows, O), dtype)
+
+
+# -------------------------------------------------------------------- rotary
+def test_rotary_keys_of_no_heads():
+    """Keys without heads are as no keys; their weight's gradient is 0."""
+    import torch
+    q, w = torch.randn(5, 2, 3, 16, device=DEV), torch.randn(16, device=DEV)
+    k, freq = q[:, :, :0], pkg.rotary_frequencies(16, device=DEV)
+    # memory that was used before
+    torch.full((1 << 20,), float("nan"), device=DEV)
+    more = dict(q_weight=w, k_weight=w, norm=True)
+    want, _ = pkg.rotary(q, None, freq, q_weight=w, norm=True)
+    got, none = pkg.rotary(q, k, freq, **more)
+    assert torch.equal(got, want) and none.shape == k.shape
+    back = pkg.rotary_backward(q, None, freq, q, None, q_weight=w, norm=True)
+    dq, dk, dwq, dwk = pkg.rotary_backward(q, k, freq, q, k, **more)
+    assert torch.equal(dq, back[0]) and torch.equal(dwq, back[2]) and dk.shape == k.shape and not dwk.any()
