@@ -46,11 +46,11 @@ template <bool SLOPE>
 __device__ inline void activate(int kind, const float *g, float *a, float *slope) {
     if (kind == LSTM_ACT_GELU) {
         // g s(2t), t = k (g + c g^3); past |g| = 32 s is 0 or 1 in fp32, and
-        // the clamp keeps 0 times infinity out of the slope
+        // the clamp, which NaN passes, keeps 0 times infinity out of the slope
         constexpr float k = 0.7978845608028654f, c = 0.044715f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float q = fminf(fmaxf(g[i], -32.0f), 32.0f), q2 = q * q;
+            const float q = g[i] > 32.0f ? 32.0f : g[i] < -32.0f ? -32.0f : g[i], q2 = q * q;
             const float t = 2.0f * k * q * (1.0f + c * q2), p = sigmoid_f(t);
             a[i] = g[i] * p;
             if (SLOPE) slope[i] = p + q * (p * sigmoid_f(-t)) * (2.0f * k * (1.0f + 3.0f * c * q2));

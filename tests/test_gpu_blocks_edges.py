@@ -375,6 +375,25 @@ def test_mlp_few_rows_of_a_wide_layer(rows, dtype):
                put(rows, O), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["silu", "gelu", "sigmoid"])
+@pytest.mark.parametrize("rows", [9, 90])
+def test_mlp_a_gate_that_is_not_a_number(rows, kind, dtype):
+    """NaN in the gate's weights of one hidden unit alone is in the gradients that its slope and its value reach."""
+    rng = np.random.default_rng(11)
+    K, F, O = 24, 40, 16
+    x, dy = draw(rng, (rows, K), dtype), draw(rng, (rows, O), dtype)
+    wg, wu, wd = draw(rng, (F, K), dtype), draw(rng, (F, K), dtype), draw(rng, (O, F), dtype)
+    wg[7, 3] = np.nan
+    t = [dev(v, dtype) for v in (x, wg, wu, wd)]
+    y, kept = pkg.gated_mlp_train(*t, activation=kind)
+    dx, dg, du, dd = (host(v) for v in pkg.gated_mlp_backward(dev(dy, dtype), *t, kept, activation=kind))
+    assert np.isnan(host(y)).all() and np.isnan(dx).all()
+    for got in (dg, du, dd.T):
+        hit = np.isnan(got).all(1)
+        assert hit[7] and not np.isnan(np.delete(got, 7, 0)).any()
+
+
 # -------------------------------------------------------------------- rotary
 def test_rotary_keys_of_no_heads():
     """Keys without heads are as no keys; their weight's gradient is 0."""
