@@ -7,22 +7,23 @@
 // of a forward call go to k_mlp_few, which is bound by the weights' traffic.
 //
 // An fp32 matrix is three bf16 ones (its value rounded, the rest rounded, the
-// rest), and its product the six largest of the nine between them, one after the
-// other in the same sums: 128 TFLOP/s of fp32 products in a training step of
-// 8191 x 512 x 1408, against 76 of the library's fp32 products there and 153 on
-// large matrices; the fp32 matrix instructions end at 157.
+// rest), and its product the six largest of the nine between them (the published
+// way to fp32 products on bf16 matrix cores), one after the other in the same sums:
+// 121 to 128 TFLOP/s of fp32 products in a training step of 8191 x 512 x 1408,
+// against 76 of the library's fp32 products there and 153 on large matrices; the
+// fp32 matrix instructions end at 157.
 //
 // k_mlp is bound by the matrix cores and their power: with every load, LDS read
 // and store taken out it gives 1410 to 1495 TFLOP/s on random values (the clock
-// falls to 1.5 GHz), whole 1120 to 1190 for y, dx and the weights' gradients at
-// 16384 x 2048 x 5632 (the library 870 to 1190 for the same products).  There the
-// matrix cores are busy half of the time, and the waits for loads and barriers
-// take a fifth.  Measured on the same sizes: 128 x 128 tiles, two workgroups a
+// falls to 1.5 GHz), whole 1020 to 1040 for y, 1090 to 1170 for dx and 1130 to 1200
+// for the weights' gradients at 16384 x 2048 x 5632, by card (the library 870 to 1190
+// for the same products).  There the matrix cores are busy half of the time, and
+// the waits for loads and barriers take a fifth.  Measured on the same sizes: 128 x 128 tiles, two workgroups a
 // CU, 950 to 970; 256 x 128 in stages of 32, two workgroups a CU, 900 to 990;
 // 256 x 256 in four stages of 32, 1020 to 1080; lines fetched into the L2 a
 // stage ahead of their loads, 1030 to 1050.  GATE and DGATE lose to what they
-// read and write with all CUs at once: 800 TFLOP/s with g and u kept, 1050
-// without; 680 (each workgroup's results wait for nothing but are not hidden
+// read and write with all CUs at once: 860 to 910 TFLOP/s with g and u kept, 1050
+// without; 620 to 650 (each workgroup's results wait for nothing but are not hidden
 // behind another's products; starting the XCDs apart did not help).
 #include <type_traits>
 
@@ -677,7 +678,7 @@ __global__ __launch_bounds__(256) void k_mlp_join(MlpCall c) {
 
 // ------------------------------------------------------------------ few rows
 // Up to 16 NT rows x: the weights' traffic is all that counts (4 x 1024 x 2816
-// bf16: 5.1 + 7.0 us for 17 MB, against 22 in four launches of 64-row tiles).  A workgroup
+// bf16: 5.4 + 7.2 us for 17 MB; the rule, few_rows, has both sides' times).  A workgroup
 // takes 16 rows of a weight (GATE: of gate and of up), its NW waves every NW-th
 // 128 bytes of k.  Weights go from memory to registers as fragments (lane (m, g):
 // row m, 16 bytes at 16 g of each 64), several on their way at a time, and meet

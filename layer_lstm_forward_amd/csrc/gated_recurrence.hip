@@ -6,20 +6,22 @@
 // Three ways, chosen by an estimate of their times (gr_plan):
 // k_gr_lanes: a thread walks the tokens of four neighbouring channels of a batch
 // row, the next tokens' values under way meanwhile.  Bound by memory: 512 x 256 x
-// 2048 bf16 304 us forward, 597 backward (5.3 and 5.4 TB/s, as a copy).
+// 2048 bf16 316 us forward, 600 backward (5.1 and 5.4 TB/s, as a copy), 512 x 128 x
+// 2048 fp32 297 and 622.
 // k_gr_tile, for little work: a workgroup spreads a tile of tokens of 32 channels
 // over its threads, composes their maps (carry -> A carry + B, A the product of
 // the a), scans them and walks the tokens again from the carries that this
 // gives: one launch, and memory is read once, but the steps of a tile wait for
-// each other (333 x 5 x 1001 fp32 with an input gate: 12 + 18 us; 512 x 256 x
-// 2048 bf16 570 + 946).
+// each other (333 x 5 x 1001 fp32 with an input gate: 13 + 20 us; 512 x 256 x
+// 2048 bf16 730 + 1015).
 // k_gr_tile in a chain, where channels are too few and tokens many: a workgroup a
 // tile, which hands its map on, finds the carry that it begins with from the
-// maps of the tiles before it, and hands on the carry that it ends with.  One
-// read of everything, and the results' bits do not depend on which tile is when
-// (16384 x 1 x 2048 bf16 65 us forward, 128 backward, the memory's time 38 and 75;
-// a launch for the maps of segments, one to join and one to walk them read it
-// twice: 70 and 113; fp32 112 and 180 against 122 and 319).
+// maps of the tiles before it, and hands on the carry that it ends with (a scan with
+// look-back, as published for prefix sums in one pass).  One read of everything, and
+// the results' bits do not depend on which tile is when (16384 x 1 x 2048 bf16 62 us
+// forward, 127 backward, the memory's time 38 and 75; fp32 109 and 178; a launch for
+// the maps of segments, one to join and one to walk them read it twice, and took 70
+// and 113, fp32 122 and 319, when a gate cost fewer instructions).
 #include <type_traits>
 
 #include "blocks.h"
@@ -232,8 +234,8 @@ struct GrTile {
 // bf16 309 us with 8 tokens a thread, 223 with 16, of 16 threads a channel; three
 // workgroups a CU instead of two, whose registers spill, 313).  32 threads a channel
 // halve the carry's way past the tiles (131072 x 1 x 256 bf16 100 -> 70 us, backward
-// 238 -> 131), and cost what is bound by memory up to a tenth (65536 x 1 x 2048
-// backward 423 -> 463).
+// 238 -> 132), and cost what is bound by memory up to a tenth (65536 x 1 x 2048
+// backward 423 -> 465, forward 231 now).
 constexpr int kChainLanes = 16, kChainRuns = 32, kChainRun = 8;
 template <class DT, bool INPUT, bool BACK>
 using GrChain = GrTile<kChainLanes, kChainRuns, std::is_same_v<DT, BF16> && !INPUT && !BACK ? 16 : kChainRun, true>;
@@ -677,7 +679,8 @@ size_t gr_words(int T, int B, int width) {
     return 256 + ((size_t)GR_KINDS * chain_tiles(T, kChainRun) * B * width * 8 + 255) / 256 * 256;
 }
 
-// The way with the least estimated time.
+// The way with the least estimated time, by the bytes without an input gate (the
+// workspace query does not know of one).
 GrWay gr_plan(int T, int B, int width, int dtype, bool backward) {
     const int V = piece(width);
     const double lanes = (double)B * ((width + V - 1) / V);

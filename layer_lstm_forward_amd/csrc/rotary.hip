@@ -2,8 +2,8 @@
 // forward and backward.
 //     r = 1 / sqrt(mean x^2 + eps), u = x r w, each pair (u_a, u_b) turned by p f_j
 //     g = the output's gradient turned back, dx = r (g w - x r mean(g w x r)), dw = sum of g x r
-// Bound by memory: 131072 tokens of 24 heads of 128 bf16 309 us forward, 497
-// backward, 6 to join the weights' sums (5.2 and 4.9 TB/s).  A head's row lies over L lanes of a wave, each with two
+// Bound by memory: 131072 tokens of 24 heads of 128 bf16 313 us forward, 501
+// backward, 6 to join the weights' sums (5.2 and 4.8 TB/s).  A head's row lies over L lanes of a wave, each with two
 // pieces of P values: the two halves of P pairs, so that a rotation needs no
 // other lane's values.  A lane keeps its pairs' sines and cosines for all heads
 // of a token that it takes.
