@@ -223,8 +223,8 @@ def gated_recurrence_backward(x, forget, y, dy, input_gate=None, state=None, dst
     """Gradients (dx, dforget, dinput_gate, dstate) of gated_recurrence() called with the same arguments.
 
     y: as that call returned it; dy: its gradient; dstate: gradient of the returned state, or None.  out: None or (dx,
-    dforget, dinput_gate) to write into, which must not share memory with an input.  dinput_gate and the last result, the gradient of `state`, are None where
-    there was none."""
+    dforget, dinput_gate) to write into, which must not share memory with an input.  dinput_gate and the last result,
+    the gradient of `state`, are None where there was none."""
     if torch is None:
         _need_torch()
     code = _recurrence_args(x, forget, input_gate, state, 2, "[T, B, width] ([B, T, width] with batch_first)")
@@ -406,8 +406,8 @@ def rotary_backward(q, k, frequencies, dq_out, dk_out, positions=None, q_weight=
     """Gradients (dq, dk, dq_weight, dk_weight) of rotary() called with the same arguments.
 
     dq_out, dk_out: gradients of its results.  out: None or (dq, dk) to write into, which may be dq_out and dk_out
-    themselves and must not share memory with anything else.  The weights' gradients are None without a norm; with norm=True they are given without weights too (the gradients of
-    ones)."""
+    themselves and must not share memory with anything else.  The weights' gradients are None without a norm; with
+    norm=True they are given without weights too (the gradients of ones)."""
     if torch is None:
         _need_torch()
     a = _Rotary(q, k, frequencies, positions, q_weight, k_weight, norm, eps, interleaved, scale, batch_first)

@@ -18,8 +18,8 @@
 // falls to 1.5 GHz), whole 1020 to 1040 for y, 1090 to 1170 for dx and 1130 to 1200
 // for the weights' gradients at 16384 x 2048 x 5632, by card (the library 870 to 1190
 // for the same products).  There the matrix cores are busy half of the time, and
-// the waits for loads and barriers take a fifth.  Measured on the same sizes: 128 x 128 tiles, two workgroups a
-// CU, 950 to 970; 256 x 128 in stages of 32, two workgroups a CU, 900 to 990;
+// the waits for loads and barriers take a fifth.  Measured on the same sizes:
+// 128 x 128 tiles, two workgroups a CU, 950 to 970; 256 x 128 in stages of 32, two workgroups a CU, 900 to 990;
 // 256 x 256 in four stages of 32, 1020 to 1080; lines fetched into the L2 a
 // stage ahead of their loads, 1030 to 1050.  GATE and DGATE lose to what they
 // read and write with all CUs at once: 860 to 910 TFLOP/s with g and u kept, 1050

@@ -106,8 +106,8 @@ struct Gate {
     }
     // s(f) A of a map's factor, 0 < A <= 1.
     __device__ float keep_factor(float A) const { return fmaf(share(), A, f > 0.0f ? A : kLeast); }
-    // Factors do not become 0, so that an infinite carry stays infinite however many gates lie between; 2^-149 of any
-    // finite one is nothing.
+    // Factors do not become 0, so that an infinite carry stays infinite however many gates lie between (2^-149 of a
+    // finite one is 5e-7 at most).
     static constexpr float kLeast = 1.4e-45f;
 };
 
